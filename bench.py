@@ -36,7 +36,7 @@ TRAFFIC_JSON = os.path.join(ROOT, "profiles", "traffic_serving_batch.json")
 KERNEL_SPAN = "k_prep_docs..k_giant_copy"
 LAUNCHES_PER_CALL = 9
 KERNEL_SRC = [os.path.join(ROOT, "byte_level_bpe_pretokenize_gb300", "csrc", f)
-              for f in ("bpe_kernels.cu", "tiles.cuh", "memo.cuh", "decode.cuh", "train.cuh", "class_table.inc")]
+              for f in ("bpe_kernels.cu", "handle.cuh", "tiles.cuh", "memo.cuh", "decode.cuh", "train.cuh", "class_table.inc")]
 
 
 def kernel_hash() -> str:

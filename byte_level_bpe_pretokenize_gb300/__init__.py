@@ -25,7 +25,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libbpe_gb300.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-cudart", "shared"]
+              "-Xcompiler", "-fPIC", "-cudart", "shared"]
 
 BPE_OK = 0
 ERRORS = {1: "INVALID_ARG", 2: "CAPACITY", 3: "CUDA", 4: "BAD_TABLE", 5: "TIMEOUT", 6: "INTERNAL", 7: "BAD_INPUT"}
@@ -37,8 +37,11 @@ class BpeError(RuntimeError):
         self.code = code
 
 
+UNITS = ("bpe_kernels.cu",)  # translation units, compiled in parallel
+
+
 def _sources():
-    return [os.path.join(_CSRC, f) for f in ("bpe_kernels.cu", "tiles.cuh", "class_table.inc")] + \
+    return [os.path.join(_CSRC, f) for f in sorted(os.listdir(_CSRC)) if f.endswith((".cu", ".cuh", ".inc"))] + \
         [os.path.join(_ROOT, "include", "bpe_gb300.h")]
 
 
@@ -49,7 +52,16 @@ def build(force: bool = False, nvcc: str = "nvcc") -> str:
         return LIB_PATH
     os.makedirs(_BUILD, exist_ok=True)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    subprocess.check_call([nvcc, *NVCC_FLAGS, "-o", tmp, os.path.join(_CSRC, "bpe_kernels.cu")])
+    objects = [f"{tmp}.{u}.o" for u in UNITS]
+    runs = [subprocess.Popen([nvcc, *NVCC_FLAGS, "-c", "-o", o, os.path.join(_CSRC, u)])
+            for u, o in zip(UNITS, objects)]
+    codes = [r.wait() for r in runs]
+    for r, code in zip(runs, codes):
+        if code:
+            raise subprocess.CalledProcessError(code, r.args)
+    subprocess.check_call([nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objects])
+    for o in objects:
+        os.remove(o)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

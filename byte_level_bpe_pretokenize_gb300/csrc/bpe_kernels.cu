@@ -62,7 +62,9 @@
 #include <unordered_set>
 #include <vector>
 
-#include "../../include/bpe_gb300.h"
+#include "handle.cuh"
+
+using namespace bpe_impl;
 
 #define BPE_CLASS_TABLE_STORAGE static __device__ const
 #include "class_table.inc"
@@ -84,12 +86,6 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint32_t kEmptySlot = 0xFFFFFFFFu;  // left id of an unused pair-table slot
 
 static_assert(kShortMax <= 64 && kCacheMaxLen <= 16, "group merges hold 2 symbols per lane");
-
-// device status bits
-constexpr uint32_t kStBadInput = 1u;
-constexpr uint32_t kStTimeout = 2u;
-constexpr uint32_t kStInternal = 4u;
-constexpr uint32_t kStCapacity = 8u;
 
 enum Cls { kO = 0, kL = 1, kN = 2, kS = 3 };
 
@@ -129,18 +125,6 @@ struct Cache {
   uint32_t mask;  // slots - 1
   int enabled;
 };
-
-struct DevSmall {
-  uint32_t status;
-  uint32_t pad;
-  int64_t total;                     // ids of the call
-  unsigned long long tile_ctr;       // tiles taken by k_tiles' warps
-  unsigned long long n_misses;       // cache misses handed to k_misses
-  unsigned long long n_giants;       // pre-tokens deferred to k_giants
-  unsigned long long giant_ctr;      // deferred pre-tokens taken by k_giants' CTAs
-  unsigned long long n_ranges;       // long runs of tiles for k_prep_long
-};
-
 
 // ------------------------------------------------------------ small helpers --
 
@@ -1040,91 +1024,14 @@ __global__ void k_total_to_host(const DevSmall* small, int64_t* h_dst) {
 
 // ------------------------------------------------------------------- host --
 
-thread_local std::string g_err;
-
-int fail(int code, const std::string& msg) {
-  g_err = msg;
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(BPE_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
-#define CK(call)                                        \
-  do {                                                  \
-    cudaError_t e_ = (call);                            \
-    if (e_ != cudaSuccess) return cuda_fail(e_, #call); \
-  } while (0)
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    cudaGetDevice(&prev);
-    if (prev != dev) cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (prev >= 0 && cur != prev) cudaSetDevice(prev);
-  }
-};
-
 }  // namespace
 
-struct bpe_handle {
-  int device = 0;
-  int n_sms = 1;  // multiprocessors of the device (grids of persistent kernels)
-  int64_t n_merges = 0, n_vocab = 0;
-  int monotone = 1;  // every merge's operands are made by lower ranks (bpe_merges_monotone)
-  uint4* d_ht = nullptr;
-  uint32_t hmask = 0;
-  int32_t* d_mrows = nullptr;
-  int32_t* d_byte_id = nullptr;
-  uint8_t* d_vbytes = nullptr;
-  int64_t* d_voffs = nullptr;
-  uint4* d_vent = nullptr;  // per token: its first 12 bytes and its length (decoding)
-  uint4* d_cache = nullptr;
-  uint32_t cache_mask = 0;
-  int64_t cache_entries = 0;
-  int cache_enabled = 1;
-  int call_memo = BPE_MEMO_AUTO;  // bpe_set_call_memo
-  DevSmall* d_small = nullptr;
-  DevSmall* h_small = nullptr;  // pinned
-  void* d_ws = nullptr;
-  size_t ws_bytes = 0;
-  bool smem_set = false;
-  cudaEvent_t ev_start = nullptr, ev_stop = nullptr;
-  cudaEvent_t* ev_phase = nullptr;  // BPE_ENCODE_LAUNCHES + 1 caller-owned events, or null
-  // bpe_encode_batch_host: kHostSlots slots of device buffers, copy streams,
-  // events
-  static constexpr int kHostSlots = 4;
-  struct HostSlot {
-    uint8_t* bytes = nullptr;
-    int64_t* offs = nullptr;
-    int32_t* ids = nullptr;
-    int64_t* out_offs = nullptr;
-    cudaEvent_t in = nullptr, done = nullptr, free = nullptr;
-  } slot[kHostSlots];
-  int64_t slot_bytes = 0, slot_docs = 0;  // capacity of each slot
-  cudaStream_t s_h2d = nullptr, s_d2h = nullptr;
-  int64_t* h_totals = nullptr;  // pinned, one per slice
-  int64_t* d_totals = nullptr;  // the same memory as the device addresses it
-  int64_t h_totals_cap = 0;
-};
+std::string& bpe_impl::last_error() {
+  static thread_local std::string message;
+  return message;
+}
 
 namespace {
-
-int ensure_ws(bpe_handle* h, size_t need) {
-  if (need <= h->ws_bytes) return BPE_OK;
-  size_t sz = need + need / 4 + 4096;
-  if (h->d_ws) CK(cudaFree(h->d_ws));
-  h->d_ws = nullptr;
-  h->ws_bytes = 0;
-  CK(cudaMalloc(&h->d_ws, sz));
-  h->ws_bytes = sz;
-  return BPE_OK;
-}
 
 int read_status(bpe_handle* h, cudaStream_t st, DevSmall* out) {
   CK(cudaMemcpyAsync(h->h_small, h->d_small, sizeof(DevSmall), cudaMemcpyDeviceToHost, st));
@@ -1135,7 +1042,8 @@ int read_status(bpe_handle* h, cudaStream_t st, DevSmall* out) {
 }
 
 int status_code(uint32_t s) {
-  if (s & kStBadInput) return fail(BPE_ERR_BAD_INPUT, "offsets not monotone or outside the buffer, or an id out of range");
+  if (s & kStBadInput)
+    return fail(BPE_ERR_BAD_INPUT, "offsets not monotone or outside the buffer, or an id or length out of range");
   if (s & kStTimeout) return fail(BPE_ERR_TIMEOUT, "a device-side wait gave up");
   if (s & kStCapacity) return fail(BPE_ERR_CAPACITY, "output capacity exceeded");
   if (s & kStInternal) return fail(BPE_ERR_INTERNAL, "device-side consistency check failed");
@@ -1239,7 +1147,6 @@ int build_word_cache(bpe_handle* h, const uint8_t* vocab_bytes, const int64_t* v
 // records; the long runs of k_prep_docs; the pool of the deferred pieces (an
 // int32 per input byte).
 namespace {
-constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct WsSizes {
   size_t first_doc, rec, first_start, tile_base, block_sum, stage, misses, giants, ranges, pool, memo, follow, total;
@@ -1457,7 +1364,7 @@ int launch_encode(bpe_handle* h, const Ws& w, const uint8_t* d_bytes, int64_t n_
 
 extern "C" {
 
-const char* bpe_last_error(void) { return g_err.c_str(); }
+const char* bpe_last_error(void) { return last_error().c_str(); }
 
 int bpe_build(const int32_t* merges, int64_t n_merges, const uint8_t* vocab_bytes, const int64_t* vocab_offsets,
               int64_t n_vocab, int device, bpe_handle** out) {
@@ -1673,7 +1580,8 @@ int bpe_sync_status(bpe_handle* h, bpe_stream_t stream) {
   DevSmall s;
   int rc = read_status(h, (cudaStream_t)stream, &s);
   if (rc) return rc;
-  return status_code(s.status);
+  if (s.op_status) CK(cudaMemsetAsync(&h->d_small->op_status, 0, sizeof(uint32_t), (cudaStream_t)stream));
+  return status_code(s.status | s.op_status);
 }
 
 int bpe_encode_batch(bpe_handle* h, const uint8_t* d_bytes, int64_t n_bytes, const int64_t* d_doc_offsets,
