@@ -37,7 +37,7 @@ class BpeError(RuntimeError):
         self.code = code
 
 
-UNITS = ("bpe_kernels.cu",)  # translation units, compiled in parallel
+UNITS = ("bpe_kernels.cu", "model_ops.cu")  # translation units, compiled in parallel
 
 
 def _sources():
@@ -71,7 +71,7 @@ _lib = None
 
 EXPORTS = ["bpe_build", "bpe_encode_batch", "bpe_encode_batch_host", "bpe_encode_batch_noalloc", "bpe_pretokenize_batch", "bpe_decode_batch", "bpe_set_word_cache",
            "bpe_set_timing_events", "bpe_set_phase_events", "bpe_set_call_memo", "bpe_sync_status", "bpe_table_info", "bpe_table_monotone", "bpe_merges_monotone",
-           "bpe_workspace_bytes", "bpe_train", "bpe_destroy", "bpe_last_error"]
+           "bpe_workspace_bytes", "bpe_train", "bpe_embed", "bpe_embed_grad", "bpe_destroy", "bpe_last_error"]
 
 
 def lib():
@@ -114,13 +114,17 @@ def lib():
             L.bpe_merges_monotone.argtypes = [p, i64, i64, ctypes.POINTER(ctypes.c_int)]
             L.bpe_train.restype = ctypes.c_int
             L.bpe_train.argtypes = [p, p, p, i64, i64, ctypes.c_int, p, ctypes.POINTER(i64)]
+            i, f = ctypes.c_int, ctypes.c_float
+            L.bpe_embed.restype = ctypes.c_int
+            L.bpe_embed.argtypes = [p, p, i64, p, i, i64, i64, i64, f, i32, p, i, i64, p]
+            L.bpe_embed_grad.restype = ctypes.c_int
+            L.bpe_embed_grad.argtypes = [p, p, i64, p, i, i64, f, i32, i64, i64, p, i, i64, i, p]
             L.bpe_workspace_bytes.restype = ctypes.c_int
             L.bpe_workspace_bytes.argtypes = [p, ctypes.POINTER(i64)]
             L.bpe_destroy.restype = ctypes.c_int
             L.bpe_destroy.argtypes = [p]
             L.bpe_last_error.restype = ctypes.c_char_p
             L.bpe_last_error.argtypes = []
-            _ = i32
             _lib = L
     return _lib
 
@@ -275,6 +279,25 @@ def bpe_workspace_bytes(handle: int) -> int:
     return b.value
 
 
+F32, F16, BF16 = 0, 1, 2  # element types of the operators below
+NO_ID = -2 ** 31  # a skip_id that no token has
+
+
+def bpe_embed(handle: int, d_ids: int, n_ids: int, d_weight: int, weight_type: int, n_rows: int, dim: int,
+              weight_stride: int, scale: float, skip_id: int, d_out: int, out_type: int, out_stride: int,
+              stream: int) -> None:
+    _check(lib().bpe_embed(handle, d_ids, n_ids, d_weight, weight_type, n_rows, dim, weight_stride, scale, skip_id,
+                           d_out, out_type, out_stride, stream))
+
+
+def bpe_embed_grad(handle: int, d_ids: int, n_ids: int, d_grad_out: int, grad_out_type: int, grad_out_stride: int,
+                   scale: float, skip_id: int, n_rows: int, dim: int, d_grad_weight: int, grad_weight_type: int,
+                   grad_weight_stride: int, accumulate: bool, stream: int) -> None:
+    _check(lib().bpe_embed_grad(handle, d_ids, n_ids, d_grad_out, grad_out_type, grad_out_stride, scale, skip_id,
+                                n_rows, dim, d_grad_weight, grad_weight_type, grad_weight_stride,
+                                1 if accumulate else 0, stream))
+
+
 def bpe_destroy(handle: int) -> None:
     _check(lib().bpe_destroy(handle))
 
@@ -332,6 +355,116 @@ class Tokenizer:
                                  id_offsets.numel() - 1, out.data_ptr(), capacity, out_off.data_ptr(), True,
                                  self._stream())
         return out[:total], out_off
+
+
+    # ---- what surrounds the model ----
+
+    def _checked(self, name, t, dtypes, dims=None):
+        if t.device.type != "cuda" or t.device.index != self.device:
+            raise ValueError(f"{name}: on {t.device}, the tokenizer is on cuda:{self.device}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: {t.dtype}, need one of {', '.join(str(d) for d in dtypes)}")
+        if dims is not None and t.dim() != dims:
+            raise ValueError(f"{name}: {t.dim()} dimensions, need {dims}")
+
+    def _ids(self, ids):
+        import torch
+        self._checked("ids", ids, (torch.int32,))
+        return ids if ids.is_contiguous() else ids.contiguous()
+
+    def embed(self, ids, weight, scale: float = 1.0, skip_id: int | None = None, dtype=None, out=None):
+        """scale * weight[ids] in weight's type, or in ``dtype``: ids int32 of
+        any shape, weight [rows, dim] in 32 or 16 bits with any row stride.
+        Tokens equal to skip_id get zeros. Differentiable with respect to
+        weight (its gradient runs embed_grad) unless ``out`` is given."""
+        import torch
+        types = _types()
+        self._checked("weight", weight, types, 2)
+        ids = self._ids(ids)
+        if out is None:
+            dtype = dtype or weight.dtype
+            if weight.requires_grad and torch.is_grad_enabled():
+                return _embed_function().apply(self, ids, weight, scale, skip_id, dtype)
+            out = torch.empty(*ids.shape, weight.shape[1], dtype=dtype, device=weight.device)
+            self._checked("dtype", out, types)
+        else:
+            self._checked("out", out, types)
+            if out.shape != (*ids.shape, weight.shape[1]) or (out.dim() != 2 and not out.is_contiguous()):
+                raise ValueError("out: needs the shape of ids and weight's columns, and to be contiguous "
+                                 "where ids is not one-dimensional")
+        if weight.stride(1) != 1 and weight.shape[1] > 1:
+            weight = weight.contiguous()
+        if out.dim() == 2 and out.stride(1) != 1 and out.shape[1] > 1:
+            raise ValueError("out: the elements of a row must be adjacent")
+        dim = weight.shape[1]
+        bpe_embed(self.handle, ids.data_ptr(), ids.numel(), weight.data_ptr(), types[weight.dtype], weight.shape[0],
+                  dim, weight.stride(0), scale, NO_ID if skip_id is None else skip_id, out.data_ptr(),
+                  types[out.dtype], out.stride(0) if out.dim() == 2 else dim, self._stream())
+        return out
+
+    def embed_grad(self, ids, grad, n_rows: int, scale: float = 1.0, skip_id: int | None = None, dtype=None,
+                   out=None, accumulate: bool = False):
+        """The gradient [n_rows, dim] of embed's weight for the gradient
+        ``grad`` [*ids.shape, dim] of its result, in grad's type or in
+        ``dtype``, or written into (accumulate: added to) ``out``."""
+        import torch
+        types = _types()
+        self._checked("grad", grad, types)
+        ids = self._ids(ids)
+        if grad.shape[:-1] != ids.shape:
+            raise ValueError("grad: needs the shape of ids and one more dimension")
+        dim = grad.shape[-1]
+        grad = grad.reshape(ids.numel(), dim)
+        if grad.stride(1) != 1 and dim > 1:
+            grad = grad.contiguous()
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs out")
+            out = torch.empty(n_rows, dim, dtype=dtype or grad.dtype, device=grad.device)
+        self._checked("out", out, types, 2)
+        if out.shape != (n_rows, dim) or (out.stride(1) != 1 and dim > 1):
+            raise ValueError("out: needs n_rows rows of grad's columns, the elements of a row adjacent")
+        bpe_embed_grad(self.handle, ids.data_ptr(), ids.numel(), grad.data_ptr(), types[grad.dtype], grad.stride(0),
+                       scale, NO_ID if skip_id is None else skip_id, n_rows, dim, out.data_ptr(), types[out.dtype],
+                       out.stride(0), accumulate, self._stream())
+        return out
+
+
+_type_codes = {}
+
+
+def _types():
+    if not _type_codes:
+        import torch
+        _type_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    return _type_codes
+
+
+def _embed_function():
+    """The autograd function of Tokenizer.embed (made once: torch is imported
+    on first use only)."""
+    global _embed_fn
+    if _embed_fn is None:
+        import torch
+
+        class EmbedFunction(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, tok, ids, weight, scale, skip_id, dtype):
+                ctx.args = (tok, weight.shape[0], scale, skip_id, weight.dtype)
+                ctx.save_for_backward(ids)
+                return tok.embed(ids, weight.detach(), scale, skip_id, dtype)
+
+            @staticmethod
+            def backward(ctx, grad):
+                tok, n_rows, scale, skip_id, dtype = ctx.args
+                (ids,) = ctx.saved_tensors
+                return None, None, tok.embed_grad(ids, grad, n_rows, scale, skip_id, dtype), None, None, None
+
+        _embed_fn = EmbedFunction
+    return _embed_fn
+
+
+_embed_fn = None
 
 
 def pretokenize(data, offsets):

@@ -1,0 +1,67 @@
+// Operators between the encoder and a language model, on packed ids: block
+// plans of a paged cache (blocks.cuh), embedding lookup and its gradient
+// (embed.cuh), penalties, biases and grammar masks on logits (logits.cuh).
+// The source pages end at the ids; these have no counterpart there.
+//
+// They share the handle's device, workspace and status with the encoder
+// (handle.cuh). No kernel waits on another CTA outside its own cluster.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "handle.cuh"
+
+using namespace bpe_impl;
+
+namespace {
+
+size_t type_size(int type) { return type == BPE_F32 ? 4 : 2; }
+bool type_ok(int type) { return type == BPE_F32 || type == BPE_F16 || type == BPE_BF16; }
+bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+template <class T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Rounds to nearest even, once, at the end of a 32-bit computation.
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
+
+// f(T{}) with the C++ type of a BPE_F32, BPE_F16 or BPE_BF16.
+template <class F>
+int with_type(int type, F f) {
+  if (type == BPE_F32) return f(float{});
+  if (type == BPE_F16) return f(__half{});
+  return f(__nv_bfloat16{});
+}
+
+// No exception (an allocation for an error message, say) leaves a C entry.
+template <class F>
+int guarded(const char* what, F f) noexcept {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    try {
+      return fail(BPE_ERR_INTERNAL, std::string(what) + ": " + e.what());
+    } catch (...) {
+      return BPE_ERR_INTERNAL;
+    }
+  }
+}
+
+}  // namespace
+
+#include "embed.cuh"

@@ -316,6 +316,71 @@ int bpe_set_phase_events(bpe_handle* h, void** events, int n);
 int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int64_t* word_counts, int64_t n_words,
               int64_t n_merges, int device, int32_t* merges_out, int64_t* n_made);
 
+/*
+ * Operators between the encoder and a language model. The pages have no
+ * counterpart: they end at the token ids. These calls take the ids and
+ * offsets as bpe_encode_batch writes them, so a step needs no host round trip
+ * between the encoder and the model:
+ *   bpe_plan_blocks    block tables and cache slots of a batch of requests;
+ *   bpe_embed          rows of an embedding table;
+ *   bpe_embed_grad     its gradient;
+ *   bpe_adjust_logits  penalties, biases and grammar masks, before the choice
+ *                      of the next ids that bpe_decode_batch takes.
+ * They use the handle's device, workspace and status; its vocabulary plays no
+ * part, so an embedding table or logits may be padded past it. Errors that
+ * only the kernels can see (an id or length out of range) do not stop a call:
+ * what is concerned is left out as stated below, nothing is read or written
+ * out of range, and the next bpe_sync_status() on the handle returns
+ * BPE_ERR_BAD_INPUT. A call that finds its workspace too small grows it
+ * (cudaFree, cudaMalloc); make a call of the largest size before any stream
+ * capture.
+ */
+#define BPE_F32 0
+#define BPE_F16 1
+#define BPE_BF16 2
+
+/*
+ * bpe_embed — out[i, :] = scale * weight[ids[i], :].
+ *
+ *   d_ids          device int32[n_ids], n_ids < 2^31 - 1024.
+ *   d_weight       device [n_rows][dim] of weight_type, rows weight_stride
+ *                  elements apart (any stride >= 0).
+ *   scale          multiplied in 32 bits; the product is rounded once.
+ *   skip_id        tokens with this id get a row of zeros (padding). Pass an
+ *                  id that does not occur, such as INT32_MIN, for none.
+ *   d_out          device [n_ids][dim] of out_type, rows out_stride elements
+ *                  apart (>= dim).
+ * Types are BPE_F32, BPE_F16 or BPE_BF16, in any pair. Pointers are aligned to
+ * their elements; rows whose addresses are all multiples of 16 bytes are
+ * moved fastest. An id outside [0, n_rows) other than skip_id gets a row of
+ * zeros and is reported (BPE_ERR_BAD_INPUT, see above).
+ */
+int bpe_embed(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const void* d_weight, int weight_type,
+              int64_t n_rows, int64_t dim, int64_t weight_stride, float scale, int32_t skip_id, void* d_out,
+              int out_type, int64_t out_stride, bpe_stream_t stream);
+
+/*
+ * bpe_embed_grad — the gradient of bpe_embed with respect to its table:
+ * grad_weight[r, :] = scale * (sum over the tokens i with ids[i] = r of
+ * grad_out[i, :]), added to what is there if accumulate is not 0.
+ *
+ *   d_ids, n_ids, scale, skip_id   as for bpe_embed.
+ *   d_grad_out     device [n_ids][dim] of grad_out_type, rows grad_out_stride
+ *                  elements apart (any stride >= 0; 0 for one row for all).
+ *   d_grad_weight  device [n_rows][dim] of grad_weight_type, rows
+ *                  grad_weight_stride elements apart (>= dim). Without
+ *                  accumulate every element is written (rows without a token
+ *                  get zeros); with it rows without a token are not touched.
+ * Sums are held in 32 bits and rounded once. Their order is fixed by the ids
+ * alone, so equal inputs give equal bits. Tokens whose id is skip_id or out of
+ * range add to no row (the latter are reported).
+ * Workspace: 16 bytes a token, 4 bytes a row.
+ */
+int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const void* d_grad_out, int grad_out_type,
+                   int64_t grad_out_stride, float scale, int32_t skip_id, int64_t n_rows, int64_t dim,
+                   void* d_grad_weight, int grad_weight_type, int64_t grad_weight_stride, int accumulate,
+                   bpe_stream_t stream);
+
 /* Waits for the stream and returns (then clears) errors the kernels of
  * earlier calls on this handle recorded. */
 int bpe_sync_status(bpe_handle* h, bpe_stream_t stream);
