@@ -71,7 +71,7 @@ _lib = None
 
 EXPORTS = ["bpe_build", "bpe_encode_batch", "bpe_encode_batch_host", "bpe_encode_batch_noalloc", "bpe_pretokenize_batch", "bpe_decode_batch", "bpe_set_word_cache",
            "bpe_set_timing_events", "bpe_set_phase_events", "bpe_set_call_memo", "bpe_sync_status", "bpe_table_info", "bpe_table_monotone", "bpe_merges_monotone",
-           "bpe_workspace_bytes", "bpe_train", "bpe_embed", "bpe_embed_grad", "bpe_destroy", "bpe_last_error"]
+           "bpe_workspace_bytes", "bpe_train", "bpe_plan_blocks", "bpe_embed", "bpe_embed_grad", "bpe_adjust_logits", "bpe_destroy", "bpe_last_error"]
 
 
 def lib():
@@ -119,6 +119,10 @@ def lib():
             L.bpe_embed.argtypes = [p, p, i64, p, i, i64, i64, i64, f, i32, p, i, i64, p]
             L.bpe_embed_grad.restype = ctypes.c_int
             L.bpe_embed_grad.argtypes = [p, p, i64, p, i, i64, f, i32, i64, i64, p, i, i64, i, p]
+            L.bpe_plan_blocks.restype = ctypes.c_int
+            L.bpe_plan_blocks.argtypes = [p, p, p, i64, i64, p, i64, p, p, i64, i64, p, p, p, i64, p, p]
+            L.bpe_adjust_logits.restype = ctypes.c_int
+            L.bpe_adjust_logits.argtypes = [p, p, p]
             L.bpe_workspace_bytes.restype = ctypes.c_int
             L.bpe_workspace_bytes.argtypes = [p, ctypes.POINTER(i64)]
             L.bpe_destroy.restype = ctypes.c_int
@@ -298,6 +302,29 @@ def bpe_embed_grad(handle: int, d_ids: int, n_ids: int, d_grad_out: int, grad_ou
                                 1 if accumulate else 0, stream))
 
 
+def bpe_plan_blocks(handle: int, d_offsets: int | None, d_cached: int | None, n_requests: int, block_size: int,
+                    d_free: int, n_free: int, d_head: int | None, d_table: int, max_blocks: int, table_stride: int,
+                    d_seq_lens: int, d_slots: int, d_positions: int, n_slots: int, d_info: int, stream: int) -> None:
+    _check(lib().bpe_plan_blocks(handle, d_offsets, d_cached, n_requests, block_size, d_free, n_free, d_head, d_table,
+                                 max_blocks, table_stride, d_seq_lens, d_slots, d_positions, n_slots, d_info, stream))
+
+
+class LogitsArgs(ctypes.Structure):
+    """bpe_logits_args (device pointers as integers, None for NULL)."""
+    _fields_ = [(n, t) for names, t in (
+        ("logits out", ctypes.c_void_p), ("logits_type out_type", ctypes.c_int),
+        ("logits_stride out_stride n_rows n_vocab", ctypes.c_int64),
+        ("prompt_ids prompt_offsets", ctypes.c_void_p), ("n_prompt_ids", ctypes.c_int64),
+        ("output_ids output_lens", ctypes.c_void_p), ("output_stride output_capacity", ctypes.c_int64),
+        ("repetition frequency presence bias_ids bias_values bias_offsets", ctypes.c_void_p),
+        ("n_bias", ctypes.c_int64), ("mask", ctypes.c_void_p), ("mask_stride n_masks", ctypes.c_int64),
+        ("mask_rows", ctypes.c_void_p)) for n in names.split()]
+
+
+def bpe_adjust_logits(handle: int, args: LogitsArgs, stream: int) -> None:
+    _check(lib().bpe_adjust_logits(handle, ctypes.byref(args), stream))
+
+
 def bpe_destroy(handle: int) -> None:
     _check(lib().bpe_destroy(handle))
 
@@ -371,6 +398,109 @@ class Tokenizer:
         import torch
         self._checked("ids", ids, (torch.int32,))
         return ids if ids.is_contiguous() else ids.contiguous()
+
+    def plan_blocks(self, offsets, cached, table, free, block_size: int, n_slots: int | None = None, head=None):
+        """Block tables, cache slots and positions for the next step of a
+        batch of requests (see bpe_plan_blocks): offsets int64[n + 1] of the
+        packed new tokens, or None for one new token each; cached int32[n]
+        tokens in the cache, or None; table int32[n, max_blocks], extended in
+        place from the free list int32[m], of which the first head (int64[1],
+        None: 0) entries are taken. n_slots: places for the new tokens, at
+        least their number (needed with offsets, whose end is on the device).
+        Returns (seq_lens int32[n], slots int64[n_slots], positions
+        int32[n_slots], info int64[2]: head after the call, blocks lacking)."""
+        import torch
+        self._checked("table", table, (torch.int32,), 2)
+        n = table.shape[0]
+        for name, t, dtype, size in (("offsets", offsets, torch.int64, n + 1), ("cached", cached, torch.int32, n),
+                                     ("free", free, torch.int32, None), ("head", head, torch.int64, 1)):
+            if t is not None:
+                self._checked(name, t, (dtype,), 1)
+                if (size is not None and t.shape[0] != size) or not t.is_contiguous():
+                    raise ValueError(f"{name}: needs {size} adjacent elements, one row of the table each")
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table: the elements of a row must be adjacent")
+        if n_slots is None:
+            if offsets is not None:
+                raise ValueError("n_slots: the number of new tokens (or more) is needed with offsets")
+            n_slots = n
+        dev = table.device
+        seq_lens = torch.empty(n, dtype=torch.int32, device=dev)
+        slots = torch.empty(n_slots, dtype=torch.int64, device=dev)
+        positions = torch.empty(n_slots, dtype=torch.int32, device=dev)
+        info = torch.empty(2, dtype=torch.int64, device=dev)
+        bpe_plan_blocks(self.handle, None if offsets is None else offsets.data_ptr(),
+                        None if cached is None else cached.data_ptr(), n, block_size, free.data_ptr(), free.shape[0],
+                        None if head is None else head.data_ptr(), table.data_ptr(), table.shape[1], table.stride(0),
+                        seq_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), n_slots, info.data_ptr(),
+                        self._stream())
+        return seq_lens, slots, positions, info
+
+    def adjust_logits(self, logits, prompt=None, output=None, repetition=None, frequency=None, presence=None,
+                      bias=None, mask=None, mask_rows=None, dtype=None, out=None):
+        """Penalties for repeated tokens, biases and grammar masks (see
+        bpe_adjust_logits) on logits [n, vocab] in 32 or 16 bits, into a new
+        tensor of logits' type or ``dtype``, or into ``out`` (which may be
+        logits). prompt: (ids int32[p], offsets int64[n + 1]) as encode
+        returns them; output: (ids int32[n, capacity], lens int32[n]);
+        repetition, frequency, presence: float32[n]; bias: (ids int32[m],
+        values float32[m], offsets int64[n + 1]); mask: int32 or uint32
+        [masks, ceil(vocab / 32)], bit v % 32 of word v / 32 set for an
+        allowed token; mask_rows: int32[n], each row's mask or -1."""
+        import torch
+        types = _types()
+        self._checked("logits", logits, types, 2)
+        n, vocab = logits.shape
+        if logits.stride(1) != 1 and vocab > 1:
+            if out is logits:
+                raise ValueError("out: the elements of a row must be adjacent")
+            logits = logits.contiguous()
+        if out is None:
+            out = torch.empty(n, vocab, dtype=dtype or logits.dtype, device=logits.device)
+        self._checked("out", out, types, 2)
+        if out.shape != logits.shape or (out.stride(1) != 1 and vocab > 1):
+            raise ValueError("out: needs the shape of logits, the elements of a row adjacent")
+        a = LogitsArgs(logits=logits.data_ptr(), out=out.data_ptr(), logits_type=types[logits.dtype],
+                       out_type=types[out.dtype], logits_stride=logits.stride(0), out_stride=out.stride(0),
+                       n_rows=n, n_vocab=vocab)
+
+        def flat(name, t, dtype, size=None):
+            self._checked(name, t, (dtype,), 1)
+            if (size is not None and t.shape[0] != size) or not t.is_contiguous():
+                raise ValueError(f"{name}: needs {'adjacent' if size is None else size} elements")
+            return t.data_ptr()
+
+        if prompt is not None:
+            ids, offsets = prompt
+            a.prompt_ids, a.n_prompt_ids = flat("prompt ids", ids, torch.int32), ids.shape[0]
+            a.prompt_offsets = flat("prompt offsets", offsets, torch.int64, n + 1)
+        if output is not None:
+            ids, lens = output
+            self._checked("output ids", ids, (torch.int32,), 2)
+            if ids.shape[0] != n or (ids.stride(1) != 1 and ids.shape[1] > 1):
+                raise ValueError("output ids: needs a row for each row of logits, its elements adjacent")
+            a.output_ids, a.output_stride, a.output_capacity = ids.data_ptr(), ids.stride(0), ids.shape[1]
+            a.output_lens = flat("output lens", lens, torch.int32, n)
+        if repetition is not None:
+            a.repetition = flat("repetition", repetition, torch.float32, n)
+        if frequency is not None:
+            a.frequency = flat("frequency", frequency, torch.float32, n)
+        if presence is not None:
+            a.presence = flat("presence", presence, torch.float32, n)
+        if bias is not None:
+            ids, values, offsets = bias
+            a.bias_ids, a.n_bias = flat("bias ids", ids, torch.int32), ids.shape[0]
+            a.bias_values = flat("bias values", values, torch.float32, ids.shape[0])
+            a.bias_offsets = flat("bias offsets", offsets, torch.int64, n + 1)
+        if mask is not None:
+            self._checked("mask", mask, (torch.int32, torch.uint32), 2)
+            if mask.shape[1] < (vocab + 31) // 32 or (mask.stride(1) != 1 and mask.shape[1] > 1):
+                raise ValueError("mask: needs a bit for each token, the words of a row adjacent")
+            a.mask, a.mask_stride, a.n_masks = mask.data_ptr(), mask.stride(0), mask.shape[0]
+            if mask_rows is not None:
+                a.mask_rows = flat("mask rows", mask_rows, torch.int32, n)
+        bpe_adjust_logits(self.handle, a, self._stream())
+        return out
 
     def embed(self, ids, weight, scale: float = 1.0, skip_id: int | None = None, dtype=None, out=None):
         """scale * weight[ids] in weight's type, or in ``dtype``: ids int32 of

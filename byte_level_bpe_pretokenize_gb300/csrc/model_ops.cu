@@ -64,4 +64,6 @@ int guarded(const char* what, F f) noexcept {
 
 }  // namespace
 
+#include "blocks.cuh"
 #include "embed.cuh"
+#include "logits.cuh"

@@ -340,6 +340,51 @@ int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int6
 #define BPE_BF16 2
 
 /*
+ * bpe_plan_blocks — block tables, cache slots and positions for the next step
+ * of a batch of requests, from their lengths on the device.
+ *
+ * A paged cache has blocks of block_size slots; slot t of block q is slot
+ * q * block_size + t of the cache. Request i holds cached[i] tokens in the
+ * first ceil(cached[i] / block_size) blocks of its table row and brings new
+ * ones; the blocks it lacks are taken from the free list.
+ *
+ *   d_offsets     device int64[n_requests + 1], as bpe_encode_batch writes
+ *                 them: request i's new tokens are [d_offsets[i],
+ *                 d_offsets[i + 1]) of the packed batch. May be NULL: one new
+ *                 token for each request (a decode step).
+ *   d_cached      device int32[n_requests], tokens in the cache. NULL: none.
+ *   block_size    slots of a block, >= 1, not only powers of two.
+ *   d_free        device int32[n_free], the free list (block numbers).
+ *   d_head        device int64*, entries of the free list that are already
+ *                 taken. NULL: none.
+ *   d_table       device int32[n_requests][max_blocks], rows table_stride
+ *                 elements apart. Rows are extended in place: entries for the
+ *                 new blocks are written, no other is touched.
+ *   d_seq_lens    device int32[n_requests]: tokens in the cache after the
+ *                 step.
+ *   d_slots       device int64[n_slots]: the cache slot of each new token; -1
+ *                 for tokens of requests that are not served and past the
+ *                 last token (n_slots may be padded to a captured size).
+ *   d_positions   device int32[n_slots]: each token's place in its request; 0
+ *                 past the last token.
+ *   d_info        device int64[2]: the free list's head after the call (may
+ *                 be d_head itself), and the blocks lacking.
+ *
+ * Blocks are dealt in request order. A request whose blocks the list cannot
+ * cover, after those of the requests before it, gets none (seq_lens holds
+ * cached[i]); requests that need no block are always served. That is no
+ * error: info[1] is how many blocks more would have served all.
+ * Reported (BPE_ERR_BAD_INPUT) and not served: a request whose offsets are
+ * not monotone in [0, n_slots], whose cached length is negative, or that needs
+ * more than max_blocks; a head outside [0, n_free] counts as an empty list.
+ * Sizes: n_requests and n_slots < 2^31 - 1. Workspace: 8 bytes a request.
+ */
+int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_cached, int64_t n_requests,
+                    int64_t block_size, const int32_t* d_free, int64_t n_free, const int64_t* d_head,
+                    int32_t* d_table, int64_t max_blocks, int64_t table_stride, int32_t* d_seq_lens, int64_t* d_slots,
+                    int32_t* d_positions, int64_t n_slots, int64_t* d_info, bpe_stream_t stream);
+
+/*
  * bpe_embed — out[i, :] = scale * weight[ids[i], :].
  *
  *   d_ids          device int32[n_ids], n_ids < 2^31 - 1024.
@@ -380,6 +425,67 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
                    int64_t grad_out_stride, float scale, int32_t skip_id, int64_t n_rows, int64_t dim,
                    void* d_grad_weight, int grad_weight_type, int64_t grad_weight_stride, int accumulate,
                    bpe_stream_t stream);
+
+/*
+ * bpe_adjust_logits — penalties for repeated tokens, biases and grammar masks
+ * on a batch's logits. For row b and token v, with k the times v occurs in the
+ * row's output:
+ *   x = logits[b][v]
+ *   v in the prompt or the output:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   k > 0:                          x = x - frequency[b] * k - presence[b]
+ *   v in the row's biases:          x = x + (the sum of its values, in order)
+ *   v's bit clear in the row's mask: x = -infinity, whatever it was (NaN too)
+ *   out[b][v] = x, computed in 32 bits and rounded once.
+ * A mask without a set bit leaves a row of -infinity.
+ *
+ * Every pointer is a device pointer. A NULL one leaves its part out:
+ *   logits, out      [n_rows][n_vocab] of logits_type and out_type, rows
+ *                    logits_stride and out_stride elements apart; out may be
+ *                    logits itself (one type, one stride), but must not
+ *                    overlap it otherwise.
+ *   prompt_ids       int32[n_prompt_ids] and prompt_offsets int64[n_rows + 1],
+ *                    as bpe_encode_batch writes them.
+ *   output_ids       int32, row b's are output_ids[b * output_stride ..
+ *                    + output_lens[b]); output_lens int32[n_rows] in
+ *                    [0, output_capacity].
+ *   repetition, frequency, presence   float[n_rows]; NULL for 1, 0 and 0. A row
+ *                    whose three are 1, 0 and 0 does not read its history.
+ *   bias_ids         int32[n_bias], bias_values float[n_bias] and bias_offsets
+ *                    int64[n_rows + 1]: row b's biases are [bias_offsets[b],
+ *                    bias_offsets[b + 1]). An id may occur more than once.
+ *   mask             uint32[n_masks], rows mask_stride words apart; bit
+ *                    (v % 32) of word v / 32 is token v's.
+ *   mask_rows        int32[n_rows]: each row's mask, -1 for none. NULL: row b
+ *                    has mask b.
+ * Ids outside [0, n_vocab), offsets that are not monotone in their list,
+ * lengths past output_capacity and mask rows past n_masks are left out and
+ * reported (BPE_ERR_BAD_INPUT).
+ * Sizes: n_rows <= 65535, n_vocab < 2^31 - 1, output_capacity < 2^30.
+ */
+typedef struct bpe_logits_args {
+  const void* logits;
+  void* out;
+  int logits_type, out_type;
+  int64_t logits_stride, out_stride;
+  int64_t n_rows, n_vocab;
+  const int32_t* prompt_ids;
+  const int64_t* prompt_offsets;
+  int64_t n_prompt_ids;
+  const int32_t* output_ids;
+  const int32_t* output_lens;
+  int64_t output_stride, output_capacity;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  const int64_t* bias_offsets;
+  int64_t n_bias;
+  const uint32_t* mask;
+  int64_t mask_stride, n_masks;
+  const int32_t* mask_rows;
+} bpe_logits_args;
+int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe_stream_t stream);
 
 /* Waits for the stream and returns (then clears) errors the kernels of
  * earlier calls on this handle recorded. */
