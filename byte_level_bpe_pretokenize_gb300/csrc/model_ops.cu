@@ -9,11 +9,14 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "handle.cuh"
 
 using namespace bpe_impl;
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -64,6 +67,7 @@ int guarded(const char* what, F f) noexcept {
 
 }  // namespace
 
+#include "vec.cuh"
 #include "blocks.cuh"
 #include "embed.cuh"
 #include "logits.cuh"

@@ -389,7 +389,8 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
  *
  *   d_ids          device int32[n_ids], n_ids < 2^31 - 1024.
  *   d_weight       device [n_rows][dim] of weight_type, rows weight_stride
- *                  elements apart (any stride >= 0).
+ *                  elements apart (any stride >= 0); n_rows < 2^31 - 1024,
+ *                  dim <= 2^22.
  *   scale          multiplied in 32 bits; the product is rounded once.
  *   skip_id        tokens with this id get a row of zeros (padding). Pass an
  *                  id that does not occur, such as INT32_MIN, for none.
