@@ -58,29 +58,94 @@ __global__ void __launch_bounds__(kEmbThreads) k_embed(const int32_t* ids, int64
   }
 }
 
-// ------------------------------------------------------------------ sort --
+// ------------------------------------------------------- sort and zero rows --
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBits = 10;  // a bin for each thread
 constexpr int kSortCluster = 16;
+constexpr int kSortBatch = 4;     // tokens that a lane holds
+constexpr int kFillRows = 2048;   // rows a CTA marks at once
+constexpr int kFillPage = 16384;  // bytes of a bulk store
 
-struct SortArgs {
+// Rows [r0, r1) without a token become zeros: the CTA reads every id and marks
+// the rows that are met; then each thread takes a row and stores its 16-byte
+// aligned inside in bulk from a page of zeros in shared memory, which leaves
+// the SM's issue slots free, and its ragged ends by element.
+struct FillArgs {
   const int32_t* ids;
   int64_t n, n_rows;
   int32_t skip_id;
-  int passes, bits;       // passes of `bits` bits each, lowest first
-  int64_t per_warp;       // tokens of a warp, a multiple of 32
-  uint2* ping[2];         // (key, token) between passes
-  int32_t *key, *pos;     // the sorted keys and tokens
-  int32_t* row_start;     // [n_rows + 1]
+  unsigned char* out;
+  int64_t row_bytes, stride_bytes, row_step;  // row_step: rows of a CTA at once, at most kFillRows
+  int element;                                // bytes of an element
+};
+
+struct FillSmem {
+  __align__(16) unsigned char zeros[kFillPage];
+  uint8_t met[kFillRows];
+};
+
+__device__ void fill_absent(const FillArgs& a, int64_t r0, int64_t r1, FillSmem& sm) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  for (int b = tid; b < kFillRows; b += threads) sm.met[b] = 0;
+  for (int b = tid; b < kFillPage / 16; b += threads) reinterpret_cast<uint4*>(sm.zeros)[b] = make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  constexpr int kBatch = 8;
+  for (int64_t i0 = tid; i0 < a.n; i0 += kBatch * threads) {
+    int32_t id[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) id[q] = i0 + q * threads < a.n ? __ldg(a.ids + i0 + q * threads) : -1;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
+      if (id[q] >= r0 && id[q] < r1 && id[q] != a.skip_id) sm.met[id[q] - r0] = 1;
+  }
+  __syncthreads();
+  const uint32_t page = (uint32_t)__cvta_generic_to_shared(sm.zeros);
+  for (int64_t r = r0 + tid; r < r1; r += threads) {
+    if (sm.met[r - r0]) continue;
+    unsigned char* row = a.out + r * a.stride_bytes;
+    unsigned char* end = row + a.row_bytes;
+    unsigned char* from = row + (-reinterpret_cast<uintptr_t>(row) & 15);
+    unsigned char* to = end - (reinterpret_cast<uintptr_t>(end) & 15);
+    if (from >= to) from = to = end;
+    auto element = [&](unsigned char* at) {
+      if (a.element == 4) *reinterpret_cast<uint32_t*>(at) = 0;
+      else *reinterpret_cast<uint16_t*>(at) = 0;
+    };
+    for (unsigned char* at = row; at < from; at += a.element) element(at);
+    for (unsigned char* at = from; at < to; at += kFillPage) {
+      const uint32_t size = (uint32_t)min((int64_t)kFillPage, (int64_t)(to - at));
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(at), "r"(page), "r"(size)
+                   : "memory");
+    }
+    for (unsigned char* at = to; at < end; at += a.element) element(at);
+  }
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncthreads();
+}
+
+// The rows of filler `who` of `fillers`.
+__device__ __forceinline__ void fill_rows(const FillArgs& a, int64_t who, int64_t fillers, FillSmem& sm) {
+  for (int64_t r = who * a.row_step; r < a.n_rows; r += fillers * a.row_step)
+    fill_absent(a, r, min(r + a.row_step, a.n_rows), sm);
+}
+
+struct SortArgs {
+  FillArgs fill;
+  int passes, bits;    // passes of `bits` bits each, lowest first
+  int64_t per_warp;    // tokens of a warp, a multiple of 32
+  uint2* ping[2];      // (key, token); the last pass p writes ping[p & 1]
   DevSmall* small;
 };
 
-// Tokens sorted by row, equal rows in token order: a counting sort by `bits`
-// bits a pass, by the CTAs of one cluster. Tokens without a row (skip_id, and
-// ids out of range, which are reported) get the key n_rows and sort last.
-// row_start[r] is the first sorted place whose key is at least r.
+// The first cluster sorts the tokens by row, equal rows in token order: a
+// counting sort by `bits` bits a pass. Tokens without a row (skip_id, and ids
+// out of range, which are reported) get the key n_rows and sort last. The
+// other clusters meanwhile zero the rows without a token: the sort needs few
+// SMs and the zeros are most of what is written.
 //
 // A pass: each warp counts the digits of its run of tokens in its own bins;
 // the bins' prefix over warps, over the cluster's CTAs (read through
@@ -88,38 +153,57 @@ struct SortArgs {
 // for each digit; then the warp walks its run again, 32 tokens at a time, and
 // a match of equal digits ranks them in token order.
 __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
-  extern __shared__ int32_t sort_smem[];
-  const int bins = 1 << a.bits;
-  int32_t* hist = sort_smem;                       // [kSortWarps][bins]
-  int32_t* total = hist + kSortWarps * bins;       // [bins]: of this CTA
-  int32_t* base = total + bins;                    // [bins]: this CTA's first place
-  int32_t* start = base + bins;                    // [bins + 1]: the cluster's first place
-  int32_t* warp_sum = start + bins + 1;            // [kSortWarps]
+  extern __shared__ __align__(16) int32_t sort_smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int n_ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  if (blockIdx.x >= n_ctas) {
+    fill_rows(a.fill, blockIdx.x - n_ctas, gridDim.x - n_ctas, *reinterpret_cast<FillSmem*>(sort_smem));
+    return;
+  }
+  const int64_t n = a.fill.n, n_rows = a.fill.n_rows;
+  const int bins = 1 << a.bits;
+  int32_t* hist = sort_smem;                  // [kSortWarps][bins]
+  int32_t* total = hist + kSortWarps * bins;  // [bins]: of this CTA
+  int32_t* base = total + bins;               // [bins]: this CTA's first place
+  int32_t* warp_sum = base + bins;            // [kSortWarps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t first = ((int64_t)rank * kSortWarps + warp) * a.per_warp;
-  const int64_t last = min(first + a.per_warp, a.n);
+  const int64_t last = min(first + a.per_warp, n);
+  const bool held = a.per_warp <= 32 * kSortBatch;  // a warp's tokens stay in its registers
   int32_t* mine = hist + warp * bins;
   for (int p = 0; p < a.passes; ++p) {
     const int shift = p * a.bits;
     const uint2* from = a.ping[(p + 1) & 1];
-    const bool final_pass = p + 1 == a.passes;
-    auto token = [&](int64_t i) -> uint2 {
-      if (p > 0) return __ldcg(from + i);
-      const int32_t id = __ldg(a.ids + i);
-      const bool ok = id != a.skip_id && emb_row_ok(id, a.n_rows);
-      if (!ok && id != a.skip_id) atomicOr(&a.small->op_status, kStBadInput);
-      return make_uint2(ok ? (uint32_t)id : (uint32_t)a.n_rows, (uint32_t)i);
+    // tokens i0 + 32 q + lane; past `last` the key is none
+    auto tokens = [&](int64_t i0, uint2 (&t)[kSortBatch]) {
+#pragma unroll
+      for (int q = 0; q < kSortBatch; ++q) {
+        const int64_t i = i0 + 32 * q + lane;
+        t[q] = make_uint2(0xFFFFFFFFu, 0);
+        if (i >= last) continue;
+        if (p > 0) {
+          t[q] = __ldcg(from + i);
+        } else {
+          const int32_t id = __ldg(a.fill.ids + i);
+          const bool ok = id != a.fill.skip_id && emb_row_ok(id, n_rows);
+          if (!ok && id != a.fill.skip_id) atomicOr(&a.small->op_status, kStBadInput);
+          t[q] = make_uint2(ok ? (uint32_t)id : (uint32_t)n_rows, (uint32_t)i);
+        }
+      }
     };
+    uint2 t[kSortBatch];
     for (int b = tid; b < kSortWarps * bins; b += kSortThreads) hist[b] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int64_t i = first + lane; i < last; i += 32) atomicAdd(&mine[(token(i).x >> shift) & (bins - 1)], 1);
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kSortBatch) {
+      tokens(i0, t);
+#pragma unroll
+      for (int q = 0; q < kSortBatch; ++q)
+        if (t[q].x != 0xFFFFFFFFu) atomicAdd(&mine[(t[q].x >> shift) & (bins - 1)], 1);
+    }
     __syncthreads();
     if (tid < bins) {
       int32_t sum = 0;
-#pragma unroll 8
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const int32_t c = hist[w * bins + tid];
         hist[w * bins + tid] = sum;
@@ -130,8 +214,9 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
     cluster.sync();
     int32_t lower = 0, all = 0;
     if (tid < bins) {
-      for (int r = 0; r < n_ctas; ++r) {
-        const int32_t v = *cluster.map_shared_rank(total + tid, r);
+#pragma unroll
+      for (int r = 0; r < kSortCluster; ++r) {
+        const int32_t v = r < n_ctas ? *cluster.map_shared_rank(total + tid, r) : 0;
         all += v;
         if (r < rank) lower += v;
       }
@@ -155,121 +240,50 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
     }
     __syncthreads();
     if (warp > 0) upto += warp_sum[warp - 1];
-    if (tid < bins) {
-      start[tid] = upto - all;
-      base[tid] = upto - all + lower;
-      if (tid == bins - 1) start[bins] = upto;
-    }
+    if (tid < bins) base[tid] = upto - all + lower;
     __syncthreads();
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool have = i < last;
-      const uint2 t = have ? token(i) : make_uint2(0, 0);
-      const int digit = have ? (int)((t.x >> shift) & (uint32_t)(bins - 1)) : bins;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
-      const int leader = __ffs(same) - 1;
-      int32_t before = 0;
-      if (have && lane == leader) before = atomicAdd(&mine[digit], __popc(same));
-      before = __shfl_sync(0xFFFFFFFFu, before, leader);
-      if (have) {
-        const int32_t to = base[digit] + before + __popc(same & ((1u << lane) - 1));
-        if (final_pass) {
-          a.key[to] = (int32_t)t.x;
-          a.pos[to] = (int32_t)t.y;
-        } else {
-          a.ping[p & 1][to] = t;
-        }
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kSortBatch) {
+      if (!held) tokens(i0, t);
+#pragma unroll
+      for (int q = 0; q < kSortBatch; ++q) {
+        if (i0 + 32 * q >= last) break;
+        const bool have = t[q].x != 0xFFFFFFFFu;
+        const int digit = have ? (int)((t[q].x >> shift) & (uint32_t)(bins - 1)) : bins;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
+        const int leader = __ffs(same) - 1;
+        int32_t before = 0;
+        if (have && lane == leader) before = base[digit] + atomicAdd(&mine[digit], __popc(same));
+        before = __shfl_sync(0xFFFFFFFFu, before, leader);
+        if (have) a.ping[p & 1][before + __popc(same & ((1u << lane) - 1))] = t[q];
       }
     }
     cluster.sync();
-  }
-  // Each row's first place, in the range of its last digit; a thread's rows
-  // step together, so that their loads overlap.
-  const int shift = (a.passes - 1) * a.bits;
-  constexpr int kRows = 8;
-  const int64_t threads = (int64_t)n_ctas * kSortThreads;
-  for (int64_t r0 = (int64_t)rank * kSortThreads + tid; r0 <= a.n_rows; r0 += kRows * threads) {
-    int32_t lo[kRows], hi[kRows];
-    bool more = false;
-#pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      const int64_t r = r0 + q * threads;
-      const int64_t d = r >> shift;
-      lo[q] = r <= a.n_rows ? start[d] : 0;
-      hi[q] = r <= a.n_rows && shift > 0 ? start[d + 1] : lo[q];
-      more |= lo[q] < hi[q];
-    }
-    while (more) {
-      more = false;
-      int32_t k[kRows];
-#pragma unroll
-      for (int q = 0; q < kRows; ++q)
-        if (lo[q] < hi[q]) k[q] = __ldcg(a.key + lo[q] + ((hi[q] - lo[q]) >> 1));
-#pragma unroll
-      for (int q = 0; q < kRows; ++q) {
-        if (lo[q] < hi[q]) {
-          const int32_t mid = lo[q] + ((hi[q] - lo[q]) >> 1);
-          if (k[q] < r0 + q * threads) lo[q] = mid + 1;
-          else hi[q] = mid;
-        }
-        more |= lo[q] < hi[q];
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kRows; ++q)
-      if (r0 + q * threads <= a.n_rows) a.row_start[r0 + q * threads] = lo[q];
   }
 }
 
 // ------------------------------------------------------------------- sum --
 
 constexpr int kSumWarps = 8;
-constexpr int kSumSlabs = 4;    // a lane holds this many vectors of a row
-constexpr int kSumAlone = 16;   // a row of up to this many tokens is one warp's
-constexpr int kSumChunk = 128;  // a row of up to this many is one block's; longer ones are cut at its multiples
+constexpr int kSumCols = 512;     // columns of a block
+constexpr int kSumMaxRun = 16;    // tokens of a warp, at most
+constexpr int kSumRing = 8192;    // bytes of a warp's tokens in flight
 
 template <class TG, class TW>
 struct SumArgs {
-  const int32_t *key, *pos, *row_start;
+  const uint2* sorted;   // (key, token)
   int64_t n, n_rows;
   const TG* grad;
   int64_t grad_stride;
   float scale;
-  int dim;
+  int dim, run;          // run: tokens of a warp
   TW* out;
   int64_t out_stride;
   int accumulate;
-  float* partial;  // [chunks][2][dim]: what a chunk adds to a long row that it begins in, and to one that begins in it
-  int64_t n_chunks;
+  float* partial;        // [chunks][2][dim]: what a chunk adds to the row that it begins in and that began before,
+                         // and to the row that it ends in and that goes on
 };
 
-// acc[s] += the vectors of tokens pos[j0 .. j1) at column col + s * 32 * V.
-template <class TG, int V>
-__device__ __forceinline__ void sum_tokens(float (&acc)[kSumSlabs][V], const int32_t* pos, int32_t j0, int32_t j1,
-                                           const TG* grad, int64_t stride, int col, int dim) {
-  for (int32_t j = j0; j < j1; j += 2) {
-    const bool two = j + 1 < j1;
-    const TG* g0 = grad + (int64_t)__ldg(pos + j) * stride + col;
-    const TG* g1 = grad + (int64_t)__ldg(pos + (two ? j + 1 : j)) * stride + col;
-    Vec<TG, V> a[kSumSlabs], b[kSumSlabs];
-#pragma unroll
-    for (int s = 0; s < kSumSlabs; ++s)
-      if (col + s * 32 * V < dim) {
-        a[s].load(g0 + s * 32 * V);
-        if (two) b[s].load(g1 + s * 32 * V);
-      }
-#pragma unroll
-    for (int s = 0; s < kSumSlabs; ++s)
-      if (col + s * 32 * V < dim) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          acc[s][e] += to_f32(a[s].x[e]);
-          if (two) acc[s][e] += to_f32(b[s].x[e]);
-        }
-      }
-  }
-}
-
+// V columns of row r from their sums.
 template <class TG, class TW, int V>
 __device__ __forceinline__ void sum_write(const SumArgs<TG, TW>& a, int64_t r, int col, const float* x) {
   TW* o = a.out + r * a.out_stride + col;
@@ -281,124 +295,227 @@ __device__ __forceinline__ void sum_write(const SumArgs<TG, TW>& a, int64_t r, i
   v.store(o);
 }
 
-// The block's warps share the tokens pos[j0 .. j1); write(col, x) gets the
-// sums of V columns, added in warp order.
-template <class TG, int V, class W>
-__device__ __forceinline__ void sum_by_block(float* smem, const int32_t* pos, int32_t j0, int32_t j1, const TG* grad,
-                                             int64_t stride, int col0, int dim, W write) {
-  constexpr int kCols = kSumSlabs * 32 * V;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t per = (j1 - j0 + kSumWarps - 1) / kSumWarps;
-  float acc[kSumSlabs][V] = {};
-  sum_tokens<TG, V>(acc, pos, min(j0 + warp * per, j1), min(j0 + (warp + 1) * per, j1), grad, stride,
-                    col0 + lane * V, dim);
-  __syncthreads();
-#pragma unroll
-  for (int s = 0; s < kSumSlabs; ++s)
-#pragma unroll
-    for (int e = 0; e < V; ++e) smem[warp * kCols + (s * V + e) * 32 + lane] = acc[s][e];
-  __syncthreads();
-  for (int v = threadIdx.x; v < kSumSlabs * 32; v += kSumWarps * 32) {
-    const int s = v >> 5, l = v & 31, col = col0 + (s * 32 + l) * V;
-    if (col >= dim) continue;
-    float x[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      x[e] = smem[(s * V + e) * 32 + l];
-#pragma unroll
-      for (int w = 1; w < kSumWarps; ++w) x[e] += smem[w * kCols + (s * V + e) * 32 + l];
-    }
-    write(col, x);
-  }
-}
-
-// Blocks [0, n_chunks): the parts of long rows in a chunk of kSumChunk sorted
-// places. The others: 8 rows each, far apart, so that frequent rows that are
-// neighbours meet different blocks.
+// A block sums kSumCols columns of a chunk of kSumWarps runs of sorted tokens;
+// a warp its run, a lane V adjacent columns in each of kSlabs slabs. Every warp
+// has the same number of tokens, however they are spread over the rows:
+//   * a row that begins and ends inside a run is written by the warp;
+//   * the sums of a run's first and last row go to shared memory, where the
+//     block joins them over its runs in order and writes the rows that begin
+//     and end inside its chunk;
+//   * what the chunk adds to a row that reaches past it goes to `partial`,
+//     which k_emb_join adds up in order.
 template <class TG, class TW, int V>
 __global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
-  __shared__ float smem[kSumWarps * kSumSlabs * 32 * V];
+  constexpr int kSlabs = kSumCols / (32 * V);
+  constexpr bool kRing = V * sizeof(TG) >= 4;  // an asynchronous copy moves 4 bytes at least
+  constexpr int kAhead = kRing ? kSumRing / (kSumCols * (int)sizeof(TG)) : 2;  // tokens in flight
+  extern __shared__ __align__(16) unsigned char sum_smem[];
+  __shared__ float part[kSumWarps][2][kSumCols];
+  __shared__ int32_t part_key[kSumWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col0 = (int)blockIdx.y * kSumSlabs * 32 * V;
-  if (blockIdx.x < a.n_chunks) {
-    const int64_t c0 = (int64_t)blockIdx.x * kSumChunk, c1 = min(c0 + kSumChunk, a.n);
-    const int32_t ra = a.key[c0], rb = a.key[c1 - 1];
-    for (int part = 0; part < 2; ++part) {
-      const int32_t r = part ? rb : ra;
-      if (r >= a.n_rows || (part && ra == rb)) continue;
-      const int32_t s = a.row_start[r], e = a.row_start[r + 1];
-      if (e - s <= kSumChunk) continue;
-      float* to = a.partial + (2 * (int64_t)blockIdx.x + part) * a.dim;
-      sum_by_block<TG, V>(smem, a.pos, (int32_t)max((int64_t)s, c0), (int32_t)min((int64_t)e, c1), a.grad,
-                          a.grad_stride, col0, a.dim, [&](int col, const float* x) {
+  const int64_t c0 = (int64_t)blockIdx.x * kSumWarps * a.run, c1 = min(c0 + kSumWarps * a.run, a.n);
+  const int col0 = (int)blockIdx.y * kSumCols;
+  const int64_t j0 = min(c0 + warp * a.run, c1);
+  const int len = (int)min((int64_t)a.run, c1 - j0);
+  uint2 mine = make_uint2(0, 0);
+  if (lane < len) mine = a.sorted[j0 + lane];
+  float acc[kSlabs][V] = {};
+  int32_t row = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, 0);
+  bool begun = false;  // the run's first row has ended
+  auto stash = [&](int which) {
 #pragma unroll
-                            for (int q = 0; q < V; ++q) to[col + q] = x[q];
-                          });
+    for (int s = 0; s < kSlabs; ++s)
+#pragma unroll
+      for (int e = 0; e < V; ++e) part[warp][which][(s * 32 + lane) * V + e] = acc[s][e];
+    if (lane == 0) part_key[warp][which] = row;
+  };
+  const TG* grad = a.grad + col0 + lane * V;
+  const int cols = a.dim - col0 - lane * V;  // this lane's slab s exists if s * 32 * V < cols
+  // adds token j's vectors, after the row that ends before it has left
+  auto add = [&](int32_t key, const Vec<TG, V>(&v)[kSlabs]) {
+    if (key != row) {
+      if (!begun) {
+        stash(0);
+      } else if (row < a.n_rows) {
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s)
+          if (s * 32 * V < cols) sum_write<TG, TW, V>(a, row, col0 + (s * 32 + lane) * V, acc[s]);
+      }
+      begun = true;
+      row = key;
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[s][e] = 0.f;
     }
-    return;
-  }
-  const int64_t blocks = gridDim.x - a.n_chunks, block = blockIdx.x - a.n_chunks;
-  __shared__ int32_t row_from[kSumWarps], row_to[kSumWarps];
-  const int64_t r = warp * blocks + block;
-  int32_t s = 0, e = 0;
-  if (r < a.n_rows) {
-    s = a.row_start[r];
-    e = a.row_start[r + 1];
-  }
-  if (lane == 0) {
-    row_from[warp] = s;
-    row_to[warp] = e;
-  }
-  if (r < a.n_rows && e - s <= kSumAlone && !(s == e && a.accumulate)) {
-    const int col = col0 + lane * V;
-    float acc[kSumSlabs][V] = {};
-    sum_tokens<TG, V>(acc, a.pos, s, e, a.grad, a.grad_stride, col, a.dim);
+    if (key < a.n_rows) {
 #pragma unroll
-    for (int q = 0; q < kSumSlabs; ++q)
-      if (col + q * 32 * V < a.dim) sum_write<TG, TW, V>(a, r, col + q * 32 * V, acc[q]);
+      for (int s = 0; s < kSlabs; ++s)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[s][e] += to_f32(v[s].x[e]);
+    }
+  };
+  if constexpr (kRing) {
+    // Each lane copies its own vectors into its warp's ring and reads them
+    // back itself, so no barrier is needed; a token is one group of copies.
+    TG* ring = reinterpret_cast<TG*>(sum_smem + warp * kSumRing) + lane * V;
+    auto fetch = [&](int j) {
+      const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j & 31);
+      const int64_t token = __shfl_sync(0xFFFFFFFFu, mine.y, j & 31);
+      if (j < len && key < a.n_rows) {
+        const TG* g = grad + token * a.grad_stride;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + j % kAhead * kSumCols);
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s)
+          if (s * 32 * V < cols) {
+            if constexpr (V * sizeof(TG) == 16)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + s * 32 * V * (int)sizeof(TG)),
+                           "l"(g + s * 32 * V)
+                           : "memory");
+            else
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + s * 32 * V * (int)sizeof(TG)),
+                           "l"(g + s * 32 * V)
+                           : "memory");
+          }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) fetch(j);
+    for (int j = 0; j < len; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
+      Vec<TG, V> v[kSlabs];
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s)
+        v[s] = *reinterpret_cast<const Vec<TG, V>*>(ring + j % kAhead * kSumCols + s * 32 * V);
+      add(key, v);
+      fetch(j + kAhead);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    for (int j = 0; j < len; j += kAhead) {
+      Vec<TG, V> v[kAhead][kSlabs];
+      int32_t key[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        key[q] = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, (j + q) & 31);
+        const int64_t token = __shfl_sync(0xFFFFFFFFu, mine.y, (j + q) & 31);
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s)
+          if (j + q < len && key[q] < a.n_rows && s * 32 * V < cols)
+            v[q][s].load(grad + token * a.grad_stride + s * 32 * V);
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (j + q < len) add(key[q], v[q]);
+    }
+  }
+  // a run of one row has only the first part, an empty run none (key -1)
+  if (len > 0) stash(begun ? 1 : 0);
+  if (lane == 0) {
+    if (len == 0) part_key[warp][0] = -1;
+    if (!begun) part_key[warp][1] = -1;
   }
   __syncthreads();
+  const int32_t before = c0 > 0 ? (int32_t)a.sorted[c0 - 1].x : -1;
+  const int32_t after = c1 < a.n ? (int32_t)a.sorted[c1].x : -1;
+  constexpr int kPer = kSumCols / (kSumWarps * 32);  // columns of a thread
+  constexpr int kW = V < kPer ? V : kPer;
+  const int c = threadIdx.x * kPer;
+  if (col0 + c >= a.dim) return;
+  float sum[kPer] = {};
+  int32_t cur = part_key[0][0];
+  bool at_start = true;  // cur is the chunk's first row
+  auto emit = [&](bool at_end) {
+    if (cur >= a.n_rows) return;
+    const bool from = at_start && cur == before, on = at_end && cur == after;
+    if (from || on) {
+      float* to = a.partial + (2 * (int64_t)blockIdx.x + (at_start ? 0 : 1)) * a.dim + col0 + c;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (col0 + c + e < a.dim) to[e] = sum[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPer; e += kW)
+        if (col0 + c + e < a.dim) sum_write<TG, TW, kW>(a, cur, col0 + c + e, sum + e);
+    }
+  };
   for (int w = 0; w < kSumWarps; ++w) {
-    const int32_t len = row_to[w] - row_from[w];
-    if (len <= kSumAlone || len > kSumChunk) continue;
-    const int64_t row = w * blocks + block;
-    sum_by_block<TG, V>(smem, a.pos, row_from[w], row_to[w], a.grad, a.grad_stride, col0, a.dim,
-                        [&](int col, const float* x) { sum_write<TG, TW, V>(a, row, col, x); });
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int32_t k = part_key[w][which];
+      if (k < 0) continue;
+      if (k != cur) {
+        emit(false);
+        cur = k;
+        at_start = false;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sum[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) sum[e] += part[w][which][c + e];
+    }
   }
+  emit(true);
 }
 
-// The parts of a long row, joined in order by the block of the chunk that it
-// begins in.
+// The parts of a row that reaches past a chunk, joined in order by the block
+// of the chunk that it begins in. A chunk's part is its second one if the row
+// begins inside it, and its first one otherwise.
 template <class TG, class TW, int V>
 __global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a) {
-  __shared__ float smem[kSumWarps * kSumSlabs * 32 * V];
-  constexpr int kCols = kSumSlabs * 32 * V;
+  constexpr int kPer = kSumCols / 32;
+  __shared__ float part[kSumWarps][kSumCols];
+  __shared__ int64_t n_parts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col0 = (int)blockIdx.y * kCols;
-  const int64_t c = blockIdx.x, c0 = c * kSumChunk;
-  const int32_t r = a.key[min(c0 + kSumChunk, a.n) - 1];
-  if (r >= a.n_rows) return;
-  const int64_t s = a.row_start[r], e = a.row_start[r + 1];
-  if (e - s <= kSumChunk || s < c0) return;
-  const int64_t parts = (e - 1) / kSumChunk - c + 1;
-  const int64_t per = (parts + kSumWarps - 1) / kSumWarps;
+  const int64_t chunk = kSumWarps * a.run;
+  const int64_t c = blockIdx.x, c0 = c * chunk, c1 = c0 + chunk;
+  if (c1 >= a.n) return;
+  const uint32_t r = a.sorted[c1].x;
+  if (r >= a.n_rows || a.sorted[c1 - 1].x != r) return;
+  const bool whole = a.sorted[c0].x == r;
+  if (whole && c0 > 0 && a.sorted[c0 - 1].x == r) return;
+  if (warp == 0) {
+    int64_t k = 1;
+    for (;; k += 32) {
+      const int64_t at = (c + k + lane) * chunk;
+      const unsigned other = __ballot_sync(0xFFFFFFFFu, at >= a.n || a.sorted[min(at, a.n - 1)].x != r);
+      if (other) {
+        k += __ffs(other) - 1;
+        break;
+      }
+    }
+    if (lane == 0) n_parts = k;
+  }
+  __syncthreads();
+  const int64_t parts = n_parts, per = (parts + kSumWarps - 1) / kSumWarps;
   const int64_t p0 = min(warp * per, parts), p1 = min(p0 + per, parts);
-  float acc[kSumSlabs * V] = {};
-#pragma unroll 4
+  const int col0 = (int)blockIdx.y * kSumCols;
+  float acc[kPer] = {};
+#pragma unroll 2
   for (int64_t p = p0; p < p1; ++p) {
-    const float* from = a.partial + (2 * (c + p) + (p == 0 && s > c0 ? 1 : 0)) * a.dim + col0;
+    const float* from = a.partial + (2 * (c + p) + (p == 0 && !whole ? 1 : 0)) * a.dim + col0 + lane;
 #pragma unroll
-    for (int q = 0; q < kSumSlabs * V; ++q)
-      if (col0 + q * 32 + lane < a.dim) acc[q] += __ldcs(from + q * 32 + lane);
+    for (int q = 0; q < kPer; ++q)
+      if (col0 + q * 32 + lane < a.dim) acc[q] += __ldcs(from + q * 32);
   }
 #pragma unroll
-  for (int q = 0; q < kSumSlabs * V; ++q) smem[warp * kCols + q * 32 + lane] = acc[q];
+  for (int q = 0; q < kPer; ++q) part[warp][q * 32 + lane] = acc[q];
   __syncthreads();
-  for (int col = threadIdx.x; col < kCols && col0 + col < a.dim; col += kSumWarps * 32) {
-    float x = smem[col];
+  constexpr int kOut = kSumCols / (kSumWarps * 32), kW = V < kOut ? V : kOut;
+  const int col = threadIdx.x * kOut;
 #pragma unroll
-    for (int w = 1; w < kSumWarps; ++w) x += smem[w * kCols + col];
-    sum_write<TG, TW, 1>(a, r, col0 + col, &x);
+  for (int e = 0; e < kOut; e += kW) {
+    if (col0 + col + e >= a.dim) break;
+    float x[kW];
+#pragma unroll
+    for (int f = 0; f < kW; ++f) {
+      x[f] = part[0][col + e + f];
+#pragma unroll
+      for (int w = 1; w < kSumWarps; ++w) x[f] += part[w][col + e + f];
+    }
+    sum_write<TG, TW, kW>(a, r, col0 + col + e, x);
   }
 }
 
@@ -474,37 +591,46 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
     SortArgs q{};
-    q.ids = d_ids;
-    q.n = n_ids;
-    q.n_rows = n_rows;
-    q.skip_id = skip_id;
+    FillArgs& f = q.fill;
+    f.ids = d_ids;
+    f.n = n_ids;
+    f.n_rows = n_rows;
+    f.skip_id = skip_id;
+    f.out = static_cast<unsigned char*>(d_grad_weight);
+    f.element = (int)type_size(grad_weight_type);
+    f.row_bytes = dim * f.element;
+    f.stride_bytes = grad_weight_stride * f.element;
     q.small = h->d_small;
     int bits = 1;
     while (n_rows >> bits) ++bits;
     q.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
     q.bits = (bits + q.passes - 1) / q.passes;
-    // One CTA sorts a small batch by itself; the cluster's barriers cost more than it saves.
-    const int ctas = n_ids <= 2048 && n_rows <= 8192 ? 1 : kSortCluster;
+    // One CTA sorts a small batch by itself: a cluster's barriers cost more than its threads save.
+    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;
     q.per_warp = (n_ids + ctas * kSortThreads - 1) / (ctas * kSortThreads) * 32;
-    const int64_t n_chunks = (n_ids + kSumChunk - 1) / kSumChunk;
-    const size_t pair = align256((size_t)n_ids * 8), list = align256((size_t)n_ids * 4),
-                 rows = align256((size_t)(n_rows + 1) * 4), parts = align256((size_t)n_chunks * 2 * (size_t)dim * 4);
-    rc = ensure_ws(h, 2 * pair + 2 * list + rows + parts);
+    // Tokens of a warp: as many as kSumMaxRun once that leaves two blocks for every SM.
+    const int64_t groups = (dim + kSumCols - 1) / kSumCols;
+    int run = kSumMaxRun;
+    while (run > 2 && (n_ids / (kSumWarps * run)) * groups < 2 * h->n_sms) run /= 2;
+    const int64_t chunk = kSumWarps * run, n_chunks = (n_ids + chunk - 1) / chunk;
+    const size_t pair = align256((size_t)n_ids * 8), parts = align256((size_t)n_chunks * 2 * (size_t)dim * 4);
+    rc = ensure_ws(h, 2 * pair + parts);
     if (rc) return rc;
     unsigned char* ws = static_cast<unsigned char*>(h->d_ws);
     q.ping[0] = reinterpret_cast<uint2*>(ws);
     q.ping[1] = reinterpret_cast<uint2*>(ws + pair);
-    q.key = reinterpret_cast<int32_t*>(ws + 2 * pair);
-    q.pos = reinterpret_cast<int32_t*>(ws + 2 * pair + list);
-    q.row_start = reinterpret_cast<int32_t*>(ws + 2 * pair + 2 * list);
-    float* partial = reinterpret_cast<float*>(ws + 2 * pair + 2 * list + rows);
-    const size_t smem = ((size_t)(kSortWarps + 3) * (1 << q.bits) + 1 + kSortWarps) * 4;
-    CK(cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    CK(cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    float* partial = reinterpret_cast<float*>(ws + 2 * pair);
+    const size_t smem = ((size_t)(kSortWarps + 2) * (1 << q.bits) + kSortWarps) * 4;
+    static_assert(((kSortWarps + 2) * (1 << kSortMaxBits) + kSortWarps) * 4 >= (int)sizeof(FillSmem));
+    rc = once_per_device(h->device, [] {
+      cudaError_t e = cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           ((kSortWarps + 2) * (1 << kSortMaxBits) + kSortWarps) * 4);
+      return e != cudaSuccess ? e : cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (rc) return rc;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = std::max(smem, sizeof(FillSmem));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -512,32 +638,46 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // Zeros: the clusters that fit beside the sort's, fewer where a CTA would have under 32 KB to write.
+    int64_t fillers = 0;
+    if (!accumulate) {
+      cfg.gridDim = dim3((unsigned)ctas);
+      int fit = 0;
+      CK(cudaOccupancyMaxActiveClusters(&fit, k_emb_sort, &cfg));
+      fillers = std::min<int64_t>(std::max(1, fit - 1), std::max<int64_t>(1, n_rows * f.row_bytes / (32768 * ctas))) * ctas;
+      f.row_step = std::min<int64_t>(kFillRows, (n_rows + fillers - 1) / fillers);
+    }
+    cfg.gridDim = dim3((unsigned)(ctas + fillers));
     CK(cudaLaunchKernelEx(&cfg, k_emb_sort, q));
+    if (n_ids == 0) return BPE_OK;
     return with_type(grad_out_type, [&](auto g_) {
       return with_type(grad_weight_type, [&](auto w) -> int {
         using TG = decltype(g_);
         using TW = decltype(w);
-        const SumArgs<TG, TW> a{q.key, q.pos, q.row_start, n_ids, n_rows, static_cast<const TG*>(d_grad_out),
-                                grad_out_stride, scale, (int)dim, static_cast<TW*>(d_grad_weight),
-                                grad_weight_stride, accumulate, partial, n_chunks};
+        const SumArgs<TG, TW> a{q.ping[(q.passes - 1) & 1], n_ids, n_rows, static_cast<const TG*>(d_grad_out),
+                                grad_out_stride, scale, (int)dim, run, static_cast<TW*>(d_grad_weight),
+                                grad_weight_stride, accumulate, partial};
         auto launch = [&](auto width) {
           constexpr int V = decltype(width)::value;
-          const unsigned groups = (unsigned)((dim + kSumSlabs * 32 * V - 1) / (kSumSlabs * 32 * V));
-          k_emb_sum<TG, TW, V><<<dim3((unsigned)(n_chunks + (n_rows + kSumWarps - 1) / kSumWarps), groups),
-                                 kSumWarps * 32, 0, st>>>(a);
-          if (n_ids > kSumChunk)
-            k_emb_join<TG, TW, V><<<dim3((unsigned)n_chunks, groups), kSumWarps * 32, 0, st>>>(a);
+          const dim3 grid((unsigned)n_chunks, (unsigned)groups);
+          constexpr int kSmem = V * sizeof(TG) >= 4 ? kSumWarps * kSumRing : 0;
+          int rc = once_per_device(h->device, [] {
+            return cudaFuncSetAttribute(k_emb_sum<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+          });
+          if (rc) return rc;
+          k_emb_sum<TG, TW, V><<<grid, kSumWarps * 32, kSmem, st>>>(a);
+          if (n_chunks > 1) k_emb_join<TG, TW, V><<<grid, kSumWarps * 32, 0, st>>>(a);
+          CK(cudaGetLastError());
+          return (int)BPE_OK;
         };
         auto fits = [&](int64_t V) {
           return dim % V == 0 && vec_ok(d_grad_out, grad_out_stride, sizeof(TG), V) &&
                  vec_ok(d_grad_weight, grad_weight_stride, sizeof(TW), V);
         };
         constexpr int kWide = 16 / (int)sizeof(TG), kNarrow = 4 / (int)sizeof(TG);
-        if (dim > 32 * kNarrow && fits(kWide)) launch(std::integral_constant<int, kWide>{});
-        else if (fits(kNarrow)) launch(std::integral_constant<int, kNarrow>{});
-        else launch(std::integral_constant<int, 1>{});
-        CK(cudaGetLastError());
-        return BPE_OK;
+        if (fits(kWide)) return launch(std::integral_constant<int, kWide>{});
+        if (fits(kNarrow)) return launch(std::integral_constant<int, kNarrow>{});
+        return launch(std::integral_constant<int, 1>{});
       });
     });
   });

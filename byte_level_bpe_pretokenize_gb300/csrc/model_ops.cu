@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "handle.cuh"
 
@@ -49,6 +50,18 @@ int with_type(int type, F f) {
   if (type == BPE_F32) return f(float{});
   if (type == BPE_F16) return f(__half{});
   return f(__nv_bfloat16{});
+}
+
+// Runs f (kernel attributes, which last as long as the process) once per device
+// for each place that calls this; the caller has the device current. Racing
+// first calls both run it.
+template <class F>
+int once_per_device(int device, F f) {
+  static std::atomic<bool> done[64];
+  if (device < 64 && done[device].load(std::memory_order_acquire)) return BPE_OK;
+  CK(f());
+  if (device < 64) done[device].store(true, std::memory_order_release);
+  return BPE_OK;
 }
 
 // No exception (an allocation for an error message, say) leaves a C entry.
