@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kEmbThreads) k_embed(const int32_t* ids, int64
   }
 }
 
-// ------------------------------------------------------- sort and zero rows --
+// ------------------------------------------------------- zero rows and sort --
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -67,6 +67,7 @@ constexpr int kSortCluster = 16;
 constexpr int kSortBatch = 4;     // tokens that a lane holds
 constexpr int kFillRows = 2048;   // rows a CTA marks at once
 constexpr int kFillPage = 16384;  // bytes of a bulk store
+constexpr int kFillThreads = 512;
 
 // Rows [r0, r1) without a token become zeros: the CTA reads every id and marks
 // the rows that are met; then each thread takes a row and stores its 16-byte
@@ -123,7 +124,7 @@ __device__ void fill_absent(const FillArgs& a, int64_t r0, int64_t r1, FillSmem&
     for (unsigned char* at = to; at < end; at += a.element) element(at);
   }
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the page is read; the grid's end completes the writes
   __syncthreads();
 }
 
@@ -133,19 +134,28 @@ __device__ __forceinline__ void fill_rows(const FillArgs& a, int64_t who, int64_
     fill_absent(a, r, min(r + a.row_step, a.n_rows), sm);
 }
 
+// Runs on the SMs that the sort leaves free: the zeros are most of what a
+// gradient writes, and need only the ids.
+__global__ void __launch_bounds__(kFillThreads) k_emb_fill(FillArgs a) {
+  __shared__ FillSmem sm;
+  let_next_begin();
+  fill_rows(a, blockIdx.x, gridDim.x, sm);
+  await_previous();
+}
+
 struct SortArgs {
-  FillArgs fill;
+  const int32_t* ids;
+  int64_t n, n_rows;
+  int32_t skip_id;
   int passes, bits;    // passes of `bits` bits each, lowest first
   int64_t per_warp;    // tokens of a warp, a multiple of 32
   uint2* ping[2];      // (key, token); the last pass p writes ping[p & 1]
   DevSmall* small;
 };
 
-// The first cluster sorts the tokens by row, equal rows in token order: a
-// counting sort by `bits` bits a pass. Tokens without a row (skip_id, and ids
-// out of range, which are reported) get the key n_rows and sort last. The
-// other clusters meanwhile zero the rows without a token: the sort needs few
-// SMs and the zeros are most of what is written.
+// Tokens sorted by row, equal rows in token order: a counting sort by `bits`
+// bits a pass, by the CTAs of one cluster. Tokens without a row (skip_id, and
+// ids out of range, which are reported) get the key n_rows and sort last.
 //
 // A pass: each warp counts the digits of its run of tokens in its own bins;
 // the bins' prefix over warps, over the cluster's CTAs (read through
@@ -156,11 +166,8 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
   extern __shared__ __align__(16) int32_t sort_smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int n_ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  if (blockIdx.x >= n_ctas) {
-    fill_rows(a.fill, blockIdx.x - n_ctas, gridDim.x - n_ctas, *reinterpret_cast<FillSmem*>(sort_smem));
-    return;
-  }
-  const int64_t n = a.fill.n, n_rows = a.fill.n_rows;
+  const int64_t n = a.n, n_rows = a.n_rows;
+  let_next_begin();
   const int bins = 1 << a.bits;
   int32_t* hist = sort_smem;                  // [kSortWarps][bins]
   int32_t* total = hist + kSortWarps * bins;  // [bins]: of this CTA
@@ -184,9 +191,9 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
         if (p > 0) {
           t[q] = __ldcg(from + i);
         } else {
-          const int32_t id = __ldg(a.fill.ids + i);
-          const bool ok = id != a.fill.skip_id && emb_row_ok(id, n_rows);
-          if (!ok && id != a.fill.skip_id) atomicOr(&a.small->op_status, kStBadInput);
+          const int32_t id = __ldg(a.ids + i);
+          const bool ok = id != a.skip_id && emb_row_ok(id, n_rows);
+          if (!ok && id != a.skip_id) atomicOr(&a.small->op_status, kStBadInput);
           t[q] = make_uint2(ok ? (uint32_t)id : (uint32_t)n_rows, (uint32_t)i);
         }
       }
@@ -266,6 +273,8 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
 constexpr int kSumWarps = 8;
 constexpr int kSumCols = 512;     // columns of a block
 constexpr int kSumMaxRun = 16;    // tokens of a warp, at most
+constexpr int kSmallTokens = 512; // most tokens of the single launch
+constexpr int64_t kSmallRows = (1ll << 32) / kSmallTokens - 1;  // and rows: a key and a token fit 32 bits
 constexpr int kSumRing = 8192;    // bytes of a warp's tokens in flight
 
 template <class TG, class TW>
@@ -295,6 +304,22 @@ __device__ __forceinline__ void sum_write(const SumArgs<TG, TW>& a, int64_t r, i
   v.store(o);
 }
 
+// acc += v: two 32-bit sums an instruction where V is even.
+template <class T, int V>
+__device__ __forceinline__ void add_vec(float (&acc)[V], const Vec<T, V>& v) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2)
+      asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+          "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+          : "+f"(acc[e]), "+f"(acc[e + 1])
+          : "f"(to_f32(v.x[e])), "f"(to_f32(v.x[e + 1])));
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] += to_f32(v.x[e]);
+  }
+}
+
 // A block sums kSumCols columns of a chunk of kSumWarps runs of sorted tokens;
 // a warp its run, a lane V adjacent columns in each of kSlabs slabs. Every warp
 // has the same number of tokens, however they are spread over the rows:
@@ -305,75 +330,75 @@ __device__ __forceinline__ void sum_write(const SumArgs<TG, TW>& a, int64_t r, i
 //   * what the chunk adds to a row that reaches past it goes to `partial`,
 //     which k_emb_join adds up in order.
 template <class TG, class TW, int V>
-__global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
+__device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2* sorted, unsigned char* sum_smem) {
   constexpr int kSlabs = kSumCols / (32 * V);
   constexpr bool kRing = V * sizeof(TG) >= 4;  // an asynchronous copy moves 4 bytes at least
   constexpr int kAhead = kRing ? kSumRing / (kSumCols * (int)sizeof(TG)) : 2;  // tokens in flight
-  extern __shared__ __align__(16) unsigned char sum_smem[];
-  __shared__ float part[kSumWarps][2][kSumCols];
+  __shared__ __align__(16) float part[kSumWarps][2][kSumCols];
   __shared__ int32_t part_key[kSumWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c0 = (int64_t)blockIdx.x * kSumWarps * a.run, c1 = min(c0 + kSumWarps * a.run, a.n);
   const int col0 = (int)blockIdx.y * kSumCols;
   const int64_t j0 = min(c0 + warp * a.run, c1);
-  const int len = (int)min((int64_t)a.run, c1 - j0);
-  uint2 mine = make_uint2(0, 0);
-  if (lane < len) mine = a.sorted[j0 + lane];
+  uint2 mine = make_uint2(0xFFFFFFFFu, 0);
+  if (lane < min((int64_t)a.run, c1 - j0)) mine = sorted[j0 + lane];
+  const int32_t before = c0 > 0 ? (int32_t)sorted[c0 - 1].x : -1;
+  const int32_t after = c1 < a.n ? (int32_t)sorted[c1].x : -1;
+  // tokens without a row are the last ones
+  const int len = __popc(__ballot_sync(0xFFFFFFFFu, mine.x < (uint32_t)a.n_rows));
   float acc[kSlabs][V] = {};
   int32_t row = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, 0);
   bool begun = false;  // the run's first row has ended
   auto stash = [&](int which) {
 #pragma unroll
-    for (int s = 0; s < kSlabs; ++s)
+    for (int s = 0; s < kSlabs; ++s) {
+      float* to = &part[warp][which][(s * 32 + lane) * V];
+      if constexpr (V >= 4) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) part[warp][which][(s * 32 + lane) * V + e] = acc[s][e];
+        for (int e = 0; e < V; e += 4)
+          *reinterpret_cast<float4*>(to + e) = make_float4(acc[s][e], acc[s][e + 1], acc[s][e + 2], acc[s][e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[e] = acc[s][e];
+      }
+    }
     if (lane == 0) part_key[warp][which] = row;
   };
   const TG* grad = a.grad + col0 + lane * V;
   const int cols = a.dim - col0 - lane * V;  // this lane's slab s exists if s * 32 * V < cols
-  // adds token j's vectors, after the row that ends before it has left
-  auto add = [&](int32_t key, const Vec<TG, V>(&v)[kSlabs]) {
-    if (key != row) {
-      if (!begun) {
-        stash(0);
-      } else if (row < a.n_rows) {
-#pragma unroll
-        for (int s = 0; s < kSlabs; ++s)
-          if (s * 32 * V < cols) sum_write<TG, TW, V>(a, row, col0 + (s * 32 + lane) * V, acc[s]);
-      }
-      begun = true;
-      row = key;
+  // the row that ended leaves, and `key` begins
+  auto next_row = [&](int32_t key) {
+    if (!begun) {
+      stash(0);
+    } else {
 #pragma unroll
       for (int s = 0; s < kSlabs; ++s)
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[s][e] = 0.f;
+        if (s * 32 * V < cols) sum_write<TG, TW, V>(a, row, col0 + (s * 32 + lane) * V, acc[s]);
     }
-    if (key < a.n_rows) {
+    begun = true;
+    row = key;
 #pragma unroll
-      for (int s = 0; s < kSlabs; ++s)
+    for (int s = 0; s < kSlabs; ++s)
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[s][e] += to_f32(v[s].x[e]);
-    }
+      for (int e = 0; e < V; ++e) acc[s][e] = 0.f;
   };
   if constexpr (kRing) {
     // Each lane copies its own vectors into its warp's ring and reads them
     // back itself, so no barrier is needed; a token is one group of copies.
-    TG* ring = reinterpret_cast<TG*>(sum_smem + warp * kSumRing) + lane * V;
-    auto fetch = [&](int j) {
-      const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j & 31);
-      const int64_t token = __shfl_sync(0xFFFFFFFFu, mine.y, j & 31);
-      if (j < len && key < a.n_rows) {
-        const TG* g = grad + token * a.grad_stride;
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + j % kAhead * kSumCols);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * kSumRing + lane * V * (int)sizeof(TG);
+    constexpr uint32_t kSlot = kSumCols * sizeof(TG), kStep = 32 * V * sizeof(TG);
+    auto fetch = [&](int j, uint32_t slot) {
+      if (j < len) {
+        const TG* g = grad + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j) * a.grad_stride;
 #pragma unroll
         for (int s = 0; s < kSlabs; ++s)
           if (s * 32 * V < cols) {
             if constexpr (V * sizeof(TG) == 16)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + s * 32 * V * (int)sizeof(TG)),
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + slot + s * kStep),
                            "l"(g + s * 32 * V)
                            : "memory");
             else
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + s * 32 * V * (int)sizeof(TG)),
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ring + slot + s * kStep),
                            "l"(g + s * 32 * V)
                            : "memory");
           }
@@ -381,34 +406,40 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j);
+    for (int j = 0; j < kAhead; ++j) fetch(j, j * kSlot);
+    uint32_t slot = 0;
     for (int j = 0; j < len; ++j) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
       const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
       Vec<TG, V> v[kSlabs];
 #pragma unroll
       for (int s = 0; s < kSlabs; ++s)
-        v[s] = *reinterpret_cast<const Vec<TG, V>*>(ring + j % kAhead * kSumCols + s * 32 * V);
-      add(key, v);
-      fetch(j + kAhead);
+        v[s] = *reinterpret_cast<const Vec<TG, V>*>(__cvta_shared_to_generic(ring + slot + s * kStep));
+      if (key != row) next_row(key);
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s) add_vec<TG, V>(acc[s], v[s]);
+      fetch(j + kAhead, slot);
+      slot = slot + kSlot == kAhead * kSlot ? 0 : slot + kSlot;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     for (int j = 0; j < len; j += kAhead) {
       Vec<TG, V> v[kAhead][kSlabs];
-      int32_t key[kAhead];
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
-        key[q] = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, (j + q) & 31);
         const int64_t token = __shfl_sync(0xFFFFFFFFu, mine.y, (j + q) & 31);
 #pragma unroll
         for (int s = 0; s < kSlabs; ++s)
-          if (j + q < len && key[q] < a.n_rows && s * 32 * V < cols)
-            v[q][s].load(grad + token * a.grad_stride + s * 32 * V);
+          if (j + q < len && s * 32 * V < cols) v[q][s].load(grad + token * a.grad_stride + s * 32 * V);
       }
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-        if (j + q < len) add(key[q], v[q]);
+      for (int q = 0; q < kAhead; ++q) {
+        if (j + q >= len) break;
+        const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, (j + q) & 31);
+        if (key != row) next_row(key);
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s) add_vec<TG, V>(acc[s], v[q][s]);
+      }
     }
   }
   // a run of one row has only the first part, an empty run none (key -1)
@@ -418,17 +449,14 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
     if (!begun) part_key[warp][1] = -1;
   }
   __syncthreads();
-  const int32_t before = c0 > 0 ? (int32_t)a.sorted[c0 - 1].x : -1;
-  const int32_t after = c1 < a.n ? (int32_t)a.sorted[c1].x : -1;
   constexpr int kPer = kSumCols / (kSumWarps * 32);  // columns of a thread
   constexpr int kW = V < kPer ? V : kPer;
   const int c = threadIdx.x * kPer;
-  if (col0 + c >= a.dim) return;
-  float sum[kPer] = {};
   int32_t cur = part_key[0][0];
+  if (col0 + c >= a.dim || cur < 0) return;
+  float sum[kPer] = {};
   bool at_start = true;  // cur is the chunk's first row
   auto emit = [&](bool at_end) {
-    if (cur >= a.n_rows) return;
     const bool from = at_start && cur == before, on = at_end && cur == after;
     if (from || on) {
       float* to = a.partial + (2 * (int64_t)blockIdx.x + (at_start ? 0 : 1)) * a.dim + col0 + c;
@@ -460,45 +488,96 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
   emit(true);
 }
 
-// The parts of a row that reaches past a chunk, joined in order by the block
-// of the chunk that it begins in. A chunk's part is its second one if the row
-// begins inside it, and its first one otherwise.
 template <class TG, class TW, int V>
-__global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a) {
-  constexpr int kPer = kSumCols / 32;
-  __shared__ float part[kSumWarps][kSumCols];
-  __shared__ int64_t n_parts;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t chunk = kSumWarps * a.run;
-  const int64_t c = blockIdx.x, c0 = c * chunk, c1 = c0 + chunk;
-  if (c1 >= a.n) return;
-  const uint32_t r = a.sorted[c1].x;
-  if (r >= a.n_rows || a.sorted[c1 - 1].x != r) return;
-  const bool whole = a.sorted[c0].x == r;
-  if (whole && c0 > 0 && a.sorted[c0 - 1].x == r) return;
-  if (warp == 0) {
-    int64_t k = 1;
-    for (;; k += 32) {
-      const int64_t at = (c + k + lane) * chunk;
-      const unsigned other = __ballot_sync(0xFFFFFFFFu, at >= a.n || a.sorted[min(at, a.n - 1)].x != r);
-      if (other) {
-        k += __ffs(other) - 1;
-        break;
-      }
+__global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
+  extern __shared__ __align__(16) unsigned char sum_smem[];
+  await_previous();
+  let_next_begin();
+  sum_chunk<TG, TW, V>(a, a.sorted, sum_smem);
+}
+
+// Up to kSmallTokens tokens in one launch: blocks [0, chunks) rank the tokens
+// by comparing each with every other, all of them in each block, which is
+// sooner done than another kernel is begun, and sum their chunk; the others
+// zero rows without a token.
+template <class TG, class TW, int V>
+__global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a, FillArgs f, uint2* sorted_out,
+                                                              int64_t n_chunks, DevSmall* small) {
+  extern __shared__ __align__(16) unsigned char sum_smem[];
+  __shared__ uint2 sorted[kSmallTokens];
+  __shared__ __align__(16) uint32_t key[kSmallTokens];
+  let_next_begin();
+  if (blockIdx.x >= n_chunks) {
+    if (blockIdx.y == 0) fill_rows(f, blockIdx.x - n_chunks, gridDim.x - n_chunks, *reinterpret_cast<FillSmem*>(sum_smem));
+    return;
+  }
+  // key * kSmallTokens + token: distinct, and in sorted order
+  const int n = (int)a.n, tid = threadIdx.x;
+  for (int i = tid; i < kSmallTokens; i += kSumWarps * 32) {
+    uint32_t k = 0xFFFFFFFFu;
+    if (i < n) {
+      const int32_t id = __ldg(f.ids + i);
+      const bool ok = id != f.skip_id && emb_row_ok(id, a.n_rows);
+      if (!ok && id != f.skip_id && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(&small->op_status, kStBadInput);
+      k = (ok ? (uint32_t)id : (uint32_t)a.n_rows) * kSmallTokens + i;
     }
-    if (lane == 0) n_parts = k;
+    key[i] = k;
   }
   __syncthreads();
-  const int64_t parts = n_parts, per = (parts + kSumWarps - 1) / kSumWarps;
+  const int64_t c0 = (int64_t)blockIdx.x * kSumWarps * a.run, c1 = c0 + kSumWarps * a.run;
+  for (int i = tid; i < n; i += kSumWarps * 32) {
+    const uint32_t k = key[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(key + j);
+      rank += (o.x < k) + (o.y < k) + (o.z < k) + (o.w < k);
+    }
+    const uint2 t = make_uint2(k / kSmallTokens, (uint32_t)i);
+    sorted[rank] = t;
+    if (rank >= c0 && rank < c1 && blockIdx.y == 0) sorted_out[rank] = t;
+  }
+  __syncthreads();
+  sum_chunk<TG, TW, V>(a, sorted, sum_smem);
+}
+
+// The parts of a row that reaches past a chunk, joined in order by the block
+// of the chunk that it begins in. A chunk's part is its second one if the row
+// begins inside it, and its first one otherwise. early: the sorted tokens are
+// older than the kernel before, so they are read before it ends.
+template <class TG, class TW, int V>
+__global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a, bool early) {
+  constexpr int kPer = kSumCols / 32;
+  __shared__ float part[kSumWarps][kSumCols];
+  if (!early) await_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t chunk = kSumWarps * a.run;
+  const int64_t c = blockIdx.x, c0 = c * chunk, c1 = min(c0 + chunk, a.n);
+  const uint32_t r = a.sorted[c1 - 1].x, first = a.sorted[c0].x;
+  const uint32_t before = c0 > 0 ? a.sorted[c0 - 1].x : 0xFFFFFFFFu;
+  const bool whole = first == r;
+  // chunks after this one that begin with r
+  int64_t parts = 1;
+  for (;; parts += 32) {
+    const int64_t at = (c + parts + lane) * chunk;
+    const unsigned other = __ballot_sync(0xFFFFFFFFu, at >= a.n || a.sorted[min(at, a.n - 1)].x != r);
+    if (other) {
+      parts += __ffs(other) - 1;
+      break;
+    }
+  }
+  if (early) await_previous();
+  if (parts == 1 || r >= a.n_rows || (whole && before == r)) return;
+  const int64_t per = (parts + kSumWarps - 1) / kSumWarps;
   const int64_t p0 = min(warp * per, parts), p1 = min(p0 + per, parts);
   const int col0 = (int)blockIdx.y * kSumCols;
   float acc[kPer] = {};
-#pragma unroll 2
+#pragma unroll 4
   for (int64_t p = p0; p < p1; ++p) {
     const float* from = a.partial + (2 * (c + p) + (p == 0 && !whole ? 1 : 0)) * a.dim + col0 + lane;
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
-      if (col0 + q * 32 + lane < a.dim) acc[q] += __ldcs(from + q * 32);
+      if (col0 + q * 32 + lane < a.dim) acc[q] += __ldcg(from + q * 32);
   }
 #pragma unroll
   for (int q = 0; q < kPer; ++q) part[warp][q * 32 + lane] = acc[q];
@@ -590,24 +669,6 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     if (n_rows == 0 || dim == 0) return BPE_OK;
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
-    SortArgs q{};
-    FillArgs& f = q.fill;
-    f.ids = d_ids;
-    f.n = n_ids;
-    f.n_rows = n_rows;
-    f.skip_id = skip_id;
-    f.out = static_cast<unsigned char*>(d_grad_weight);
-    f.element = (int)type_size(grad_weight_type);
-    f.row_bytes = dim * f.element;
-    f.stride_bytes = grad_weight_stride * f.element;
-    q.small = h->d_small;
-    int bits = 1;
-    while (n_rows >> bits) ++bits;
-    q.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
-    q.bits = (bits + q.passes - 1) / q.passes;
-    // One CTA sorts a small batch by itself: a cluster's barriers cost more than its threads save.
-    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;
-    q.per_warp = (n_ids + ctas * kSortThreads - 1) / (ctas * kSortThreads) * 32;
     // Tokens of a warp: as many as kSumMaxRun once that leaves two blocks for every SM.
     const int64_t groups = (dim + kSumCols - 1) / kSumCols;
     int run = kSumMaxRun;
@@ -617,57 +678,90 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     rc = ensure_ws(h, 2 * pair + parts);
     if (rc) return rc;
     unsigned char* ws = static_cast<unsigned char*>(h->d_ws);
-    q.ping[0] = reinterpret_cast<uint2*>(ws);
-    q.ping[1] = reinterpret_cast<uint2*>(ws + pair);
+    uint2* const ping[2] = {reinterpret_cast<uint2*>(ws), reinterpret_cast<uint2*>(ws + pair)};
     float* partial = reinterpret_cast<float*>(ws + 2 * pair);
-    const size_t smem = ((size_t)(kSortWarps + 2) * (1 << q.bits) + kSortWarps) * 4;
-    static_assert(((kSortWarps + 2) * (1 << kSortMaxBits) + kSortWarps) * 4 >= (int)sizeof(FillSmem));
-    rc = once_per_device(h->device, [] {
-      cudaError_t e = cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           ((kSortWarps + 2) * (1 << kSortMaxBits) + kSortWarps) * 4);
-      return e != cudaSuccess ? e : cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    });
-    if (rc) return rc;
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = std::max(smem, sizeof(FillSmem));
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    // Zeros: the clusters that fit beside the sort's, fewer where a CTA would have under 32 KB to write.
+    FillArgs f{};
+    f.ids = d_ids;
+    f.n = n_ids;
+    f.n_rows = n_rows;
+    f.skip_id = skip_id;
+    f.out = static_cast<unsigned char*>(d_grad_weight);
+    f.element = (int)type_size(grad_weight_type);
+    f.row_bytes = dim * f.element;
+    f.stride_bytes = grad_weight_stride * f.element;
+    const bool small = n_ids <= kSmallTokens && n_rows < kSmallRows;
+    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of the sort: a cluster's barriers cost more than a few tokens gain
     int64_t fillers = 0;
     if (!accumulate) {
-      cfg.gridDim = dim3((unsigned)ctas);
-      int fit = 0;
-      CK(cudaOccupancyMaxActiveClusters(&fit, k_emb_sort, &cfg));
-      fillers = std::min<int64_t>(std::max(1, fit - 1), std::max<int64_t>(1, n_rows * f.row_bytes / (32768 * ctas))) * ctas;
+      // the SMs beside the sort, fewer where each would have under 32 KB to write
+      fillers = std::min<int64_t>(small ? h->n_sms : h->n_sms - ctas, std::max<int64_t>(1, n_rows * f.row_bytes / 32768));
       f.row_step = std::min<int64_t>(kFillRows, (n_rows + fillers - 1) / fillers);
     }
-    cfg.gridDim = dim3((unsigned)(ctas + fillers));
-    CK(cudaLaunchKernelEx(&cfg, k_emb_sort, q));
-    if (n_ids == 0) return BPE_OK;
+    int passes = 1;
+    if (!small) {
+      SortArgs q{};
+      q.ids = d_ids;
+      q.n = n_ids;
+      q.n_rows = n_rows;
+      q.skip_id = skip_id;
+      int bits = 1;
+      while (n_rows >> bits) ++bits;
+      passes = q.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
+      q.bits = (bits + q.passes - 1) / q.passes;
+      q.per_warp = (n_ids + ctas * kSortThreads - 1) / (ctas * kSortThreads) * 32;
+      q.ping[0] = ping[0];
+      q.ping[1] = ping[1];
+      q.small = h->d_small;
+      rc = once_per_device(h->device, [] {
+        cudaError_t e = cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             ((kSortWarps + 2) * (1 << kSortMaxBits) + kSortWarps) * 4);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(k_emb_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      });
+      if (rc) return rc;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)ctas);
+      cfg.blockDim = dim3(kSortThreads);
+      cfg.dynamicSmemBytes = ((size_t)(kSortWarps + 2) * (1 << q.bits) + kSortWarps) * 4;
+      cfg.stream = st;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)ctas;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      CK(cudaLaunchKernelEx(&cfg, k_emb_sort, q));
+      if (fillers) CK(launch_after(k_emb_fill, dim3((unsigned)fillers), kFillThreads, 0, st, f));
+    }
+    if (n_chunks + fillers == 0) return BPE_OK;
     return with_type(grad_out_type, [&](auto g_) {
       return with_type(grad_weight_type, [&](auto w) -> int {
         using TG = decltype(g_);
         using TW = decltype(w);
-        const SumArgs<TG, TW> a{q.ping[(q.passes - 1) & 1], n_ids, n_rows, static_cast<const TG*>(d_grad_out),
+        const SumArgs<TG, TW> a{ping[(passes - 1) & 1], n_ids, n_rows, static_cast<const TG*>(d_grad_out),
                                 grad_out_stride, scale, (int)dim, run, static_cast<TW*>(d_grad_weight),
                                 grad_weight_stride, accumulate, partial};
         auto launch = [&](auto width) {
           constexpr int V = decltype(width)::value;
-          const dim3 grid((unsigned)n_chunks, (unsigned)groups);
-          constexpr int kSmem = V * sizeof(TG) >= 4 ? kSumWarps * kSumRing : 0;
-          int rc = once_per_device(h->device, [] {
-            return cudaFuncSetAttribute(k_emb_sum<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+          constexpr size_t kSmem = V * sizeof(TG) >= 4 ? kSumWarps * kSumRing : 0;
+          constexpr size_t kSmallSmem = std::max(kSmem, sizeof(FillSmem));
+          int rc = once_per_device(h->device, [=] {
+            cudaError_t e = cudaFuncSetAttribute(k_emb_sum<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)kSmem);
+            return e != cudaSuccess ? e
+                                    : cudaFuncSetAttribute(k_emb_small<TG, TW, V>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
           });
           if (rc) return rc;
-          k_emb_sum<TG, TW, V><<<grid, kSumWarps * 32, kSmem, st>>>(a);
-          if (n_chunks > 1) k_emb_join<TG, TW, V><<<grid, kSumWarps * 32, 0, st>>>(a);
-          CK(cudaGetLastError());
+          const dim3 grid((unsigned)n_chunks, (unsigned)groups);
+          if (small) {
+            k_emb_small<TG, TW, V><<<dim3((unsigned)(n_chunks + fillers), (unsigned)groups), kSumWarps * 32, kSmallSmem,
+                                     st>>>(a, f, ping[0], n_chunks, h->d_small);
+            CK(cudaGetLastError());
+          } else {
+            CK(launch_after(k_emb_sum<TG, TW, V>, grid, kSumWarps * 32, kSmem, st, a));
+          }
+          if (n_chunks > 1) CK(launch_after(k_emb_join<TG, TW, V>, grid, kSumWarps * 32, 0, st, a, !small));
           return (int)BPE_OK;
         };
         auto fits = [&](int64_t V) {

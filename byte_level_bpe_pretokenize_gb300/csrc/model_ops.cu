@@ -64,6 +64,29 @@ int once_per_device(int device, F f) {
   return BPE_OK;
 }
 
+// Programmatic dependent launch. A kernel launched by launch_after may begin
+// once every block of the kernel before it has called let_next_begin or ended;
+// what it does before await_previous must not depend on that kernel. Each
+// kernel of such a chain awaits the one before it, so the end of the last one
+// is the end of all; the first is an ordinary launch.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // No exception (an allocation for an error message, say) leaves a C entry.
 template <class F>
 int guarded(const char* what, F f) noexcept {
