@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import subprocess
 import threading
 
@@ -337,6 +338,7 @@ class Tokenizer:
 
     def __init__(self, merges, vocab_bytes, vocab_offsets, device: int = 0):
         self.device = device
+        self._lib = lib()
         self.handle = bpe_build(merges, vocab_bytes, vocab_offsets, device)
 
     def close(self):
@@ -385,19 +387,24 @@ class Tokenizer:
 
 
     # ---- what surrounds the model ----
+    # These calls take microseconds on the GPU, so their checks ask each tensor
+    # for as little as they can; _refuse finds the words for what failed.
 
-    def _checked(self, name, t, dtypes, dims=None):
-        if t.device.type != "cuda" or t.device.index != self.device:
+    def _refuse(self, name, t, dtypes, dims=None, size=None):
+        if t.get_device() != self.device:
             raise ValueError(f"{name}: on {t.device}, the tokenizer is on cuda:{self.device}")
         if t.dtype not in dtypes:
-            raise ValueError(f"{name}: {t.dtype}, need one of {', '.join(str(d) for d in dtypes)}")
+            raise ValueError(f"{name}: {t.dtype}, need {' or '.join(str(d) for d in dtypes)}")
         if dims is not None and t.dim() != dims:
             raise ValueError(f"{name}: {t.dim()} dimensions, need {dims}")
+        raise ValueError(f"{name}: needs {'adjacent elements' if size is None else f'{size} adjacent elements'}")
 
-    def _ids(self, ids):
-        import torch
-        self._checked("ids", ids, (torch.int32,))
-        return ids if ids.is_contiguous() else ids.contiguous()
+    def _flat(self, name, t, dtype, size=None):
+        """The address of a one-dimensional tensor without gaps."""
+        if (t.get_device() != self.device or t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous()
+                or (size is not None and t.numel() != size)):
+            self._refuse(name, t, (dtype,), 1, size)
+        return t.data_ptr()
 
     def plan_blocks(self, offsets, cached, table, free, block_size: int, n_slots: int | None = None, head=None):
         """Block tables, cache slots and positions for the next step of a
@@ -410,30 +417,32 @@ class Tokenizer:
         Returns (seq_lens int32[n], slots int64[n_slots], positions
         int32[n_slots], info int64[2]: head after the call, blocks lacking)."""
         import torch
-        self._checked("table", table, (torch.int32,), 2)
-        n = table.shape[0]
-        for name, t, dtype, size in (("offsets", offsets, torch.int64, n + 1), ("cached", cached, torch.int32, n),
-                                     ("free", free, torch.int32, None), ("head", head, torch.int64, 1)):
-            if t is not None:
-                self._checked(name, t, (dtype,), 1)
-                if (size is not None and t.shape[0] != size) or not t.is_contiguous():
-                    raise ValueError(f"{name}: needs {size} adjacent elements, one row of the table each")
-        if table.shape[1] > 1 and table.stride(1) != 1:
+        i32, i64 = torch.int32, torch.int64
+        if table.get_device() != self.device or table.dtype is not i32 or table.dim() != 2:
+            self._refuse("table", table, (i32,), 2)
+        n, width = table.shape
+        stride, step = table.stride()
+        if step != 1 and width > 1:
             raise ValueError("table: the elements of a row must be adjacent")
         if n_slots is None:
             if offsets is not None:
                 raise ValueError("n_slots: the number of new tokens (or more) is needed with offsets")
             n_slots = n
+        p_offsets = None if offsets is None else self._flat("offsets", offsets, i64, n + 1)
+        p_cached = None if cached is None else self._flat("cached", cached, i32, n)
+        p_free = self._flat("free", free, i32)
+        p_head = None if head is None else self._flat("head", head, i64, 1)
         dev = table.device
-        seq_lens = torch.empty(n, dtype=torch.int32, device=dev)
-        slots = torch.empty(n_slots, dtype=torch.int64, device=dev)
-        positions = torch.empty(n_slots, dtype=torch.int32, device=dev)
-        info = torch.empty(2, dtype=torch.int64, device=dev)
-        bpe_plan_blocks(self.handle, None if offsets is None else offsets.data_ptr(),
-                        None if cached is None else cached.data_ptr(), n, block_size, free.data_ptr(), free.shape[0],
-                        None if head is None else head.data_ptr(), table.data_ptr(), table.shape[1], table.stride(0),
-                        seq_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), n_slots, info.data_ptr(),
-                        self._stream())
+        seq_lens = torch.empty(n, dtype=i32, device=dev)
+        slots = torch.empty(n_slots, dtype=i64, device=dev)
+        positions = torch.empty(n_slots, dtype=i32, device=dev)
+        info = torch.empty(2, dtype=i64, device=dev)
+        rc = self._lib.bpe_plan_blocks(self.handle, p_offsets, p_cached, n, block_size, p_free, free.numel(), p_head,
+                                       table.data_ptr(), width, stride, seq_lens.data_ptr(), slots.data_ptr(),
+                                       positions.data_ptr(), n_slots, info.data_ptr(),
+                                       torch._C._cuda_getCurrentRawStream(self.device))
+        if rc:
+            _check(rc)
         return seq_lens, slots, positions, info
 
     def adjust_logits(self, logits, prompt=None, output=None, repetition=None, frequency=None, presence=None,
@@ -448,59 +457,78 @@ class Tokenizer:
         [masks, ceil(vocab / 32)], bit v % 32 of word v / 32 set for an
         allowed token; mask_rows: int32[n], each row's mask or -1."""
         import torch
-        types = _types()
-        self._checked("logits", logits, types, 2)
+        i32, i64, f32 = torch.int32, torch.int64, torch.float32
+        types, flat = _types(), self._flat
+        code = types.get(logits.dtype)
+        if logits.get_device() != self.device or code is None or logits.dim() != 2:
+            self._refuse("logits", logits, types, 2)
         n, vocab = logits.shape
-        if logits.stride(1) != 1 and vocab > 1:
+        stride, step = logits.stride()
+        if step != 1 and vocab > 1:
             if out is logits:
                 raise ValueError("out: the elements of a row must be adjacent")
             logits = logits.contiguous()
+            stride = vocab
         if out is None:
-            out = torch.empty(n, vocab, dtype=dtype or logits.dtype, device=logits.device)
-        self._checked("out", out, types, 2)
-        if out.shape != logits.shape or (out.stride(1) != 1 and vocab > 1):
-            raise ValueError("out: needs the shape of logits, the elements of a row adjacent")
-        a = LogitsArgs(logits=logits.data_ptr(), out=out.data_ptr(), logits_type=types[logits.dtype],
-                       out_type=types[out.dtype], logits_stride=logits.stride(0), out_stride=out.stride(0),
-                       n_rows=n, n_vocab=vocab)
-
-        def flat(name, t, dtype, size=None):
-            self._checked(name, t, (dtype,), 1)
-            if (size is not None and t.shape[0] != size) or not t.is_contiguous():
-                raise ValueError(f"{name}: needs {'adjacent' if size is None else size} elements")
-            return t.data_ptr()
-
+            out = torch.empty((n, vocab), dtype=dtype or logits.dtype, device=logits.device)
+            out_stride = vocab
+        else:
+            if out.get_device() != self.device or out.dim() != 2:
+                self._refuse("out", out, types, 2)
+            out_stride, step = out.stride()
+            if out.shape != logits.shape or (step != 1 and vocab > 1):
+                raise ValueError("out: needs the shape of logits, the elements of a row adjacent")
+        out_code = types.get(out.dtype)
+        if out_code is None:
+            self._refuse("out", out, types, 2)
+        p_ids = p_off = o_ids = o_lens = b_ids = b_values = b_off = p_mask = p_rows = 0
+        n_prompt = o_stride = o_cap = n_bias = m_stride = n_masks = 0
         if prompt is not None:
             ids, offsets = prompt
-            a.prompt_ids, a.n_prompt_ids = flat("prompt ids", ids, torch.int32), ids.shape[0]
-            a.prompt_offsets = flat("prompt offsets", offsets, torch.int64, n + 1)
+            p_ids, n_prompt, p_off = flat("prompt ids", ids, i32), ids.numel(), flat("prompt offsets", offsets, i64, n + 1)
         if output is not None:
             ids, lens = output
-            self._checked("output ids", ids, (torch.int32,), 2)
-            if ids.shape[0] != n or (ids.stride(1) != 1 and ids.shape[1] > 1):
+            if ids.get_device() != self.device or ids.dtype is not i32 or ids.dim() != 2:
+                self._refuse("output ids", ids, (i32,), 2)
+            o_stride, step = ids.stride()
+            rows, o_cap = ids.shape
+            if rows != n or (step != 1 and o_cap > 1):
                 raise ValueError("output ids: needs a row for each row of logits, its elements adjacent")
-            a.output_ids, a.output_stride, a.output_capacity = ids.data_ptr(), ids.stride(0), ids.shape[1]
-            a.output_lens = flat("output lens", lens, torch.int32, n)
-        if repetition is not None:
-            a.repetition = flat("repetition", repetition, torch.float32, n)
-        if frequency is not None:
-            a.frequency = flat("frequency", frequency, torch.float32, n)
-        if presence is not None:
-            a.presence = flat("presence", presence, torch.float32, n)
+            o_ids, o_lens = ids.data_ptr(), flat("output lens", lens, i32, n)
+        p_rep = 0 if repetition is None else flat("repetition", repetition, f32, n)
+        p_freq = 0 if frequency is None else flat("frequency", frequency, f32, n)
+        p_pres = 0 if presence is None else flat("presence", presence, f32, n)
         if bias is not None:
             ids, values, offsets = bias
-            a.bias_ids, a.n_bias = flat("bias ids", ids, torch.int32), ids.shape[0]
-            a.bias_values = flat("bias values", values, torch.float32, ids.shape[0])
-            a.bias_offsets = flat("bias offsets", offsets, torch.int64, n + 1)
+            n_bias = ids.numel()
+            b_ids, b_values = flat("bias ids", ids, i32), flat("bias values", values, f32, n_bias)
+            b_off = flat("bias offsets", offsets, i64, n + 1)
         if mask is not None:
-            self._checked("mask", mask, (torch.int32, torch.uint32), 2)
-            if mask.shape[1] < (vocab + 31) // 32 or (mask.stride(1) != 1 and mask.shape[1] > 1):
+            if (mask.get_device() != self.device or (mask.dtype is not i32 and mask.dtype is not torch.uint32)
+                    or mask.dim() != 2):
+                self._refuse("mask", mask, (i32, torch.uint32), 2)
+            n_masks, words = mask.shape
+            m_stride, step = mask.stride()
+            if words < (vocab + 31) // 32 or (step != 1 and words > 1):
                 raise ValueError("mask: needs a bit for each token, the words of a row adjacent")
-            a.mask, a.mask_stride, a.n_masks = mask.data_ptr(), mask.stride(0), mask.shape[0]
+            p_mask = mask.data_ptr()
             if mask_rows is not None:
-                a.mask_rows = flat("mask rows", mask_rows, torch.int32, n)
-        bpe_adjust_logits(self.handle, a, self._stream())
+                p_rows = flat("mask rows", mask_rows, i32, n)
+        rc = self._lib.bpe_adjust_logits(
+            self.handle,
+            _pack_logits(logits.data_ptr(), out.data_ptr(), code, out_code, stride, out_stride, n, vocab, p_ids, p_off,
+                         n_prompt, o_ids, o_lens, o_stride, o_cap, p_rep, p_freq, p_pres, b_ids, b_values, b_off,
+                         n_bias, p_mask, m_stride, n_masks, p_rows),
+            torch._C._cuda_getCurrentRawStream(self.device))
+        if rc:
+            _check(rc)
         return out
+
+    def _packed_ids(self, ids):
+        import torch
+        if ids.get_device() != self.device or ids.dtype is not torch.int32:
+            self._refuse("ids", ids, (torch.int32,))
+        return ids if ids.is_contiguous() else ids.contiguous()
 
     def embed(self, ids, weight, scale: float = 1.0, skip_id: int | None = None, dtype=None, out=None):
         """scale * weight[ids] in weight's type, or in ``dtype``: ids int32 of
@@ -509,27 +537,39 @@ class Tokenizer:
         weight (its gradient runs embed_grad) unless ``out`` is given."""
         import torch
         types = _types()
-        self._checked("weight", weight, types, 2)
-        ids = self._ids(ids)
+        code = types.get(weight.dtype)
+        if weight.get_device() != self.device or code is None or weight.dim() != 2:
+            self._refuse("weight", weight, types, 2)
+        ids = self._packed_ids(ids)
+        n_rows, dim = weight.shape
         if out is None:
             dtype = dtype or weight.dtype
             if weight.requires_grad and torch.is_grad_enabled():
                 return _embed_function().apply(self, ids, weight, scale, skip_id, dtype)
-            out = torch.empty(*ids.shape, weight.shape[1], dtype=dtype, device=weight.device)
-            self._checked("dtype", out, types)
+            out = torch.empty((*ids.shape, dim), dtype=dtype, device=weight.device)
+            out_stride = dim
         else:
-            self._checked("out", out, types)
-            if out.shape != (*ids.shape, weight.shape[1]) or (out.dim() != 2 and not out.is_contiguous()):
-                raise ValueError("out: needs the shape of ids and weight's columns, and to be contiguous "
-                                 "where ids is not one-dimensional")
-        if weight.stride(1) != 1 and weight.shape[1] > 1:
+            if out.get_device() != self.device or out.shape != (*ids.shape, dim):
+                raise ValueError("out: needs the shape of ids and weight's columns, on the tokenizer's device")
+            out_stride = dim
+            if out.dim() == 2:
+                out_stride, step = out.stride()
+                if step != 1 and dim > 1:
+                    raise ValueError("out: the elements of a row must be adjacent")
+            elif not out.is_contiguous():
+                raise ValueError("out: needs to be contiguous where ids is not one-dimensional")
+        out_code = types.get(out.dtype)
+        if out_code is None:
+            self._refuse("out", out, types)
+        stride, step = weight.stride()
+        if step != 1 and dim > 1:
             weight = weight.contiguous()
-        if out.dim() == 2 and out.stride(1) != 1 and out.shape[1] > 1:
-            raise ValueError("out: the elements of a row must be adjacent")
-        dim = weight.shape[1]
-        bpe_embed(self.handle, ids.data_ptr(), ids.numel(), weight.data_ptr(), types[weight.dtype], weight.shape[0],
-                  dim, weight.stride(0), scale, NO_ID if skip_id is None else skip_id, out.data_ptr(),
-                  types[out.dtype], out.stride(0) if out.dim() == 2 else dim, self._stream())
+            stride = dim
+        rc = self._lib.bpe_embed(self.handle, ids.data_ptr(), ids.numel(), weight.data_ptr(), code, n_rows, dim, stride,
+                                 scale, NO_ID if skip_id is None else skip_id, out.data_ptr(), out_code, out_stride,
+                                 torch._C._cuda_getCurrentRawStream(self.device))
+        if rc:
+            _check(rc)
         return out
 
     def embed_grad(self, ids, grad, n_rows: int, scale: float = 1.0, skip_id: int | None = None, dtype=None,
@@ -539,26 +579,45 @@ class Tokenizer:
         ``dtype``, or written into (accumulate: added to) ``out``."""
         import torch
         types = _types()
-        self._checked("grad", grad, types)
-        ids = self._ids(ids)
+        code = types.get(grad.dtype)
+        if grad.get_device() != self.device or code is None:
+            self._refuse("grad", grad, types)
+        ids = self._packed_ids(ids)
+        n = ids.numel()
         if grad.shape[:-1] != ids.shape:
             raise ValueError("grad: needs the shape of ids and one more dimension")
         dim = grad.shape[-1]
-        grad = grad.reshape(ids.numel(), dim)
-        if grad.stride(1) != 1 and dim > 1:
+        if grad.dim() != 2:
+            grad = grad.reshape(n, dim)
+        stride, step = grad.stride()
+        if step != 1 and dim > 1:
             grad = grad.contiguous()
+            stride = dim
         if out is None:
             if accumulate:
                 raise ValueError("accumulate needs out")
-            out = torch.empty(n_rows, dim, dtype=dtype or grad.dtype, device=grad.device)
-        self._checked("out", out, types, 2)
-        if out.shape != (n_rows, dim) or (out.stride(1) != 1 and dim > 1):
-            raise ValueError("out: needs n_rows rows of grad's columns, the elements of a row adjacent")
-        bpe_embed_grad(self.handle, ids.data_ptr(), ids.numel(), grad.data_ptr(), types[grad.dtype], grad.stride(0),
-                       scale, NO_ID if skip_id is None else skip_id, n_rows, dim, out.data_ptr(), types[out.dtype],
-                       out.stride(0), accumulate, self._stream())
+            out = torch.empty((n_rows, dim), dtype=dtype or grad.dtype, device=grad.device)
+            out_stride = dim
+        else:
+            if out.get_device() != self.device or out.dim() != 2:
+                self._refuse("out", out, types, 2)
+            out_stride, step = out.stride()
+            if out.shape != (n_rows, dim) or (step != 1 and dim > 1):
+                raise ValueError("out: needs n_rows rows of grad's columns, the elements of a row adjacent")
+        out_code = types.get(out.dtype)
+        if out_code is None:
+            self._refuse("out", out, types, 2)
+        rc = self._lib.bpe_embed_grad(self.handle, ids.data_ptr(), n, grad.data_ptr(), code, stride, scale,
+                                      NO_ID if skip_id is None else skip_id, n_rows, dim, out.data_ptr(), out_code,
+                                      out_stride, accumulate, torch._C._cuda_getCurrentRawStream(self.device))
+        if rc:
+            _check(rc)
         return out
 
+
+# bpe_logits_args in native layout, for Tokenizer.adjust_logits: one pack takes
+# a tenth of the time of filling a LogitsArgs field by field
+_pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
 _type_codes = {}
 
