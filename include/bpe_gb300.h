@@ -367,17 +367,20 @@ int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int6
  *                 last token (n_slots may be padded to a captured size).
  *   d_positions   device int32[n_slots]: each token's place in its request; 0
  *                 past the last token.
- *   d_info        device int64[2]: the free list's head after the call (may
- *                 be d_head itself), and the blocks lacking.
+ *   d_info        device int64[2]: the free list's head after the call (the
+ *                 next step's d_head), and the blocks lacking.
+ * d_info and d_seq_lens must not overlap d_head and d_cached.
  *
  * Blocks are dealt in request order. A request whose blocks the list cannot
  * cover, after those of the requests before it, gets none (seq_lens holds
  * cached[i]); requests that need no block are always served. That is no
  * error: info[1] is how many blocks more would have served all.
  * Reported (BPE_ERR_BAD_INPUT) and not served: a request whose offsets are
- * not monotone in [0, n_slots], whose cached length is negative, or that needs
- * more than max_blocks; a head outside [0, n_free] counts as an empty list.
- * Sizes: n_requests and n_slots < 2^31 - 1. Workspace: 8 bytes a request.
+ * not monotone in [0, n_slots], whose cached length is negative, that would
+ * pass 2^31 - block_size tokens, or that needs more than max_blocks; a head
+ * outside [0, n_free] counts as an empty list.
+ * Sizes: n_requests and n_slots < 2^31 - 1. Workspace: 8 bytes a request above
+ * 2048 requests.
  */
 int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_cached, int64_t n_requests,
                     int64_t block_size, const int32_t* d_free, int64_t n_free, const int64_t* d_head,

@@ -130,6 +130,17 @@ def test_one_long_request_among_empty_ones(tok):
     assert run(tok, offsets, cached, table, free, 16, offsets[-1] + 3) == list(want)
 
 
+@pytest.mark.parametrize("n", [5, 3000])
+def test_many_empty_requests_in_a_tile(tok, n):
+    """More requests start at one token than a tile has tokens."""
+    offsets = [0] * (n // 2) + [7] * (n - n // 2) + [2000]
+    cached = [(i * 7) % 40 for i in range(n)]
+    table = [[i * 100 + k if k < -(-c // 16) else -1 for k in range(130)] for i, c in enumerate(cached)]
+    free = list(range(900_000, 900_400))
+    want = plain(offsets, cached, table, free, 16, 2000, 2)
+    assert run(tok, offsets, cached, table, free, 16, 2000, 2) == list(want)
+
+
 def test_no_requests(tok):
     import torch
     table = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
@@ -225,7 +236,8 @@ def test_refusals(bpe, tok):
                       (4, -16), (4, 2 ** 31), (5, None), (5, free.data_ptr() + 2), (6, -1), (7, head.data_ptr() + 4),
                       (8, None), (8, table.data_ptr() + 2), (9, -1), (10, 2), (11, None), (11, seq.data_ptr() + 1),
                       (12, None), (12, slots.data_ptr() + 4), (13, None), (13, pos.data_ptr() + 2), (14, -1),
-                      (14, 2 ** 31), (15, None), (15, info.data_ptr() + 4)):
+                      (14, 2 ** 31), (15, None), (15, info.data_ptr() + 4), (15, head.data_ptr()),
+                      (7, info.data_ptr() + 8), (11, cached.data_ptr()), (11, cached.data_ptr() + 12)):
         assert L.bpe_plan_blocks(*(good[:at] + [value] + good[at + 1:])) == 1, (at, value)
         assert b"bpe_plan_blocks" in L.bpe_last_error()
     assert L.bpe_plan_blocks(*([tok.handle, None] + good[2:14] + [n - 1] + good[15:])) == 1
