@@ -103,149 +103,150 @@ __device__ __forceinline__ void plan_max(unsigned long long* to, unsigned long l
   if ((threadIdx.x & 31) == 0 && x) atomicMax(to, x);
 }
 
-// What the tokens [t0, t1) of a tile need of their requests: the last request
-// that starts at or before t, for each. Requests that start inside the tile
-// have their first token in shared memory if they are no more than kPlanTile;
-// else (many empty ones) a token searches the offsets themselves.
 constexpr int kPlanThreads = 256;
-constexpr int kPlanTile = 1024;  // tokens of a block
+constexpr int kPlanPairs = 4;                                // pairs of tokens of a thread, at most
+constexpr int kPlanTile = kPlanThreads * 2 * kPlanPairs;     // tokens of a block, at most
+constexpr int kPlanList = 2048;                              // requests that a block lists
 
-__device__ __forceinline__ int64_t plan_upper(const int64_t* offsets, int64_t lo, int64_t hi, int64_t t) {
-  while (lo < hi) {
-    const int64_t mid = lo + ((hi - lo) >> 1);
-    if (__ldg(offsets + mid) <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
-// The same by a warp, 32 offsets a step.
-__device__ __forceinline__ int64_t plan_upper_warp(const int64_t* offsets, int64_t n, int64_t t) {
-  const int lane = threadIdx.x & 31;
-  int64_t lo = 0, hi = n;  // the answer is in [lo, hi]
-  while (lo < hi) {
-    const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
-    const bool below = at < hi && __ldg(offsets + at) <= t;
-    const int k = __popc(__ballot_sync(0xFFFFFFFFu, below));  // offsets rise, so these are the first k
-    hi = min(hi, lo + (k + 1) * step - 1);
-    lo = min(lo + k * step, hi);
-  }
-  return lo;
-}
-
-struct PlanTile {
-  int64_t low, count;  // requests before the tile's first that starts in it; how many start in it
-  int32_t start[kPlanTile];
+// Consecutive requests, in shared memory.
+struct PlanList {
+  int32_t start[kPlanList + 1];  // first new token, relative to the tile's
+  int32_t cached[kPlanList];     // -1 - (what is in the cache) for a request that is not ok
+  int32_t held[kPlanList];
+  int32_t base[kPlanList];       // G_i - g_i, -1 where not served
 };
 
-__device__ __forceinline__ void plan_tile(const PlanArgs& a, int64_t t0, int64_t t1, PlanTile& p) {
-  const int warp = threadIdx.x >> 5;
-  if (a.offsets && warp < 2) {
-    const int64_t u = plan_upper_warp(a.offsets, a.n, warp == 0 ? t0 : t1 - 1);
-    if ((threadIdx.x & 31) == 0) (warp == 0 ? p.low : p.count) = u;
-  }
-  __syncthreads();
-  if (a.offsets && p.count - p.low <= kPlanTile)
-    for (int64_t k = threadIdx.x; k < p.count - p.low; k += kPlanThreads)
-      p.start[k] = (int32_t)(__ldg(a.offsets + p.low + k) - t0);
-  __syncthreads();
+__device__ __forceinline__ int32_t plan_relative(int64_t offset, int64_t t0) {
+  return (int32_t)min(max(offset - t0, (int64_t)INT32_MIN), (int64_t)INT32_MAX);
 }
 
-// Slots, positions and table entries of the tile's tokens; base(i) is G_i -
-// g_i of request i, or -1 where it is not served. A block that is dealt has
+// Slots, positions and table entries of the tokens [t0, t1), whose requests
+// are `first` and the next ones in the list. A thread takes pairs of
+// neighbours: one search finds both, and they are stored as one vector. Its
+// pairs step together, so that their loads overlap. A block that is dealt has
 // one token in its first slot, and that token writes its table entry.
-template <class B>
-__device__ __forceinline__ void plan_tokens(const PlanArgs& a, int64_t t0, int64_t t1, const PlanTile& p, int64_t head,
-                                            B base) {
-  for (int64_t t = t0 + threadIdx.x; t < t1; t += kPlanThreads) {
-    int64_t i = t;
-    if (a.offsets) {
-      const int64_t count = p.count - p.low;
-      if (count >= 0 && count <= kPlanTile) {
-        int lo = 0, hi = (int)count;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (p.start[mid] <= t - t0) lo = mid + 1;
-          else hi = mid;
+__device__ __forceinline__ void plan_tokens(const PlanArgs& a, int64_t t0, int64_t t1, int64_t head, int64_t first,
+                                            int count, const PlanList& list) {
+  const int len = (int)(t1 - t0);
+  const bool vectors = ((reinterpret_cast<uintptr_t>(a.slots + t0) & 15) | (reinterpret_cast<uintptr_t>(a.positions + t0) & 7)) == 0;
+  const int32_t* free_list = a.free_list + head;
+  int32_t position[kPlanPairs][2], in[kPlanPairs][2], entry[kPlanPairs][2];
+  int32_t* dealt[kPlanPairs][2];  // the table entry that the token writes, or null
+#pragma unroll
+  for (int q = 0; q < kPlanPairs; ++q) {
+    const int at = 2 * (int)threadIdx.x + 2 * kPlanThreads * q;
+    int l = 0;
+    if (at < len) {
+      if (a.offsets) {
+        int h = count;
+        while (l < h) {
+          const int mid = (l + h) >> 1;
+          if (list.start[mid] <= at) l = mid + 1;
+          else h = mid;
         }
-        i = p.low + lo - 1;
       } else {
-        i = plan_upper(a.offsets, 0, a.n, t) - 1;
+        l = min(at + 1, count);
       }
     }
-    int64_t slot = -1;
-    uint32_t position = 0;
-    if (i >= 0 && i < a.n) {
-      const PlanRequest r = plan_request(a, i);
-      if (r.ok && t >= r.first && t < r.first + r.fresh) {
-        position = (uint32_t)(r.cached + (t - r.first));
-        const int64_t dealt = base(i);
-        if (dealt >= 0) {
-          const uint32_t b = a.block(position), in = position - b * a.block.d;
-          int32_t* entry = a.table + i * a.table_stride + b;
-          int32_t q;
-          if (b < r.held) {
-            q = *entry;
-          } else {
-            q = __ldg(a.free_list + head + dealt + (b - r.held));
-            if (in == 0) *entry = q;
-          }
-          slot = (int64_t)q * a.block.d + in;
-        }
+    --l;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int x = at + e;
+      while (e == 1 && x < len && l + 1 < count && list.start[l + 1] <= x) ++l;
+      position[q][e] = 0;
+      in[q][e] = -1;
+      dealt[q][e] = nullptr;
+      if (x >= len || l < 0) continue;
+      const int32_t from = list.start[l], c = list.cached[l];
+      if (c < 0 || x < from || x >= list.start[l + 1]) continue;
+      const uint32_t p = (uint32_t)(c + (x - from));
+      position[q][e] = (int32_t)p;
+      const int32_t base = list.base[l];
+      if (base < 0) continue;
+      const uint32_t b = a.block(p);
+      in[q][e] = (int32_t)(p - b * a.block.d);
+      const int32_t fresh = (int32_t)b - list.held[l];
+      int32_t* row = a.table + (first + l) * a.table_stride + b;
+      entry[q][e] = *(fresh < 0 ? row : free_list + base + fresh);
+      if (fresh >= 0 && in[q][e] == 0) dealt[q][e] = row;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kPlanPairs; ++q) {
+    const int at = 2 * (int)threadIdx.x + 2 * kPlanThreads * q;
+    if (at >= len) break;
+    int64_t slot[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      slot[e] = in[q][e] < 0 ? -1 : (int64_t)entry[q][e] * a.block.d + in[q][e];
+      if (dealt[q][e]) *dealt[q][e] = entry[q][e];
+    }
+    if (vectors && at + 1 < len) {
+      __stcs(reinterpret_cast<longlong2*>(a.slots + t0 + at), make_longlong2(slot[0], slot[1]));
+      __stcs(reinterpret_cast<int2*>(a.positions + t0 + at), make_int2(position[q][0], position[q][1]));
+    } else {
+      for (int e = 0; e < 2 && at + e < len; ++e) {
+        a.slots[t0 + at + e] = slot[e];
+        a.positions[t0 + at + e] = position[q][e];
       }
     }
-    __stcs(a.slots + t, slot);
-    __stcs(a.positions + t, (int32_t)position);
   }
 }
 
-// Up to kPlanOne requests: every block adds up all requests' blocks itself,
-// which takes less time than a launch, and plans its tile of tokens.
-constexpr int kPlanOne = 2048;
-
-__global__ void __launch_bounds__(kPlanThreads) k_plan_one(PlanArgs a) {
-  constexpr int kPer = kPlanOne / kPlanThreads;
-  __shared__ PlanTile tile;
-  __shared__ int64_t base[kPlanOne];
+// Up to kPlanList requests: every block adds up all requests' blocks itself,
+// which takes less time than a launch, and plans its tile of tokens from the
+// list that it then has.
+__global__ void __launch_bounds__(kPlanThreads) k_plan_one(PlanArgs a, int tile) {
+  constexpr int kPer = kPlanList / kPlanThreads;
+  __shared__ PlanList list;
   __shared__ int64_t warp_sum[kPlanThreads / 32];
   __shared__ unsigned long long taken;
   const int tid = threadIdx.x, n = (int)a.n;
+  const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = min(t0 + tile, a.n_slots);
   const bool lead = blockIdx.x == 0;
   bool bad;
   const int64_t head = plan_head(a, &bad), room = a.n_free - head;
   if (tid == 0) taken = 0;
-  PlanRequest r[kPer];
+  // thread t has requests [t * per, t * per + per)
+  const int per = (n + kPlanThreads - 1) / kPlanThreads;
+  uint32_t gets[kPer];
   int64_t mine = 0;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
-    const int i = tid * kPer + q;
-    if (i >= n) continue;
-    r[q] = plan_request(a, i);
-    mine += r[q].gets;
-    bad |= !r[q].ok;
+    const int i = tid * per + q;
+    if (q >= per || i >= n) break;
+    const PlanRequest r = plan_request(a, i);
+    list.start[i] = plan_relative(r.first, t0);
+    list.cached[i] = r.ok ? r.cached : -1 - max(r.cached, 0);
+    list.held[i] = (int32_t)r.held;
+    gets[q] = r.gets;
+    mine += r.gets;
+    bad |= !r.ok;
+    if (lead) a.seq_lens[i] = r.ok ? (int32_t)(r.cached + r.fresh) : max(r.cached, 0);
   }
+  if (tid == 0) list.start[n] = plan_relative(a.offsets ? __ldg(a.offsets + n) : a.n, t0);
   int64_t total;
   int64_t upto = plan_scan<kPlanThreads / 32>(mine, &total, warp_sum) - mine;
   unsigned long long best = 0;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
-    const int i = tid * kPer + q;
-    if (i >= n) continue;
-    upto += r[q].gets;
-    const bool served = r[q].ok && (r[q].gets == 0 || upto <= room);
-    base[i] = served ? upto - r[q].gets : -1;
+    const int i = tid * per + q;
+    if (q >= per || i >= n) break;
+    upto += gets[q];
+    // a request without new blocks takes no entry, and its sum may be past the list
+    const bool served = gets[q] == 0 || upto <= room;
+    list.base[i] = served ? (gets[q] ? (int32_t)(upto - gets[q]) : 0) : -1;
     if (upto <= room) best = (unsigned long long)upto;
-    if (lead) a.seq_lens[i] = served ? (int32_t)(r[q].cached + r[q].fresh) : max(r[q].cached, 0);
+    if (lead && !served) a.seq_lens[i] = list.cached[i];
   }
   if (lead) plan_max(&taken, best);
   if (lead && bad) atomicOr(&a.small->op_status, kStBadInput);
-  const int64_t t0 = (int64_t)blockIdx.x * kPlanTile, t1 = min(t0 + kPlanTile, a.n_slots);
-  plan_tile(a, t0, t1, tile);  // its barriers also publish base and taken
+  __syncthreads();
   if (lead && tid == 0) {
     a.info[0] = head + (int64_t)taken;
     a.info[1] = max((int64_t)0, total - room);
   }
-  plan_tokens(a, t0, t1, tile, head, [&](int64_t i) { return base[i]; });
+  if (t0 < t1) plan_tokens(a, t0, t1, head, 0, n, list);
 }
 
 // More requests: one cluster adds up their blocks (a CTA a contiguous part, the
@@ -293,7 +294,8 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanSumT
     if (i < i1) {
       const bool served = r.ok && (r.gets == 0 || upto <= room);
       if (upto <= room) best = max(best, (unsigned long long)upto);
-      a.base[i] = served ? upto - r.gets : -1;
+      // a request without new blocks takes no entry, and its sum may be past the list
+      a.base[i] = served ? (r.gets ? upto - r.gets : 0) : -1;
       a.seq_lens[i] = served ? (int32_t)(r.cached + r.fresh) : max(r.cached, 0);
     }
   }
@@ -311,15 +313,82 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanSumT
 }
 
 // ... and the blocks of a second launch plan their tiles of tokens, having
-// found their requests while the first one ran.
-__global__ void __launch_bounds__(kPlanThreads) k_plan_tokens(PlanArgs a) {
-  __shared__ PlanTile tile;
+// listed their requests while the first one ran: the last that starts at or
+// before the tile, and those that start inside it. Where these are more than
+// a list holds (many are empty), the tile's tokens search the offsets.
+__global__ void __launch_bounds__(kPlanThreads) k_plan_tokens(PlanArgs a, int tile) {
+  __shared__ PlanList list;
+  const int tid = threadIdx.x;
   bool bad;
   const int64_t head = plan_head(a, &bad);
-  const int64_t t0 = (int64_t)blockIdx.x * kPlanTile, t1 = min(t0 + kPlanTile, a.n_slots);
-  plan_tile(a, t0, t1, tile);
+  const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = min(t0 + tile, a.n_slots);
+  // the number of requests that start at or before t0, by as many probes a step as threads
+  int64_t lo = a.offsets ? 0 : min(t0 + 1, a.n), hi = a.offsets ? a.n : lo;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + kPlanThreads - 1) / kPlanThreads, at = lo + (tid + 1) * step - 1;
+    const int k = __syncthreads_count(at < hi && __ldg(a.offsets + at) <= t0);  // offsets rise: these are the first k
+    hi = min(hi, lo + (k + 1) * step - 1);
+    lo = min(lo + k * step, hi);
+  }
+  const int64_t first = max(lo - 1, (int64_t)0);
+  int count = 0;      // requests listed
+  bool whole = false; // and no other one is the tile's
+  while (count < kPlanList && !whole) {
+    const int64_t i = first + count + tid;
+    bool inside = false;
+    if (i < a.n) {
+      const PlanRequest r = plan_request(a, i);
+      list.start[count + tid] = plan_relative(r.first, t0);
+      list.cached[count + tid] = r.ok ? r.cached : -1;
+      list.held[count + tid] = (int32_t)r.held;
+      inside = r.first < t1;
+    } else if (i == a.n) {
+      list.start[count + tid] = plan_relative(a.offsets ? __ldg(a.offsets + i) : i, t0);
+    }
+    const int k = __syncthreads_count(inside);
+    whole = k < kPlanThreads;
+    count += k;
+  }
+  // the start after the last listed request, which bounds it
+  if (!whole && tid == 0) {
+    const int64_t i = min(first + count, a.n);
+    list.start[count] = plan_relative(a.offsets ? __ldg(a.offsets + i) : i, t0);
+  }
   await_previous();
-  plan_tokens(a, t0, t1, tile, head, [&](int64_t i) { return __ldcg(a.base + i); });
+  for (int k = tid; k < count; k += kPlanThreads) list.base[k] = (int32_t)__ldcg(a.base + first + k);
+  __syncthreads();
+  whole |= list.start[count] >= t1 - t0 || first + count >= a.n;
+  if (whole) {
+    plan_tokens(a, t0, t1, head, first, count, list);
+    return;
+  }
+  for (int64_t t = t0 + tid; t < t1; t += kPlanThreads) {
+    int64_t l = 0, h = a.n;
+    while (l < h) {
+      const int64_t mid = l + ((h - l) >> 1);
+      if (__ldg(a.offsets + mid) <= t) l = mid + 1;
+      else h = mid;
+    }
+    int64_t slot = -1, position = 0;
+    const int64_t i = l - 1;
+    if (i >= 0) {
+      const PlanRequest r = plan_request(a, i);
+      if (r.ok && t >= r.first && t < r.first + r.fresh) {
+        position = r.cached + (t - r.first);
+        const int64_t base = __ldcg(a.base + i);
+        if (base >= 0) {
+          const uint32_t b = a.block((uint32_t)position);
+          const int32_t in = (int32_t)((uint32_t)position - b * a.block.d), fresh = (int32_t)b - (int32_t)r.held;
+          int32_t* row = a.table + i * a.table_stride + b;
+          const int32_t entry = *(fresh < 0 ? row : a.free_list + head + base + fresh);
+          if (fresh >= 0 && in == 0) *row = entry;
+          slot = (int64_t)entry * a.block.d + in;
+        }
+      }
+    }
+    a.slots[t] = slot;
+    a.positions[t] = (int32_t)position;
+  }
 }
 
 }  // namespace
@@ -333,6 +402,7 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
   return guarded("bpe_plan_blocks", [&]() -> int {
     if (!h) return fail(BPE_ERR_INVALID_ARG, "bpe_plan_blocks: null handle");
     if (n_requests < 0 || n_requests >= INT32_MAX || block_size < 1 || block_size > INT32_MAX || n_free < 0 ||
+        n_free > INT32_MAX ||
         max_blocks < 0 || n_slots < 0 || n_slots >= INT32_MAX)
       return fail(BPE_ERR_INVALID_ARG, "bpe_plan_blocks: a size is negative or too large");
     if (n_requests > 1 && table_stride < max_blocks)
@@ -357,9 +427,12 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
     cudaStream_t st = (cudaStream_t)stream;
     PlanArgs a{d_offsets, d_cached, n_requests, n_free, max_blocks, table_stride, n_slots, FastDiv(block_size), d_free,
                d_head, d_table, d_seq_lens, d_slots, d_positions, d_info, nullptr, h->d_small};
-    const unsigned tiles = (unsigned)((n_slots + kPlanTile - 1) / kPlanTile);
-    if (n_requests <= kPlanOne) {
-      k_plan_one<<<std::max(1u, tiles), kPlanThreads, 0, st>>>(a);
+    // tokens of a thread: as few as leave at most two blocks an SM
+    const int64_t each = (n_slots + kPlanThreads * 4 * h->n_sms - 1) / (kPlanThreads * 4 * h->n_sms);
+    const int tile = 2 * kPlanThreads * (int)std::min<int64_t>(kPlanPairs, std::max<int64_t>(1, each));
+    const unsigned tiles = (unsigned)((n_slots + tile - 1) / tile);
+    if (n_requests <= kPlanList) {
+      k_plan_one<<<std::max(1u, tiles), kPlanThreads, 0, st>>>(a, tile);
       CK(cudaGetLastError());
       return BPE_OK;
     }
@@ -368,7 +441,7 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
     a.base = static_cast<int64_t*>(h->d_ws);
     k_plan_requests<<<kPlanCluster, kPlanSumThreads, 0, st>>>(a);
     CK(cudaGetLastError());
-    if (tiles) CK(launch_after(k_plan_tokens, dim3(tiles), kPlanThreads, 0, st, a));
+    if (tiles) CK(launch_after(k_plan_tokens, dim3(tiles), kPlanThreads, 0, st, a, tile));
     return BPE_OK;
   });
 }

@@ -379,7 +379,7 @@ int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int6
  * not monotone in [0, n_slots], whose cached length is negative, that would
  * pass 2^31 - block_size tokens, or that needs more than max_blocks; a head
  * outside [0, n_free] counts as an empty list.
- * Sizes: n_requests and n_slots < 2^31 - 1. Workspace: 8 bytes a request above
+ * Sizes: n_requests and n_slots < 2^31 - 1, n_free < 2^31. Workspace: 8 bytes a request above
  * 2048 requests.
  */
 int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_cached, int64_t n_requests,
