@@ -12,105 +12,324 @@
 
 namespace {
 
-constexpr int kLogThreads = 256;
-constexpr int kLogChunk = 4096;  // tokens of a CTA
-constexpr uint32_t kLogPrompt = 0x80000000u, kLogBias = 0x40000000u, kLogCount = 0x3FFFFFFFu;
+constexpr int kLogThreads = 512;
+constexpr int kLogWarps = kLogThreads / 32;
+constexpr int kLogGroup = 8;         // tokens of a vector
+constexpr int kLogAhead = 2;         // vectors of a thread in flight
+constexpr int kLogIds = 2;           // 16-byte loads of ids of a thread in flight
+constexpr int kLogMinChunk = 2048;   // tokens of a CTA
+constexpr int kLogMaxChunk = 16384;
+constexpr int kLogList = 2048;       // concerned tokens that a CTA lists at once
+constexpr int kLogBiases = 1024;     // biases of a chunk that it lists
 
-// Adds v to bias[at], equal places in lane order; at < 0 for none. One warp.
-__device__ __forceinline__ void log_add_bias(float* bias, uint32_t* seen, int at, float v, int lane) {
-  const unsigned same = __match_any_sync(0xFFFFFFFFu, at);
-  float sum = at >= 0 ? bias[at] : 0.f;
-  if (__any_sync(0xFFFFFFFFu, at >= 0 && (same & (same - 1)))) {
-    for (int k = 0; k < 32; ++k) {
-      const float vk = __shfl_sync(0xFFFFFFFFu, v, k);
-      if (same >> k & 1) sum += vk;
+// What a row's history says about a chunk, in shared memory: a bit for each
+// token that occurs in it, and the times it occurs in the output, in 16 bits
+// where no output is longer than that. Both are only added to, without a look
+// at what was there, so nothing waits for shared memory.
+struct LogTable {
+  uint32_t* bits;    // [chunk / 32]
+  uint32_t* biased;  // [chunk / 32] a bit for each token with a bias
+  uint32_t* counts;  // [chunk] or, packed, [chunk / 2]
+  bool packed;
+
+  static int bytes(int chunk, bool by_output, bool packed) {
+    return chunk / 4 + (by_output ? packed ? chunk * 2 : chunk * 4 : 0);
+  }
+  __device__ __forceinline__ void clear(int chunk, bool by_output) const {
+    const int words = chunk / 16 + (by_output ? packed ? chunk / 2 : chunk : 0);
+    for (int v = threadIdx.x; v < words / 4; v += kLogThreads) reinterpret_cast<uint4*>(bits)[v] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void see(int v) const { atomicOr(&bits[v >> 5], 1u << (v & 31)); }
+  __device__ __forceinline__ void count(int v) const {
+    if (packed) atomicAdd(&counts[v >> 1], (v & 1) ? 0x10000u : 1u);
+    else atomicAdd(&counts[v], 1u);
+  }
+  __device__ __forceinline__ bool seen(int v) const { return bits[v >> 5] >> (v & 31) & 1; }
+  __device__ __forceinline__ uint32_t times(int v) const {
+    return packed ? counts[v >> 1] >> ((v & 1) * 16) & 0xFFFFu : counts[v];
+  }
+};
+
+// A row's parameters, and where its history and biases are.
+struct LogRow {
+  float rep, freq, pres;
+  const int32_t *prompt, *output, *bias_ids;
+  const float* bias_values;
+  int64_t n_prompt, n_output, n_bias;
+  const uint32_t* mask;  // its words, or null
+  bool concerned;        // anything but the mask concerns it
+};
+
+__device__ __forceinline__ LogRow log_row(const bpe_logits_args& a, int64_t b, bool table, bool* bad) {
+  LogRow r{1.f, 0.f, 0.f, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, nullptr, false};
+  if (table) {
+    // all loads first, so that they overlap
+    const int64_t p0 = a.prompt_ids ? __ldg(a.prompt_offsets + b) : 0, p1 = a.prompt_ids ? __ldg(a.prompt_offsets + b + 1) : 0;
+    const int64_t len = a.output_ids ? __ldg(a.output_lens + b) : 0;
+    const int64_t b0 = a.bias_ids ? __ldg(a.bias_offsets + b) : 0, b1 = a.bias_ids ? __ldg(a.bias_offsets + b + 1) : 0;
+    if (a.repetition) r.rep = __ldg(a.repetition + b);
+    if (a.frequency) r.freq = __ldg(a.frequency + b);
+    if (a.presence) r.pres = __ldg(a.presence + b);
+    if (r.rep != 1.f) {
+      if (p0 < 0 || p1 < p0 || p1 > a.n_prompt_ids) *bad = true;
+      else r.prompt = a.prompt_ids + p0, r.n_prompt = p1 - p0;
     }
-  } else {
-    sum += v;
+    if (r.rep != 1.f || r.freq != 0.f || r.pres != 0.f) {
+      if (len < 0 || len > a.output_capacity) *bad = true;
+      else r.output = a.output_ids + b * a.output_stride, r.n_output = len;
+    }
+    if (b0 < 0 || b1 < b0 || b1 > a.n_bias) *bad = true;
+    else r.bias_ids = a.bias_ids + b0, r.bias_values = a.bias_values + b0, r.n_bias = b1 - b0;
+    r.concerned = r.n_prompt + r.n_output + r.n_bias > 0;
   }
-  if (at >= 0 && (same & ((1u << lane) - 1)) == 0) {
-    bias[at] = sum;
-    atomicOr(&seen[at], kLogBias);
+  if (a.mask) {
+    const int64_t row = a.mask_rows ? __ldg(a.mask_rows + b) : b;
+    if (row < -1 || row >= a.n_masks) *bad = true;
+    else if (row >= 0) r.mask = a.mask + row * a.mask_stride;
   }
-  __syncwarp();
+  return r;
 }
 
-template <class TI, class TO>
-__global__ void __launch_bounds__(kLogThreads) k_logits(bpe_logits_args a, DevSmall* small) {
-  __shared__ uint32_t seen[kLogChunk];
-  __shared__ float bias[kLogChunk];
+// f(id) for each id of a list; whole 16-byte vectors of ids are loaded as such,
+// several at a time.
+template <class F>
+__device__ __forceinline__ void log_each(const int32_t* ids, int64_t count, F f) {
   const int tid = threadIdx.x;
-  const int64_t b = blockIdx.y, v0 = (int64_t)blockIdx.x * kLogChunk;
-  const int n = (int)min((int64_t)kLogChunk, a.n_vocab - v0);
-  bool bad = false;
-  const float rep = a.repetition ? a.repetition[b] : 1.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f, pres = a.presence ? a.presence[b] : 0.f;
-  for (int v = tid; v < n; v += kLogThreads) {
-    seen[v] = 0;
-    bias[v] = 0.f;
-  }
-  __syncthreads();
-  if (rep != 1.f && a.prompt_ids) {
-    const int64_t s = a.prompt_offsets[b], e = a.prompt_offsets[b + 1];
-    if (s < 0 || e < s || e > a.n_prompt_ids) bad = true;
-    else
-      for (int64_t j = s + tid; j < e; j += kLogThreads) {
-        const int64_t id = a.prompt_ids[j];
-        if (id < 0 || id >= a.n_vocab) bad = true;
-        else if (id >= v0 && id < v0 + n) atomicOr(&seen[id - v0], kLogPrompt);
-      }
-  }
-  if ((rep != 1.f || freq != 0.f || pres != 0.f) && a.output_ids) {
-    const int64_t len = a.output_lens[b];
-    if (len < 0 || len > a.output_capacity) bad = true;
-    else
-      for (int64_t j = tid; j < len; j += kLogThreads) {
-        const int64_t id = a.output_ids[b * a.output_stride + j];
-        if (id < 0 || id >= a.n_vocab) bad = true;
-        else if (id >= v0 && id < v0 + n) atomicAdd(&seen[id - v0], 1u);
-      }
-  }
-  __syncthreads();
-  if (tid < 32 && a.bias_ids) {
-    const int64_t s = a.bias_offsets[b], e = a.bias_offsets[b + 1];
-    if (s < 0 || e < s || e > a.n_bias) bad = true;
-    else
-      for (int64_t j = s; j < e; j += 32) {
-        int at = -1;
-        float v = 0.f;
-        if (j + tid < e) {
-          const int64_t id = a.bias_ids[j + tid];
-          if (id < 0 || id >= a.n_vocab) bad = true;
-          else if (id >= v0 && id < v0 + n) at = (int)(id - v0);
-          v = a.bias_values[j + tid];
-        }
-        log_add_bias(bias, seen, at, v, tid);
-      }
-  }
-  __syncthreads();
-  int64_t mask_row = -1;
-  if (a.mask) {
-    mask_row = a.mask_rows ? a.mask_rows[b] : b;
-    if (mask_row < -1 || mask_row >= a.n_masks) {
-      bad = true;
-      mask_row = -1;
+  const int64_t head = min((int64_t)((-reinterpret_cast<uintptr_t>(ids) & 15) / 4), count);
+  const int64_t vecs = (count - head) / 4, tail = head + vecs * 4;
+  // at most three ids before the vectors and three after
+  const int64_t edge = tid < head ? tid : tail + tid - head;
+  const bool has_edge = edge < count;
+  const uint32_t edge_id = has_edge ? (uint32_t)__ldg(ids + edge) : 0;
+  const uint4* from = reinterpret_cast<const uint4*>(ids + head);
+  for (int64_t j = tid; j < vecs; j += kLogIds * kLogThreads) {
+    uint4 id[kLogIds];
+#pragma unroll
+    for (int q = 0; q < kLogIds; ++q)
+      if (j + q * kLogThreads < vecs) id[q] = __ldg(from + j + q * kLogThreads);
+#pragma unroll
+    for (int q = 0; q < kLogIds; ++q) {
+      if (j + q * kLogThreads >= vecs) break;
+      f(id[q].x);
+      f(id[q].y);
+      f(id[q].z);
+      f(id[q].w);
     }
   }
+  if (has_edge) f(edge_id);
+}
+
+// The bits of the tokens from v on, 8 of them at least; `words` of the mask may
+// be read.
+__device__ __forceinline__ uint32_t log_open(const uint32_t* mask, int v, int words) {
+  const int w = v >> 5;
+  return __funnelshift_r(__ldg(mask + w), __ldg(mask + min(w + 1, words - 1)), v & 31);
+}
+
+// A seen token's logit.
+__device__ __forceinline__ float log_penalty(const LogRow& r, float x, uint32_t times) {
+  x = x > 0.f ? x / r.rep : x * r.rep;
+  return times ? x - r.freq * (float)times - r.pres : x;
+}
+
+// Tokens [v0, v0 + n) of a row pass through registers once, 16 bytes of input
+// at a time, and leave with the mask applied; by kThreads threads, of which
+// this is tid. The first vectors are loaded before row() gives the row's mask.
+template <class TI, class TO, int kThreads, class R>
+__device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, int64_t v0, int n, int tid, R row) {
+  const int words = (int)((a.n_vocab + 31) >> 5);
   const TI* in = static_cast<const TI*>(a.logits) + b * a.logits_stride + v0;
   TO* out = static_cast<TO*>(a.out) + b * a.out_stride + v0;
-  for (int v = tid; v < n; v += kLogThreads) {
-    float x = to_f32(in[v]);
-    const uint32_t q = seen[v];
-    if (q) {
-      const uint32_t k = q & kLogCount;
-      if (k || (q & kLogPrompt)) x = x > 0.f ? x / rep : x * rep;
-      if (k) x = x - freq * (float)k - pres;
-      if (q & kLogBias) x += bias[v];
+  // vectors start at the first 16-byte boundary of the input; if the output
+  // has none there, every token goes by itself
+  int head = (int)((-reinterpret_cast<uintptr_t>(in) & 15) / sizeof(TI));
+  if (reinterpret_cast<uintptr_t>(out + head) & 15) head = n;
+  head = min(head, n);
+  const int groups = (n - head) / kLogGroup;
+  constexpr int kAhead = sizeof(TI) == 4 ? kLogAhead / 2 : kLogAhead;
+  Vec<TI, kLogGroup> x[kAhead];
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q)
+    if (tid + q * kThreads < groups) x[q].load(in + head + (tid + q * kThreads) * kLogGroup);
+  const uint32_t* mask = row();
+  for (int g0 = tid; g0 < groups; g0 += kAhead * kThreads) {
+    if (g0 != tid) {
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (g0 + q * kThreads < groups) x[q].load(in + head + (g0 + q * kThreads) * kLogGroup);
     }
-    if (mask_row >= 0 && !(a.mask[mask_row * a.mask_stride + ((v0 + v) >> 5)] >> ((v0 + v) & 31) & 1)) x = -INFINITY;
-    out[v] = from_f32<TO>(x);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      if (g0 + q * kThreads >= groups) break;
+      const int v = head + (g0 + q * kThreads) * kLogGroup;
+      const uint32_t bits = mask ? log_open(mask, (int)v0 + v, words) : 0xFFFFFFFFu;
+      Vec<TO, kLogGroup> o;
+#pragma unroll
+      for (int e = 0; e < kLogGroup; ++e)
+        o.x[e] = from_f32<TO>(bits >> e & 1 ? to_f32(x[q].x[e]) : -INFINITY);
+      o.store(out + v);
+    }
   }
+  // what is before the first vector and after the last
+  const int tail = head + groups * kLogGroup;
+  for (int k = tid; k < head + n - tail; k += kThreads) {
+    const int v = k < head ? k : tail + k - head;
+    out[v] = from_f32<TO>(!mask || (log_open(mask, (int)v0 + v, words) & 1) ? to_f32(in[v]) : -INFINITY);
+  }
+}
+
+// A CTA takes `chunk` tokens of one row. With kTable, what the row's history
+// and biases say about them is gathered in shared memory, and after the pass
+// the few tokens that are concerned are written again, each once: the pass has
+// left a token that the mask shuts at -infinity, and in place it has
+// left the bits of every other one. Only integer atomics whose results nobody
+// takes, and biases listed in their order: nothing depends on timing.
+//
+// All CTAs of a row read its whole history, which is L2 traffic and a few
+// instructions an id. What was slower: testing for concerned tokens in the
+// pass (most warps hold one, and the whole warp waits for its division), a
+// hash table or lists filled by atomics that return a value (a chain of waits
+// for each id), warps that gather while others pass (too few to hide it), and
+// a second launch or the last CTA of a row for the gathering.
+template <class TI, class TO, bool kTable, bool kBias>
+__global__ void __launch_bounds__(kLogThreads, 3) k_logits(bpe_logits_args a, int chunk, bool packed, DevSmall* small) {
+  extern __shared__ __align__(16) uint32_t log_smem[];
+  __shared__ uint16_t list[kTable ? kLogList : 1];
+  __shared__ uint16_t bias_token[kBias ? kLogBiases : 1];
+  __shared__ float bias_value[kBias ? kLogBiases : 1];
+  __shared__ int warp_sum[kLogWarps], n_biases;
+  const LogTable t{log_smem, log_smem + chunk / 32, log_smem + chunk / 16, packed};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t b = blockIdx.y, v0 = (int64_t)blockIdx.x * chunk;
+  const int n = (int)min((int64_t)chunk, a.n_vocab - v0);
+  const uint32_t low = (uint32_t)v0, vocab = (uint32_t)a.n_vocab;
+  bool bad = false;
+  LogRow r;
+  log_pass<TI, TO, kLogThreads>(a, b, v0, n, tid, [&] {
+    r = log_row(a, b, kTable, &bad);
+    if (!kTable || !r.concerned) return r.mask;
+    t.clear(chunk, a.output_ids != nullptr);
+    __syncthreads();
+    log_each(r.prompt, r.n_prompt, [&](uint32_t id) {
+      if (id - low < (uint32_t)n) t.see((int)(id - low));
+      bad |= id >= vocab;
+    });
+    log_each(r.output, r.n_output, [&](uint32_t id) {
+      if (id - low < (uint32_t)n) {
+        t.see((int)(id - low));
+        t.count((int)(id - low));
+      }
+      bad |= id >= vocab;
+    });
+    if (kBias && warp == kLogWarps - 1) {
+      // the chunk's biases in their order; past kLogBiases they are only counted
+      int m = 0;
+      constexpr int kLook = 4;
+      for (int64_t j = lane; j - lane < r.n_bias; j += 32 * kLook) {
+        uint32_t id[kLook];
+        float value[kLook];
+#pragma unroll
+        for (int q = 0; q < kLook; ++q) {
+          const bool have = j + 32 * q < r.n_bias;
+          id[q] = have ? (uint32_t)__ldg(r.bias_ids + j + 32 * q) : 0;
+          value[q] = have ? __ldg(r.bias_values + j + 32 * q) : 0.f;
+          bad |= have && id[q] >= vocab;
+          if (!have || id[q] - low >= (uint32_t)n) id[q] = 0xFFFFFFFFu;
+        }
+#pragma unroll
+        for (int q = 0; q < kLook; ++q) {
+          const unsigned in_chunk = __ballot_sync(0xFFFFFFFFu, id[q] != 0xFFFFFFFFu);
+          const int at = m + __popc(in_chunk & ((1u << lane) - 1));
+          if (id[q] != 0xFFFFFFFFu) {
+            const int v = (int)(id[q] - low);
+            atomicOr(&t.biased[v >> 5], 1u << (v & 31));
+            if (at < kLogBiases) {
+              bias_token[at] = (uint16_t)v;
+              bias_value[at] = value[q];
+            }
+          }
+          m += __popc(in_chunk);
+        }
+      }
+      if (lane == 0) n_biases = m;
+    }
+    return r.mask;
+  });
   if (bad) atomicOr(&small->op_status, kStBadInput);
+  if (!kTable || !r.concerned) return;
+  const int words = (int)((a.n_vocab + 31) >> 5);
+  const TI* in = static_cast<const TI*>(a.logits) + b * a.logits_stride + v0;
+  TO* out = static_cast<TO*>(a.out) + b * a.out_stride + v0;
+  auto open = [&](int v) { return !r.mask || (log_open(r.mask, (int)v0 + v, words) & 1); };
+  auto penalised = [&](int v) {
+    const float x = to_f32(in[v]);
+    return t.seen(v) ? log_penalty(r, x, a.output_ids ? t.times(v) : 0) : x;
+  };
+  __syncthreads();
+  if (r.n_prompt + r.n_output > 0) {
+    // list the seen tokens, kLogThreads words of bits at most at a time, and share them out
+    for (int w0 = 0; w0 < chunk / 32; w0 += kLogThreads) {
+      const int w = w0 + tid;
+      const uint32_t bits = w < chunk / 32 ? t.bits[w] & ~t.biased[w] : 0;
+      const int mine = __popc(bits);
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      int total = 0;
+#pragma unroll
+      for (int k = 0; k < kLogWarps; ++k) {
+        if (k < warp) upto += warp_sum[k];
+        total += warp_sum[k];
+      }
+      for (int k0 = 0; k0 < total; k0 += kLogList) {
+        int at = upto - mine - k0;
+        for (uint32_t m = bits; m && at < kLogList; m &= m - 1, ++at)
+          if (at >= 0) list[at] = (uint16_t)(w * 32 + __ffs(m) - 1);
+        __syncthreads();
+        for (int k = tid; k < min(total - k0, kLogList); k += kLogThreads) {
+          const int v = list[k];
+          if (open(v)) out[v] = from_f32<TO>(penalised(v));
+        }
+        __syncthreads();
+      }
+      __syncthreads();  // warp_sum is read by all before it is written again
+    }
+  }
+  if (!kBias) return;
+  const int m = n_biases;
+  if (m <= kLogBiases) {
+    // whoever has a token's first bias adds up all of them
+    for (int k = tid; k < m; k += kLogThreads) {
+      const int v = bias_token[k];
+      float sum = bias_value[k];
+      bool first = true;
+      for (int o = 0; o < m; ++o) {
+        if (bias_token[o] != v) continue;
+        if (o < k) first = false;
+        if (o > k) sum += bias_value[o];
+      }
+      if (first && open(v)) out[v] = from_f32<TO>(penalised(v) + sum);
+    }
+  } else {
+    // more than the list holds: the same on the row's own list
+    for (int64_t k = tid; k < r.n_bias; k += kLogThreads) {
+      const uint32_t id = (uint32_t)__ldg(r.bias_ids + k);
+      if (id - low >= (uint32_t)n) continue;
+      float sum = __ldg(r.bias_values + k);
+      bool first = true;
+      for (int64_t o = 0; o < k && first; ++o) first = (uint32_t)__ldg(r.bias_ids + o) != id;
+      if (!first) continue;
+      for (int64_t o = k + 1; o < r.n_bias; ++o)
+        if ((uint32_t)__ldg(r.bias_ids + o) == id) sum += __ldg(r.bias_values + o);
+      const int v = (int)(id - low);
+      if (open(v)) out[v] = from_f32<TO>(penalised(v) + sum);
+    }
+  }
 }
 
 }  // namespace
@@ -122,7 +341,8 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
     if (!type_ok(a.logits_type) || !type_ok(a.out_type))
       return fail(BPE_ERR_INVALID_ARG, "bpe_adjust_logits: unknown type");
     if (a.n_rows < 0 || a.n_rows > 65535 || a.n_vocab < 0 || a.n_vocab >= INT32_MAX || a.n_prompt_ids < 0 ||
-        a.output_capacity < 0 || a.output_capacity > (int64_t)kLogCount || a.n_bias < 0 || a.n_masks < 0)
+        a.output_capacity < 0 || a.output_capacity >= (1 << 29) || a.n_bias < 0 || a.n_bias > INT32_MAX ||
+        a.n_masks < 0)
       return fail(BPE_ERR_INVALID_ARG, "bpe_adjust_logits: a size is negative or too large");
     if (a.n_rows == 0 || a.n_vocab == 0) return BPE_OK;
     if (!a.logits || !a.out || (a.prompt_ids && !a.prompt_offsets) || (a.output_ids && !a.output_lens) ||
@@ -144,12 +364,35 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
       return fail(BPE_ERR_INVALID_ARG, "bpe_adjust_logits: in place needs one type and one stride");
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
+    const bool by_bias = a.bias_ids && a.n_bias > 0;
+    const bool table = by_bias || (a.prompt_ids && a.repetition) ||
+                       (a.output_ids && (a.repetition || a.frequency || a.presence));
+    // Tokens of a CTA: long chunks read the history less often and hide its
+    // latency behind a longer pass; short ones spread few rows over more SMs,
+    // and leave room for counts of 32 bits where an output may need them.
+    const bool packed = a.output_capacity <= 0xFFFF;
+    int chunk = packed ? kLogMaxChunk : kLogMaxChunk / 2;
+    while (chunk > kLogMinChunk && a.n_rows * ((a.n_vocab + chunk - 1) / chunk) < 2 * h->n_sms) chunk /= 2;
+    const dim3 grid((unsigned)((a.n_vocab + chunk - 1) / chunk), (unsigned)a.n_rows);
     return with_type(a.logits_type, [&](auto i) {
       return with_type(a.out_type, [&](auto o) -> int {
-        const dim3 grid((unsigned)((a.n_vocab + kLogChunk - 1) / kLogChunk), (unsigned)a.n_rows);
-        k_logits<decltype(i), decltype(o)><<<grid, kLogThreads, 0, st>>>(a, h->d_small);
-        CK(cudaGetLastError());
-        return BPE_OK;
+        using TI = decltype(i);
+        using TO = decltype(o);
+        auto launch = [&](auto with_table, auto with_bias) {
+          constexpr bool kTable = decltype(with_table)::value, kBias = decltype(with_bias)::value;
+          const int smem = kTable ? LogTable::bytes(chunk, a.output_ids != nullptr, packed) : 0;
+          int rc = once_per_device(h->device, [] {
+            return cudaFuncSetAttribute(k_logits<TI, TO, kTable, kBias>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        LogTable::bytes(kLogMaxChunk, true, true));
+          });
+          if (rc) return rc;
+          k_logits<TI, TO, kTable, kBias><<<grid, kLogThreads, smem, st>>>(a, chunk, packed, h->d_small);
+          CK(cudaGetLastError());
+          return (int)BPE_OK;
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        return !table ? launch(No{}, No{}) : by_bias ? launch(Yes{}, Yes{}) : launch(Yes{}, No{});
       });
     });
   });

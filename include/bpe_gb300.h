@@ -465,7 +465,8 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
  * Ids outside [0, n_vocab), offsets that are not monotone in their list,
  * lengths past output_capacity and mask rows past n_masks are left out and
  * reported (BPE_ERR_BAD_INPUT).
- * Sizes: n_rows <= 65535, n_vocab < 2^31 - 1, output_capacity < 2^30.
+ * Sizes: n_rows <= 65535, n_vocab < 2^31 - 1, n_bias < 2^31, output_capacity <
+ * 2^29. No workspace.
  */
 typedef struct bpe_logits_args {
   const void* logits;

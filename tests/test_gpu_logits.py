@@ -154,6 +154,18 @@ def test_long_and_repeated_history(tok, prompt, output, bias, hot):
     assert (call(tok, s) == call(tok, s)).all()
 
 
+@pytest.mark.parametrize("n,vocab,prompt,output,bias,masks,hot", [
+    (400, 9001, 60, 30, 5, 400, None), (80, 32_256, 9000, 50, 0, 0, None), (90, 32_256, 200, 12_000, 300, 3, None),
+    (350, 8200, 3000, 100, 0, 2, 40), (310, 5000, 0, 0, 700, 0, 300), (320, 8000, 40, 0, 0, 1, None)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "f32"), ("f16", "f16")])
+def test_many_rows(tok, n, vocab, prompt, output, bias, masks, hot, dtype, out):
+    s = make(n, vocab, prompt, output, bias, masks, n + vocab, dtype, hot=hot)
+    want, bound = plain(s)
+    assert_close(call(tok, s, dtype=dtypes()[out]), want, bound, "many rows")
+    if dtype == out:
+        assert_close(call(tok, s, out=s["logits"]), want, bound, "many rows in place")
+
+
 def test_one_row_takes_all_of_the_history(tok):
     import torch
     s = make(6, 5000, 100, 20, 20, 0, 9)
