@@ -390,7 +390,7 @@ class Tokenizer:
     # These calls take microseconds on the GPU, so their checks ask each tensor
     # for as little as they can; _refuse finds the words for what failed.
 
-    def _refuse(self, name, t, dtypes, dims=None, size=None):
+    def _refuse(self, name, t, dtypes, size=None, dims=None):
         if t.get_device() != self.device:
             raise ValueError(f"{name}: on {t.device}, the tokenizer is on cuda:{self.device}")
         if t.dtype not in dtypes:
@@ -399,11 +399,10 @@ class Tokenizer:
             raise ValueError(f"{name}: {t.dim()} dimensions, need {dims}")
         raise ValueError(f"{name}: needs {'adjacent elements' if size is None else f'{size} adjacent elements'}")
 
-    def _flat(self, name, t, dtype, size=None):
-        """The address of a one-dimensional tensor without gaps."""
-        if (t.get_device() != self.device or t.dtype is not dtype or t.dim() != 1 or not t.is_contiguous()
-                or (size is not None and t.numel() != size)):
-            self._refuse(name, t, (dtype,), 1, size)
+    def _flat(self, name, t, dtype, size):
+        """The address of a tensor of `size` adjacent elements."""
+        if t.dtype is not dtype or t.get_device() != self.device or t.numel() != size or not t.is_contiguous():
+            self._refuse(name, t, (dtype,), size)
         return t.data_ptr()
 
     def plan_blocks(self, offsets, cached, table, free, block_size: int, n_slots: int | None = None, head=None):
@@ -416,10 +415,10 @@ class Tokenizer:
         least their number (needed with offsets, whose end is on the device).
         Returns (seq_lens int32[n], slots int64[n_slots], positions
         int32[n_slots], info int64[2]: head after the call, blocks lacking)."""
-        import torch
-        i32, i64 = torch.int32, torch.int64
-        if table.get_device() != self.device or table.dtype is not i32 or table.dim() != 2:
-            self._refuse("table", table, (i32,), 2)
+        torch, flat = _torch(), self._flat
+        i32, i64 = _int32, _int64
+        if table.dtype is not i32 or table.get_device() != self.device or table.dim() != 2:
+            self._refuse("table", table, (i32,), dims=2)
         n, width = table.shape
         stride, step = table.stride()
         if step != 1 and width > 1:
@@ -428,19 +427,19 @@ class Tokenizer:
             if offsets is not None:
                 raise ValueError("n_slots: the number of new tokens (or more) is needed with offsets")
             n_slots = n
-        p_offsets = None if offsets is None else self._flat("offsets", offsets, i64, n + 1)
-        p_cached = None if cached is None else self._flat("cached", cached, i32, n)
-        p_free = self._flat("free", free, i32)
-        p_head = None if head is None else self._flat("head", head, i64, 1)
-        dev = table.device
-        seq_lens = torch.empty(n, dtype=i32, device=dev)
-        slots = torch.empty(n_slots, dtype=i64, device=dev)
-        positions = torch.empty(n_slots, dtype=i32, device=dev)
-        info = torch.empty(2, dtype=i64, device=dev)
-        rc = self._lib.bpe_plan_blocks(self.handle, p_offsets, p_cached, n, block_size, p_free, free.numel(), p_head,
+        n_free = free.numel()
+        p_offsets = None if offsets is None else flat("offsets", offsets, i64, n + 1)
+        p_cached = None if cached is None else flat("cached", cached, i32, n)
+        p_free = flat("free", free, i32, n_free)
+        p_head = None if head is None else flat("head", head, i64, 1)
+        empty, dev = torch.empty, table.device
+        seq_lens = empty(n, dtype=i32, device=dev)
+        slots = empty(n_slots, dtype=i64, device=dev)
+        positions = empty(n_slots, dtype=i32, device=dev)
+        info = empty(2, dtype=i64, device=dev)
+        rc = self._lib.bpe_plan_blocks(self.handle, p_offsets, p_cached, n, block_size, p_free, n_free, p_head,
                                        table.data_ptr(), width, stride, seq_lens.data_ptr(), slots.data_ptr(),
-                                       positions.data_ptr(), n_slots, info.data_ptr(),
-                                       torch._C._cuda_getCurrentRawStream(self.device))
+                                       positions.data_ptr(), n_slots, info.data_ptr(), _raw_stream(self.device))
         if rc:
             _check(rc)
         return seq_lens, slots, positions, info
@@ -456,12 +455,11 @@ class Tokenizer:
         values float32[m], offsets int64[n + 1]); mask: int32 or uint32
         [masks, ceil(vocab / 32)], bit v % 32 of word v / 32 set for an
         allowed token; mask_rows: int32[n], each row's mask or -1."""
-        import torch
-        i32, i64, f32 = torch.int32, torch.int64, torch.float32
-        types, flat = _types(), self._flat
+        torch, types, flat = _torch(), _type_codes, self._flat
+        i32, i64, f32 = _int32, _int64, _float32
         code = types.get(logits.dtype)
-        if logits.get_device() != self.device or code is None or logits.dim() != 2:
-            self._refuse("logits", logits, types, 2)
+        if code is None or logits.get_device() != self.device or logits.dim() != 2:
+            self._refuse("logits", logits, types, dims=2)
         n, vocab = logits.shape
         stride, step = logits.stride()
         if step != 1 and vocab > 1:
@@ -474,22 +472,23 @@ class Tokenizer:
             out_stride = vocab
         else:
             if out.get_device() != self.device or out.dim() != 2:
-                self._refuse("out", out, types, 2)
+                self._refuse("out", out, types, dims=2)
             out_stride, step = out.stride()
             if out.shape != logits.shape or (step != 1 and vocab > 1):
                 raise ValueError("out: needs the shape of logits, the elements of a row adjacent")
         out_code = types.get(out.dtype)
         if out_code is None:
-            self._refuse("out", out, types, 2)
+            self._refuse("out", out, types)
         p_ids = p_off = o_ids = o_lens = b_ids = b_values = b_off = p_mask = p_rows = 0
         n_prompt = o_stride = o_cap = n_bias = m_stride = n_masks = 0
         if prompt is not None:
             ids, offsets = prompt
-            p_ids, n_prompt, p_off = flat("prompt ids", ids, i32), ids.numel(), flat("prompt offsets", offsets, i64, n + 1)
+            n_prompt = ids.numel()
+            p_ids, p_off = flat("prompt ids", ids, i32, n_prompt), flat("prompt offsets", offsets, i64, n + 1)
         if output is not None:
             ids, lens = output
-            if ids.get_device() != self.device or ids.dtype is not i32 or ids.dim() != 2:
-                self._refuse("output ids", ids, (i32,), 2)
+            if ids.dtype is not i32 or ids.get_device() != self.device or ids.dim() != 2:
+                self._refuse("output ids", ids, (i32,), dims=2)
             o_stride, step = ids.stride()
             rows, o_cap = ids.shape
             if rows != n or (step != 1 and o_cap > 1):
@@ -501,12 +500,12 @@ class Tokenizer:
         if bias is not None:
             ids, values, offsets = bias
             n_bias = ids.numel()
-            b_ids, b_values = flat("bias ids", ids, i32), flat("bias values", values, f32, n_bias)
+            b_ids, b_values = flat("bias ids", ids, i32, n_bias), flat("bias values", values, f32, n_bias)
             b_off = flat("bias offsets", offsets, i64, n + 1)
         if mask is not None:
-            if (mask.get_device() != self.device or (mask.dtype is not i32 and mask.dtype is not torch.uint32)
-                    or mask.dim() != 2):
-                self._refuse("mask", mask, (i32, torch.uint32), 2)
+            if (mask.dtype is not i32 and mask.dtype is not torch.uint32) or mask.get_device() != self.device \
+                    or mask.dim() != 2:
+                self._refuse("mask", mask, (i32, torch.uint32), dims=2)
             n_masks, words = mask.shape
             m_stride, step = mask.stride()
             if words < (vocab + 31) // 32 or (step != 1 and words > 1):
@@ -518,56 +517,50 @@ class Tokenizer:
             self.handle,
             _pack_logits(logits.data_ptr(), out.data_ptr(), code, out_code, stride, out_stride, n, vocab, p_ids, p_off,
                          n_prompt, o_ids, o_lens, o_stride, o_cap, p_rep, p_freq, p_pres, b_ids, b_values, b_off,
-                         n_bias, p_mask, m_stride, n_masks, p_rows),
-            torch._C._cuda_getCurrentRawStream(self.device))
+                         n_bias, p_mask, m_stride, n_masks, p_rows), _raw_stream(self.device))
         if rc:
             _check(rc)
         return out
-
-    def _packed_ids(self, ids):
-        import torch
-        if ids.get_device() != self.device or ids.dtype is not torch.int32:
-            self._refuse("ids", ids, (torch.int32,))
-        return ids if ids.is_contiguous() else ids.contiguous()
 
     def embed(self, ids, weight, scale: float = 1.0, skip_id: int | None = None, dtype=None, out=None):
         """scale * weight[ids] in weight's type, or in ``dtype``: ids int32 of
         any shape, weight [rows, dim] in 32 or 16 bits with any row stride.
         Tokens equal to skip_id get zeros. Differentiable with respect to
         weight (its gradient runs embed_grad) unless ``out`` is given."""
-        import torch
-        types = _types()
+        torch, types, device = _torch(), _type_codes, self.device
         code = types.get(weight.dtype)
-        if weight.get_device() != self.device or code is None or weight.dim() != 2:
-            self._refuse("weight", weight, types, 2)
-        ids = self._packed_ids(ids)
+        if code is None or weight.get_device() != device or weight.dim() != 2:
+            self._refuse("weight", weight, types, dims=2)
+        if ids.dtype is not _int32 or ids.get_device() != device:
+            self._refuse("ids", ids, (_int32,))
+        if not ids.is_contiguous():
+            ids = ids.contiguous()
         n_rows, dim = weight.shape
+        stride, step = weight.stride()
+        shape = (*ids.shape, dim)
+        out_stride = dim
         if out is None:
-            dtype = dtype or weight.dtype
             if weight.requires_grad and torch.is_grad_enabled():
-                return _embed_function().apply(self, ids, weight, scale, skip_id, dtype)
-            out = torch.empty((*ids.shape, dim), dtype=dtype, device=weight.device)
-            out_stride = dim
+                return _embed_function().apply(self, ids, weight, scale, skip_id, dtype or weight.dtype)
+            out = torch.empty(shape, dtype=dtype or weight.dtype, device=weight.device)
         else:
-            if out.get_device() != self.device or out.shape != (*ids.shape, dim):
+            if out.get_device() != device or out.shape != shape:
                 raise ValueError("out: needs the shape of ids and weight's columns, on the tokenizer's device")
-            out_stride = dim
-            if out.dim() == 2:
-                out_stride, step = out.stride()
-                if step != 1 and dim > 1:
+            if len(shape) == 2:
+                out_stride, out_step = out.stride()
+                if out_step != 1 and dim > 1:
                     raise ValueError("out: the elements of a row must be adjacent")
             elif not out.is_contiguous():
                 raise ValueError("out: needs to be contiguous where ids is not one-dimensional")
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)
-        stride, step = weight.stride()
         if step != 1 and dim > 1:
             weight = weight.contiguous()
             stride = dim
         rc = self._lib.bpe_embed(self.handle, ids.data_ptr(), ids.numel(), weight.data_ptr(), code, n_rows, dim, stride,
                                  scale, NO_ID if skip_id is None else skip_id, out.data_ptr(), out_code, out_stride,
-                                 torch._C._cuda_getCurrentRawStream(self.device))
+                                 _raw_stream(device))
         if rc:
             _check(rc)
         return out
@@ -577,17 +570,20 @@ class Tokenizer:
         """The gradient [n_rows, dim] of embed's weight for the gradient
         ``grad`` [*ids.shape, dim] of its result, in grad's type or in
         ``dtype``, or written into (accumulate: added to) ``out``."""
-        import torch
-        types = _types()
+        torch, types, device = _torch(), _type_codes, self.device
         code = types.get(grad.dtype)
-        if grad.get_device() != self.device or code is None:
+        if code is None or grad.get_device() != device:
             self._refuse("grad", grad, types)
-        ids = self._packed_ids(ids)
+        if ids.dtype is not _int32 or ids.get_device() != device:
+            self._refuse("ids", ids, (_int32,))
+        if not ids.is_contiguous():
+            ids = ids.contiguous()
         n = ids.numel()
-        if grad.shape[:-1] != ids.shape:
+        shape = grad.shape
+        dim = shape[-1]
+        if shape[:-1] != ids.shape:
             raise ValueError("grad: needs the shape of ids and one more dimension")
-        dim = grad.shape[-1]
-        if grad.dim() != 2:
+        if len(shape) != 2:
             grad = grad.reshape(n, dim)
         stride, step = grad.stride()
         if step != 1 and dim > 1:
@@ -599,17 +595,17 @@ class Tokenizer:
             out = torch.empty((n_rows, dim), dtype=dtype or grad.dtype, device=grad.device)
             out_stride = dim
         else:
-            if out.get_device() != self.device or out.dim() != 2:
-                self._refuse("out", out, types, 2)
+            if out.get_device() != device or out.dim() != 2:
+                self._refuse("out", out, types, dims=2)
             out_stride, step = out.stride()
             if out.shape != (n_rows, dim) or (step != 1 and dim > 1):
                 raise ValueError("out: needs n_rows rows of grad's columns, the elements of a row adjacent")
         out_code = types.get(out.dtype)
         if out_code is None:
-            self._refuse("out", out, types, 2)
+            self._refuse("out", out, types)
         rc = self._lib.bpe_embed_grad(self.handle, ids.data_ptr(), n, grad.data_ptr(), code, stride, scale,
                                       NO_ID if skip_id is None else skip_id, n_rows, dim, out.data_ptr(), out_code,
-                                      out_stride, accumulate, torch._C._cuda_getCurrentRawStream(self.device))
+                                      out_stride, accumulate, _raw_stream(device))
         if rc:
             _check(rc)
         return out
@@ -619,14 +615,20 @@ class Tokenizer:
 # a tenth of the time of filling a LogitsArgs field by field
 _pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
-_type_codes = {}
+_type_codes = {}  # torch dtype -> BPE_* code
+_torch_module = _int32 = _int64 = _float32 = _raw_stream = None
 
 
-def _types():
-    if not _type_codes:
+def _torch():
+    """torch, imported on first use, with what the calls above take from it."""
+    global _torch_module, _int32, _int64, _float32, _raw_stream
+    if _torch_module is None:
         import torch
+        _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
+        _raw_stream = torch._C._cuda_getCurrentRawStream
         _type_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
-    return _type_codes
+        _torch_module = torch
+    return _torch_module
 
 
 def _embed_function():

@@ -12,15 +12,15 @@
 
 namespace {
 
-constexpr int kLogThreads = 512;
+constexpr int kLogThreads = 256;
 constexpr int kLogWarps = kLogThreads / 32;
 constexpr int kLogGroup = 8;         // tokens of a vector
 constexpr int kLogAhead = 2;         // vectors of a thread in flight
 constexpr int kLogIds = 2;           // 16-byte loads of ids of a thread in flight
 constexpr int kLogMinChunk = 2048;   // tokens of a CTA
-constexpr int kLogMaxChunk = 16384;
-constexpr int kLogList = 2048;       // concerned tokens that a CTA lists at once
-constexpr int kLogBiases = 1024;     // biases of a chunk that it lists
+constexpr int kLogMaxChunk = 8192;
+constexpr int kLogList = 1024;       // concerned tokens that a CTA lists at once
+constexpr int kLogBiases = 512;     // biases of a chunk that it lists
 
 // What a row's history says about a chunk, in shared memory: a bit for each
 // token that occurs in it, and the times it occurs in the output, in 16 bits
@@ -192,7 +192,7 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // for each id), warps that gather while others pass (too few to hide it), and
 // a second launch or the last CTA of a row for the gathering.
 template <class TI, class TO, bool kTable, bool kBias>
-__global__ void __launch_bounds__(kLogThreads, 3) k_logits(bpe_logits_args a, int chunk, bool packed, DevSmall* small) {
+__global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, int chunk, bool packed, DevSmall* small) {
   extern __shared__ __align__(16) uint32_t log_smem[];
   __shared__ uint16_t list[kTable ? kLogList : 1];
   __shared__ uint16_t bias_token[kBias ? kLogBiases : 1];
@@ -371,7 +371,7 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
     // latency behind a longer pass; short ones spread few rows over more SMs,
     // and leave room for counts of 32 bits where an output may need them.
     const bool packed = a.output_capacity <= 0xFFFF;
-    int chunk = packed ? kLogMaxChunk : kLogMaxChunk / 2;
+    int chunk = table && !packed ? kLogMaxChunk / 2 : kLogMaxChunk;
     while (chunk > kLogMinChunk && a.n_rows * ((a.n_vocab + chunk - 1) / chunk) < 2 * h->n_sms) chunk /= 2;
     const dim3 grid((unsigned)((a.n_vocab + chunk - 1) / chunk), (unsigned)a.n_rows);
     return with_type(a.logits_type, [&](auto i) {
