@@ -1499,6 +1499,9 @@ int bpe_destroy(bpe_handle* h) {
   }
   if (h->s_h2d) cudaStreamDestroy(h->s_h2d);
   if (h->s_d2h) cudaStreamDestroy(h->s_d2h);
+  if (h->s_side) cudaStreamDestroy(h->s_side);
+  if (h->ev_fork) cudaEventDestroy(h->ev_fork);
+  if (h->ev_join) cudaEventDestroy(h->ev_join);
   if (h->h_totals) cudaFreeHost(h->h_totals);
   if (h->h_small) cudaFreeHost(h->h_small);
   delete h;

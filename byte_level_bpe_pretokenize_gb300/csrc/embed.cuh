@@ -93,15 +93,9 @@ __device__ void fill_absent(const FillArgs& a, int64_t r0, int64_t r1, FillSmem&
   for (int b = tid; b < kFillPage / 16; b += threads) reinterpret_cast<uint4*>(sm.zeros)[b] = make_uint4(0, 0, 0, 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
-  constexpr int kBatch = 8;
-  for (int64_t i0 = tid; i0 < a.n; i0 += kBatch * threads) {
-    int32_t id[kBatch];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) id[q] = i0 + q * threads < a.n ? __ldg(a.ids + i0 + q * threads) : -1;
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q)
-      if (id[q] >= r0 && id[q] < r1 && id[q] != a.skip_id) sm.met[id[q] - r0] = 1;
-  }
+  each_id<4>(a.ids, a.n, tid, threads, [&](uint32_t id) {
+    if (id - (uint32_t)r0 < (uint32_t)(r1 - r0) && (int32_t)id != a.skip_id) sm.met[id - (uint32_t)r0] = 1;
+  });
   __syncthreads();
   const uint32_t page = (uint32_t)__cvta_generic_to_shared(sm.zeros);
   for (int64_t r = r0 + tid; r < r1; r += threads) {
@@ -268,6 +262,96 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
   }
 }
 
+// Up to kRankTokens tokens: the blocks share the tokens out, and each finds the
+// places of its own. It counts all tokens into buckets of neighbouring rows,
+// which gives each bucket's first place, and in its token's bucket it counts
+// the keys below the token's. All blocks count the same, but none waits for
+// another: the passes of a sort do, twice each.
+constexpr int kRankEach = 24;  // tokens of a thread
+constexpr int kRankThreads = 512;
+constexpr int kRankTokens = kRankEach * kRankThreads;
+constexpr int kRankOwn = 64;   // tokens whose place a block finds
+constexpr int kRankShare = kRankThreads / kRankOwn;
+constexpr int kRankBits = 10;  // buckets: two a thread
+constexpr int kRankBuckets = 1 << kRankBits;
+
+struct RankArgs {
+  const int32_t* ids;
+  int n;
+  uint32_t n_rows, by;  // by: a row times this, plus the token, sorts as (row, token)
+  int32_t skip_id, shift;  // shift: the rows of a bucket, as a power of two
+  uint2* sorted;
+  DevSmall* small;
+};
+
+__global__ void __launch_bounds__(kRankThreads) k_emb_rank(RankArgs a) {
+  static_assert(kRankBuckets == 2 * kRankThreads);
+  extern __shared__ uint32_t rank_keys[];  // [n] by bucket
+  __shared__ int next[kRankBuckets];       // a bucket's next place: once all are taken, its end
+  __shared__ uint32_t mine[kRankOwn];
+  __shared__ int part[kRankShare][kRankOwn], warp_sum[kRankThreads / 32];
+  let_next_begin();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = (int)blockIdx.x * kRankOwn;
+  int32_t id[kRankEach];
+#pragma unroll
+  for (int q = 0; q < kRankEach; ++q) id[q] = tid + q * kRankThreads < a.n ? __ldg(a.ids + tid + q * kRankThreads) : 0;
+  next[tid] = next[tid + kRankThreads] = 0;
+  __syncthreads();
+  uint32_t row[kRankEach];
+#pragma unroll
+  for (int q = 0; q < kRankEach; ++q) {
+    const int i = tid + q * kRankThreads;
+    const bool ok = id[q] != a.skip_id && (uint32_t)id[q] < a.n_rows;
+    row[q] = ok ? (uint32_t)id[q] : a.n_rows;
+    if (i >= a.n) continue;
+    atomicAdd(&next[row[q] >> a.shift], 1);
+    if (i >= first && i < first + kRankOwn) {
+      if (!ok && id[q] != a.skip_id) atomicOr(&a.small->op_status, kStBadInput);
+      mine[i - first] = row[q];
+    }
+  }
+  __syncthreads();
+  const int c0 = next[2 * tid], c1 = next[2 * tid + 1];
+  int upto = c0 + c1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRankThreads / 32; ++w)
+    if (w < warp) upto += warp_sum[w];
+  next[2 * tid] = upto - c0 - c1;
+  next[2 * tid + 1] = upto - c1;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kRankEach; ++q) {
+    const int i = tid + q * kRankThreads;
+    if (i < a.n) rank_keys[atomicAdd(&next[row[q] >> a.shift], 1)] = row[q] * a.by + (uint32_t)i;
+  }
+  __syncthreads();
+  const int own = tid % kRankOwn, share = tid / kRankOwn, i = first + own;
+  int begin = 0, below = 0;
+  uint32_t r = 0;
+  if (i < a.n) {
+    r = mine[own];
+    const uint32_t bucket = r >> a.shift, k = r * a.by + (uint32_t)i;
+    begin = bucket > 0 ? next[bucket - 1] : 0;
+    const int end = next[bucket];
+#pragma unroll 4
+    for (int j = begin + share; j < end; j += kRankShare) below += rank_keys[j] < k;
+  }
+  part[share][own] = below;
+  __syncthreads();
+  if (share == 0 && i < a.n) {
+#pragma unroll
+    for (int q = 1; q < kRankShare; ++q) below += part[q][own];
+    a.sorted[begin + below] = make_uint2(r, (uint32_t)i);
+  }
+}
+
 // ------------------------------------------------------------------- sum --
 
 constexpr int kSumWarps = 8;
@@ -275,7 +359,7 @@ constexpr int kSumCols = 512;     // columns of a block
 constexpr int kSumMaxRun = 16;    // tokens of a warp, at most
 constexpr int kSmallTokens = 512; // most tokens of the single launch
 constexpr int64_t kSmallRows = (1ll << 32) / kSmallTokens - 1;  // and rows: a key and a token fit 32 bits
-constexpr int kSumRing = 8192;    // bytes of a warp's tokens in flight
+constexpr int kSumRing = 8320;    // bytes of a warp's tokens in flight
 
 template <class TG, class TW>
 struct SumArgs {
@@ -332,8 +416,9 @@ __device__ __forceinline__ void add_vec(float (&acc)[V], const Vec<T, V>& v) {
 template <class TG, class TW, int V>
 __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2* sorted, unsigned char* sum_smem) {
   constexpr int kSlabs = kSumCols / (32 * V);
-  constexpr bool kRing = V * sizeof(TG) >= 4;  // an asynchronous copy moves 4 bytes at least
-  constexpr int kAhead = kRing ? kSumRing / (kSumCols * (int)sizeof(TG)) : 2;  // tokens in flight
+  constexpr bool kVectors = V * sizeof(TG) == 16;
+  constexpr int kSlot = kSumCols * (int)sizeof(TG) + (kVectors ? 0 : 16);  // of a token in the ring
+  constexpr int kAhead = kSumRing / kSlot;                                 // tokens in flight
   __shared__ __align__(16) float part[kSumWarps][2][kSumCols];
   __shared__ int32_t part_key[kSumWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -382,26 +467,18 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[s][e] = 0.f;
   };
-  if constexpr (kRing) {
+  if constexpr (kVectors) {
     // Each lane copies its own vectors into its warp's ring and reads them
     // back itself, so no barrier is needed; a token is one group of copies.
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * kSumRing + lane * V * (int)sizeof(TG);
-    constexpr uint32_t kSlot = kSumCols * sizeof(TG), kStep = 32 * V * sizeof(TG);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * kSumRing + lane * 16;
     auto fetch = [&](int j, uint32_t slot) {
       if (j < len) {
         const TG* g = grad + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j) * a.grad_stride;
 #pragma unroll
         for (int s = 0; s < kSlabs; ++s)
-          if (s * 32 * V < cols) {
-            if constexpr (V * sizeof(TG) == 16)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + slot + s * kStep),
-                           "l"(g + s * 32 * V)
-                           : "memory");
-            else
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ring + slot + s * kStep),
-                           "l"(g + s * 32 * V)
-                           : "memory");
-          }
+          if (s * 32 * V < cols)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + slot + s * 512), "l"(g + s * 32 * V)
+                         : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -414,7 +491,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
       Vec<TG, V> v[kSlabs];
 #pragma unroll
       for (int s = 0; s < kSlabs; ++s)
-        v[s] = *reinterpret_cast<const Vec<TG, V>*>(__cvta_shared_to_generic(ring + slot + s * kStep));
+        v[s] = *reinterpret_cast<const Vec<TG, V>*>(__cvta_shared_to_generic(ring + slot + s * 512));
       if (key != row) next_row(key);
 #pragma unroll
       for (int s = 0; s < kSlabs; ++s) add_vec<TG, V>(acc[s], v[s]);
@@ -423,24 +500,49 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    for (int j = 0; j < len; j += kAhead) {
-      Vec<TG, V> v[kAhead][kSlabs];
-#pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        const int64_t token = __shfl_sync(0xFFFFFFFFu, mine.y, (j + q) & 31);
-#pragma unroll
-        for (int s = 0; s < kSlabs; ++s)
-          if (j + q < len && s * 32 * V < cols) v[q][s].load(grad + token * a.grad_stride + s * 32 * V);
+    // Rows that are not aligned: the warp copies the 16-byte granules that a
+    // token's columns lie in, and the lanes read theirs from inside them.
+    unsigned char* ring = sum_smem + warp * kSumRing;
+    const int bytes = min(kSumCols, a.dim - col0) * (int)sizeof(TG);
+    const char* from0 = reinterpret_cast<const char*>(a.grad + col0);
+    auto source = [&](int j) {
+      return from0 + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j & 31) * a.grad_stride * (int64_t)sizeof(TG);
+    };
+    auto fetch = [&](int j, int slot) {
+      const char* from = source(j);
+      if (j < len) {
+        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + slot * kSlot);
+        for (int g = lane * 16; g < off + bytes; g += 512) {
+          const int size = min(16, off + bytes - g);  // nothing past the row is read
+          const char* at = from - off + g;
+          if (at < reinterpret_cast<const char*>(a.grad)) {  // nor before the first one
+            for (int e = off; e < size; e += sizeof(TG))
+              *reinterpret_cast<TG*>(ring + slot * kSlot + e) = *reinterpret_cast<const TG*>(at + e);
+            continue;
+          }
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + g), "l"(at), "r"(size) : "memory");
+        }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        if (j + q >= len) break;
-        const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, (j + q) & 31);
-        if (key != row) next_row(key);
+    for (int j = 0; j < kAhead; ++j) fetch(j, j);
+    int slot = 0;
+    for (int j = 0; j < len; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      __syncwarp();
+      const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
+      const TG* v = reinterpret_cast<const TG*>(ring + slot * kSlot + (reinterpret_cast<uintptr_t>(source(j)) & 15)) + lane;
+      if (key != row) next_row(key);
 #pragma unroll
-        for (int s = 0; s < kSlabs; ++s) add_vec<TG, V>(acc[s], v[q][s]);
-      }
+      for (int s = 0; s < kSlabs; ++s)
+        if (s * 32 < cols) acc[s][0] += to_f32(v[s * 32]);
+      __syncwarp();
+      fetch(j + kAhead, slot);
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   // a run of one row has only the first part, an empty run none (key -1)
   if (len > 0) stash(begun ? 1 : 0);
@@ -519,7 +621,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a,
       const int32_t id = __ldg(f.ids + i);
       const bool ok = id != f.skip_id && emb_row_ok(id, a.n_rows);
       if (!ok && id != f.skip_id && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(&small->op_status, kStBadInput);
-      k = (ok ? (uint32_t)id : (uint32_t)a.n_rows) * kSmallTokens + i;
+      k = (ok ? (uint32_t)id : (uint32_t)a.n_rows) * kSmallTokens + (uint32_t)i;
     }
     key[i] = k;
   }
@@ -690,15 +792,41 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     f.row_bytes = dim * f.element;
     f.stride_bytes = grad_weight_stride * f.element;
     const bool small = n_ids <= kSmallTokens && n_rows < kSmallRows;
-    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of the sort: a cluster's barriers cost more than a few tokens gain
+    const bool rank = !small && n_ids <= kRankTokens && (n_rows + 1) * n_ids < (1ll << 32);
+    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of a sort: a cluster's barriers cost more than a few tokens gain
+    // Zeros beside the kernels that find and sum the tokens, fewer blocks where
+    // each would have under 32 KB to write. Where they take longer than the
+    // sort they go on a stream of their own, so that the sums need not wait
+    // for them; that costs four calls on the host.
+    const bool aside = !small && !rank && !accumulate && n_rows * f.row_bytes >= (64ll << 20);
     int64_t fillers = 0;
     if (!accumulate) {
-      // the SMs beside the sort, fewer where each would have under 32 KB to write
-      fillers = std::min<int64_t>(small ? h->n_sms : h->n_sms - ctas, std::max<int64_t>(1, n_rows * f.row_bytes / 32768));
+      fillers = std::min<int64_t>(small || rank || aside ? h->n_sms : h->n_sms - ctas,
+                                  std::max<int64_t>(1, n_rows * f.row_bytes / 32768));
       f.row_step = std::min<int64_t>(kFillRows, (n_rows + fillers - 1) / fillers);
     }
     int passes = 1;
-    if (!small) {
+    if (aside) {
+      if (!h->s_side) {
+        int low = 0, high = 0;
+        CK(cudaDeviceGetStreamPriorityRange(&low, &high));
+        CK(cudaStreamCreateWithPriority(&h->s_side, cudaStreamNonBlocking, low));
+      }
+      if (!h->ev_fork) CK(cudaEventCreateWithFlags(&h->ev_fork, cudaEventDisableTiming));
+      if (!h->ev_join) CK(cudaEventCreateWithFlags(&h->ev_join, cudaEventDisableTiming));
+      CK(cudaEventRecord(h->ev_fork, st));
+    }
+    if (rank) {
+      int shift = 0;
+      while (n_rows >> shift >= kRankBuckets) ++shift;
+      const RankArgs q{d_ids, (int)n_ids, (uint32_t)n_rows, (uint32_t)n_ids, skip_id, shift, ping[0], h->d_small};
+      rc = once_per_device(h->device, [] {
+        return cudaFuncSetAttribute(k_emb_rank, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankTokens * 4);
+      });
+      if (rc) return rc;
+      k_emb_rank<<<(unsigned)((n_ids + kRankOwn - 1) / kRankOwn), kRankThreads, (size_t)n_ids * 4, st>>>(q);
+      CK(cudaGetLastError());
+    } else if (!small) {
       SortArgs q{};
       q.ids = d_ids;
       q.n = n_ids;
@@ -731,7 +859,14 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       CK(cudaLaunchKernelEx(&cfg, k_emb_sort, q));
-      if (fillers) CK(launch_after(k_emb_fill, dim3((unsigned)fillers), kFillThreads, 0, st, f));
+    }
+    if (aside) {
+      CK(cudaStreamWaitEvent(h->s_side, h->ev_fork, 0));
+      k_emb_fill<<<(unsigned)fillers, kFillThreads, 0, h->s_side>>>(f);
+      CK(cudaGetLastError());
+      CK(cudaEventRecord(h->ev_join, h->s_side));
+    } else if (fillers && !small) {
+      CK(launch_after(k_emb_fill, dim3((unsigned)fillers), kFillThreads, 0, st, f));
     }
     if (n_chunks + fillers == 0) return BPE_OK;
     return with_type(grad_out_type, [&](auto g_) {
@@ -743,7 +878,7 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
                                 grad_weight_stride, accumulate, partial};
         auto launch = [&](auto width) {
           constexpr int V = decltype(width)::value;
-          constexpr size_t kSmem = V * sizeof(TG) >= 4 ? kSumWarps * kSumRing : 0;
+          constexpr size_t kSmem = kSumWarps * kSumRing;
           constexpr size_t kSmallSmem = std::max(kSmem, sizeof(FillSmem));
           int rc = once_per_device(h->device, [=] {
             cudaError_t e = cudaFuncSetAttribute(k_emb_sum<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -762,15 +897,15 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
             CK(launch_after(k_emb_sum<TG, TW, V>, grid, kSumWarps * 32, kSmem, st, a));
           }
           if (n_chunks > 1) CK(launch_after(k_emb_join<TG, TW, V>, grid, kSumWarps * 32, 0, st, a, !small));
+          if (aside) CK(cudaStreamWaitEvent(st, h->ev_join, 0));
           return (int)BPE_OK;
         };
         auto fits = [&](int64_t V) {
           return dim % V == 0 && vec_ok(d_grad_out, grad_out_stride, sizeof(TG), V) &&
                  vec_ok(d_grad_weight, grad_weight_stride, sizeof(TW), V);
         };
-        constexpr int kWide = 16 / (int)sizeof(TG), kNarrow = 4 / (int)sizeof(TG);
+        constexpr int kWide = 16 / (int)sizeof(TG);
         if (fits(kWide)) return launch(std::integral_constant<int, kWide>{});
-        if (fits(kNarrow)) return launch(std::integral_constant<int, kNarrow>{});
         return launch(std::integral_constant<int, 1>{});
       });
     });

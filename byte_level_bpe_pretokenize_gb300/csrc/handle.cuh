@@ -102,6 +102,9 @@ struct bpe_handle {
   } slot[kHostSlots];
   int64_t slot_bytes = 0, slot_docs = 0;  // capacity of each slot
   cudaStream_t s_h2d = nullptr, s_d2h = nullptr;
+  // bpe_embed_grad: zeros written beside its other kernels
+  cudaStream_t s_side = nullptr;
+  cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
   int64_t* h_totals = nullptr;  // pinned, one per slice
   int64_t* d_totals = nullptr;  // the same memory as the device addresses it
   int64_t h_totals_cap = 0;

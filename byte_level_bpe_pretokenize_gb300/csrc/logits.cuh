@@ -90,35 +90,6 @@ __device__ __forceinline__ LogRow log_row(const bpe_logits_args& a, int64_t b, b
   return r;
 }
 
-// f(id) for each id of a list; whole 16-byte vectors of ids are loaded as such,
-// several at a time.
-template <class F>
-__device__ __forceinline__ void log_each(const int32_t* ids, int64_t count, F f) {
-  const int tid = threadIdx.x;
-  const int64_t head = min((int64_t)((-reinterpret_cast<uintptr_t>(ids) & 15) / 4), count);
-  const int64_t vecs = (count - head) / 4, tail = head + vecs * 4;
-  // at most three ids before the vectors and three after
-  const int64_t edge = tid < head ? tid : tail + tid - head;
-  const bool has_edge = edge < count;
-  const uint32_t edge_id = has_edge ? (uint32_t)__ldg(ids + edge) : 0;
-  const uint4* from = reinterpret_cast<const uint4*>(ids + head);
-  for (int64_t j = tid; j < vecs; j += kLogIds * kLogThreads) {
-    uint4 id[kLogIds];
-#pragma unroll
-    for (int q = 0; q < kLogIds; ++q)
-      if (j + q * kLogThreads < vecs) id[q] = __ldg(from + j + q * kLogThreads);
-#pragma unroll
-    for (int q = 0; q < kLogIds; ++q) {
-      if (j + q * kLogThreads >= vecs) break;
-      f(id[q].x);
-      f(id[q].y);
-      f(id[q].z);
-      f(id[q].w);
-    }
-  }
-  if (has_edge) f(edge_id);
-}
-
 // The bits of the tokens from v on, 8 of them at least; `words` of the mask may
 // be read.
 __device__ __forceinline__ uint32_t log_open(const uint32_t* mask, int v, int words) {
@@ -210,11 +181,11 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
     if (!kTable || !r.concerned) return r.mask;
     t.clear(chunk, a.output_ids != nullptr);
     __syncthreads();
-    log_each(r.prompt, r.n_prompt, [&](uint32_t id) {
+    each_id<kLogIds>(r.prompt, r.n_prompt, tid, kLogThreads, [&](uint32_t id) {
       if (id - low < (uint32_t)n) t.see((int)(id - low));
       bad |= id >= vocab;
     });
-    log_each(r.output, r.n_output, [&](uint32_t id) {
+    each_id<kLogIds>(r.output, r.n_output, tid, kLogThreads, [&](uint32_t id) {
       if (id - low < (uint32_t)n) {
         t.see((int)(id - low));
         t.count((int)(id - low));

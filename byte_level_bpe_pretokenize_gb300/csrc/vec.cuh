@@ -41,6 +41,34 @@ struct __align__(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Vec {
   }
 };
 
+// f(id) for each id of a list, by `threads` threads of which this is tid;
+// whole 16-byte vectors of ids are loaded as such, kLoads at a time.
+template <int kLoads, class F>
+__device__ __forceinline__ void each_id(const int32_t* ids, int64_t count, int tid, int threads, F f) {
+  const int64_t head = min((int64_t)((-reinterpret_cast<uintptr_t>(ids) & 15) / 4), count);
+  const int64_t vecs = (count - head) / 4, tail = head + vecs * 4;
+  // at most three ids before the vectors and three after
+  const int64_t edge = tid < head ? tid : tail + tid - head;
+  const bool has_edge = edge < count;
+  const uint32_t edge_id = has_edge ? (uint32_t)__ldg(ids + edge) : 0;
+  const uint4* from = reinterpret_cast<const uint4*>(ids + head);
+  for (int64_t j = tid; j < vecs; j += kLoads * threads) {
+    uint4 id[kLoads];
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      if (j + q * threads < vecs) id[q] = __ldg(from + j + q * threads);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      if (j + q * threads >= vecs) break;
+      f(id[q].x);
+      f(id[q].y);
+      f(id[q].z);
+      f(id[q].w);
+    }
+  }
+  if (has_edge) f(edge_id);
+}
+
 // Whether V elements of `size` bytes at every multiple of V from p, and from p
 // plus multiples of stride elements, are aligned for Vec.
 inline bool vec_ok(const void* p, int64_t stride, int64_t size, int64_t V) {

@@ -207,6 +207,31 @@ def test_gradient_of_many_tokens(tok, n):
     assert_close(tok.embed_grad(ids, g, 5000), want, bound, "many tokens")
 
 
+@pytest.mark.parametrize("grad,weight,dim", [("bf16", "bf16", 1024), ("f32", "f32", 513)])
+def test_gradient_of_a_large_table(tok, grad, weight, dim):
+    """Many tokens and a table of 80 MB: its zeros are written beside the sums."""
+    import torch
+    n, rows = 15_000, 40_000
+    ids, g = make_ids(n, rows, "skewed"), rand((n, dim), grad, 30)
+    want, bound = want_grad(ids, g, rows, 0.5)
+    out = torch.full((rows, dim), 3.0, dtype=dtypes()[weight], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            tok.embed_grad(ids, g, rows, scale=0.5, out=out)
+        after = out.clone()  # ordered behind the call on its stream
+    torch.cuda.current_stream().wait_stream(side)
+    assert_close(after, want, bound, "large table")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        tok.embed_grad(ids, g, rows, scale=0.5, out=out)
+    out.fill_(5.0)
+    graph.replay()
+    assert torch.equal(out, after)
+
+
 def test_gradient_skips(tok):
     import torch
     ids, g = make_ids(700, 20, "uniform"), rand((700, 40), "f32", 11)
