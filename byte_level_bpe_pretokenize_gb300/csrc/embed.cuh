@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kRankThreads) k_emb_rank(RankArgs a) {
 
 constexpr int kSumWarps = 8;
 constexpr int kSumCols = 512;     // columns of a block
-constexpr int kSumMaxRun = 16;    // tokens of a warp, at most
+constexpr int kSumMaxRun = 32;    // tokens of a warp, at most
 constexpr int kSmallTokens = 512; // most tokens of the single launch
 constexpr int64_t kSmallRows = (1ll << 32) / kSmallTokens - 1;  // and rows: a key and a token fit 32 bits
 constexpr int kSumRing = 8320;    // bytes of a warp's tokens in flight
@@ -419,6 +419,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
   constexpr bool kVectors = V * sizeof(TG) == 16;
   constexpr int kSlot = kSumCols * (int)sizeof(TG) + (kVectors ? 0 : 16);  // of a token in the ring
   constexpr int kAhead = kSumRing / kSlot;                                 // tokens in flight
+  const int ring_bytes = min(kAhead, a.run) * kSlot;                       // a run has no more
   __shared__ __align__(16) float part[kSumWarps][2][kSumCols];
   __shared__ int32_t part_key[kSumWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -470,7 +471,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
   if constexpr (kVectors) {
     // Each lane copies its own vectors into its warp's ring and reads them
     // back itself, so no barrier is needed; a token is one group of copies.
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * kSumRing + lane * 16;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * ring_bytes + lane * 16;
     auto fetch = [&](int j, uint32_t slot) {
       if (j < len) {
         const TG* g = grad + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j) * a.grad_stride;
@@ -502,7 +503,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
   } else {
     // Rows that are not aligned: the warp copies the 16-byte granules that a
     // token's columns lie in, and the lanes read theirs from inside them.
-    unsigned char* ring = sum_smem + warp * kSumRing;
+    unsigned char* ring = sum_smem + warp * ring_bytes;
     const int bytes = min(kSumCols, a.dim - col0) * (int)sizeof(TG);
     const char* from0 = reinterpret_cast<const char*>(a.grad + col0);
     auto source = [&](int j) {
@@ -771,10 +772,10 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     if (n_rows == 0 || dim == 0) return BPE_OK;
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
-    // Tokens of a warp: as many as kSumMaxRun once that leaves two blocks for every SM.
+    // Tokens of a warp: as many as leave a block for every SM.
     const int64_t groups = (dim + kSumCols - 1) / kSumCols;
     int run = kSumMaxRun;
-    while (run > 2 && (n_ids / (kSumWarps * run)) * groups < 2 * h->n_sms) run /= 2;
+    while (run > 2 && (n_ids / (kSumWarps * run)) * groups < h->n_sms) run /= 2;
     const int64_t chunk = kSumWarps * run, n_chunks = (n_ids + chunk - 1) / chunk;
     const size_t pair = align256((size_t)n_ids * 8), parts = align256((size_t)n_chunks * 2 * (size_t)dim * 4);
     rc = ensure_ws(h, 2 * pair + parts);
@@ -801,8 +802,9 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     const bool aside = !small && !rank && !accumulate && n_rows * f.row_bytes >= (64ll << 20);
     int64_t fillers = 0;
     if (!accumulate) {
-      fillers = std::min<int64_t>(small || rank || aside ? h->n_sms : h->n_sms - ctas,
-                                  std::max<int64_t>(1, n_rows * f.row_bytes / 32768));
+      // more blocks even out the SMs' rates, but each reads all ids
+      const int64_t most = small ? 8 * h->n_sms : 2 * (rank || aside ? h->n_sms : h->n_sms - ctas);
+      fillers = std::min<int64_t>(most, std::max<int64_t>(1, n_rows * f.row_bytes / 32768));
       f.row_step = std::min<int64_t>(kFillRows, (n_rows + fillers - 1) / fillers);
     }
     int passes = 1;
@@ -878,8 +880,9 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
                                 grad_weight_stride, accumulate, partial};
         auto launch = [&](auto width) {
           constexpr int V = decltype(width)::value;
-          constexpr size_t kSmem = kSumWarps * kSumRing;
-          constexpr size_t kSmallSmem = std::max(kSmem, sizeof(FillSmem));
+          constexpr size_t kSmem = kSumWarps * kSumRing, kSmallSmem = std::max(kSmem, sizeof(FillSmem));
+          constexpr int kSlot = kSumCols * (int)sizeof(TG) + (V * sizeof(TG) == 16 ? 0 : 16);
+          const size_t smem = kSumWarps * (size_t)std::min(kSumRing / kSlot, run) * kSlot;
           int rc = once_per_device(h->device, [=] {
             cudaError_t e = cudaFuncSetAttribute(k_emb_sum<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)kSmem);
@@ -890,11 +893,11 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
           if (rc) return rc;
           const dim3 grid((unsigned)n_chunks, (unsigned)groups);
           if (small) {
-            k_emb_small<TG, TW, V><<<dim3((unsigned)(n_chunks + fillers), (unsigned)groups), kSumWarps * 32, kSmallSmem,
-                                     st>>>(a, f, ping[0], n_chunks, h->d_small);
+            k_emb_small<TG, TW, V><<<dim3((unsigned)(n_chunks + fillers), (unsigned)groups), kSumWarps * 32,
+                                     std::max(smem, sizeof(FillSmem)), st>>>(a, f, ping[0], n_chunks, h->d_small);
             CK(cudaGetLastError());
           } else {
-            CK(launch_after(k_emb_sum<TG, TW, V>, grid, kSumWarps * 32, kSmem, st, a));
+            CK(launch_after(k_emb_sum<TG, TW, V>, grid, kSumWarps * 32, smem, st, a));
           }
           if (n_chunks > 1) CK(launch_after(k_emb_join<TG, TW, V>, grid, kSumWarps * 32, 0, st, a, !small));
           if (aside) CK(cudaStreamWaitEvent(st, h->ev_join, 0));
