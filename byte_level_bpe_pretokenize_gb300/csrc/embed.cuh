@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int kEmbThreads = 256;
+constexpr int kEmbThreads = 128;
 constexpr int64_t kEmbMaxDim = 1 << 22;  // columns of a block times the grid's limit
 
 __device__ __forceinline__ bool emb_row_ok(int32_t id, int64_t n_rows) { return id >= 0 && id < n_rows; }
@@ -20,7 +20,7 @@ __device__ __forceinline__ bool emb_row_ok(int32_t id, int64_t n_rows) { return 
 // A block takes rows of tokens x tx threads: each thread holds kEmbRows tokens'
 // vectors of V elements in flight at one column and walks the columns in steps
 // of tx vectors.
-constexpr int kEmbRows = 4;
+constexpr int kEmbRows = 2;
 
 template <class TW, class TO, int V>
 __global__ void __launch_bounds__(kEmbThreads) k_embed(const int32_t* ids, int64_t n_ids, const TW* weight,
@@ -742,7 +742,10 @@ int bpe_embed(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const void* d_
           while ((1 << tx_log2) < kEmbThreads && (1 << tx_log2) < vecs) ++tx_log2;
           const int64_t tokens = kEmbRows * (kEmbThreads >> tx_log2);
           const int64_t blocks = (n_ids + tokens - 1) / tokens;
-          k_embed<TW, TO, V><<<(unsigned)blocks, kEmbThreads, 0, st>>>(
+          // few tokens: several blocks share their columns
+          const int64_t steps = (vecs + (1 << tx_log2) - 1) >> tx_log2;
+          const int64_t share = std::max<int64_t>(1, std::min<int64_t>(steps, 2 * h->n_sms / blocks));
+          k_embed<TW, TO, V><<<dim3((unsigned)blocks, (unsigned)std::min<int64_t>(share, 65535)), kEmbThreads, 0, st>>>(
               d_ids, n_ids, static_cast<const TW*>(d_weight), n_rows, (int)dim, weight_stride, scale, skip_id,
               static_cast<TO*>(d_out), out_stride, tx_log2, h->d_small);
         };
