@@ -128,7 +128,8 @@ __device__ __forceinline__ int32_t plan_relative(int64_t offset, int64_t t0) {
 __device__ __forceinline__ void plan_tokens(const PlanArgs& a, int64_t t0, int64_t t1, int64_t head, int64_t first,
                                             int count, const PlanList& list) {
   const int len = (int)(t1 - t0);
-  const bool vectors = ((reinterpret_cast<uintptr_t>(a.slots + t0) & 15) | (reinterpret_cast<uintptr_t>(a.positions + t0) & 7)) == 0;
+  const bool vectors =
+      ((reinterpret_cast<uintptr_t>(a.slots + t0) & 15) | (reinterpret_cast<uintptr_t>(a.positions + t0) & 7)) == 0;
   const int32_t* free_list = a.free_list + head;
   int32_t position[kPlanPairs][2], in[kPlanPairs][2], entry[kPlanPairs][2];
   int32_t* dealt[kPlanPairs][2];  // the table entry that the token writes, or null
@@ -422,7 +423,7 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
     };
     // blocks read the head and the lengths while others write their successors
     if (overlap(d_info, 16, d_head, 8) || overlap(d_seq_lens, n_requests * 4, d_cached, n_requests * 4))
-      return fail(BPE_ERR_INVALID_ARG, "bpe_plan_blocks: d_info and d_seq_lens cannot replace d_head and d_cached in place");
+      return fail(BPE_ERR_INVALID_ARG, "bpe_plan_blocks: d_info and d_seq_lens cannot replace d_head and d_cached");
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
     PlanArgs a{d_offsets, d_cached, n_requests, n_free, max_blocks, table_stride, n_slots, FastDiv(block_size), d_free,

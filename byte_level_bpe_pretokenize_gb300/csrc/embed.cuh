@@ -118,7 +118,8 @@ __device__ void fill_absent(const FillArgs& a, int64_t r0, int64_t r1, FillSmem&
     for (unsigned char* at = to; at < end; at += a.element) element(at);
   }
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the page is read; the grid's end completes the writes
+  // the page is read; the grid's end completes the writes
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncthreads();
 }
 
@@ -414,24 +415,29 @@ __device__ __forceinline__ void add_vec(float (&acc)[V], const Vec<T, V>& v) {
 //   * what the chunk adds to a row that reaches past it goes to `partial`,
 //     which k_emb_join adds up in order.
 template <class TG, class TW, int V>
-__device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2* sorted, unsigned char* sum_smem) {
+__device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2* sorted, int64_t c0, int64_t c1,
+                                          int run, unsigned char* sum_smem) {
   constexpr int kSlabs = kSumCols / (32 * V);
   constexpr bool kVectors = V * sizeof(TG) == 16;
   constexpr int kSlot = kSumCols * (int)sizeof(TG) + (kVectors ? 0 : 16);  // of a token in the ring
   constexpr int kAhead = kSumRing / kSlot;                                 // tokens in flight
-  const int ring_bytes = min(kAhead, a.run) * kSlot;                       // a run has no more
+  const int ring_bytes = min(kAhead, run) * kSlot;                         // a run has no more
   __shared__ __align__(16) float part[kSumWarps][2][kSumCols];
   __shared__ int32_t part_key[kSumWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c0 = (int64_t)blockIdx.x * kSumWarps * a.run, c1 = min(c0 + kSumWarps * a.run, a.n);
   const int col0 = (int)blockIdx.y * kSumCols;
-  const int64_t j0 = min(c0 + warp * a.run, c1);
-  uint2 mine = make_uint2(0xFFFFFFFFu, 0);
-  if (lane < min((int64_t)a.run, c1 - j0)) mine = sorted[j0 + lane];
+  const int64_t j0 = min(c0 + warp * run, c1), j1 = min(j0 + run, c1);
   const int32_t before = c0 > 0 ? (int32_t)sorted[c0 - 1].x : -1;
   const int32_t after = c1 < a.n ? (int32_t)sorted[c1].x : -1;
-  // tokens without a row are the last ones
-  const int len = __popc(__ballot_sync(0xFFFFFFFFu, mine.x < (uint32_t)a.n_rows));
+  // up to 32 tokens of the run, a lane each; those without a row are the last
+  uint2 mine = make_uint2(0xFFFFFFFFu, 0);
+  int len = 0;
+  auto take = [&](int64_t from) {
+    mine = from + lane < j1 ? sorted[from + lane] : make_uint2(0xFFFFFFFFu, 0);
+    len = __popc(__ballot_sync(0xFFFFFFFFu, mine.x < (uint32_t)a.n_rows));
+  };
+  take(j0);
+  const bool any = len > 0;
   float acc[kSlabs][V] = {};
   int32_t row = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, 0);
   bool begun = false;  // the run's first row has ended
@@ -468,87 +474,94 @@ __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2*
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[s][e] = 0.f;
   };
-  if constexpr (kVectors) {
-    // Each lane copies its own vectors into its warp's ring and reads them
-    // back itself, so no barrier is needed; a token is one group of copies.
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * ring_bytes + lane * 16;
-    auto fetch = [&](int j, uint32_t slot) {
-      if (j < len) {
-        const TG* g = grad + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j) * a.grad_stride;
+  for (int64_t from = j0;;) {
+    if constexpr (kVectors) {
+      // Each lane copies its own vectors into its warp's ring and reads them
+      // back itself, so no barrier is needed; a token is one group of copies.
+      const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sum_smem) + warp * ring_bytes + lane * 16;
+      auto fetch = [&](int j, uint32_t slot) {
+        if (j < len) {
+          const TG* g = grad + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j) * a.grad_stride;
+#pragma unroll
+          for (int s = 0; s < kSlabs; ++s)
+            if (s * 32 * V < cols)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + slot + s * 512), "l"(g + s * 32 * V)
+                           : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) fetch(j, j * kSlot);
+      uint32_t slot = 0;
+      for (int j = 0; j < len; ++j) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
+        Vec<TG, V> v[kSlabs];
 #pragma unroll
         for (int s = 0; s < kSlabs; ++s)
-          if (s * 32 * V < cols)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + slot + s * 512), "l"(g + s * 32 * V)
-                         : "memory");
+          v[s] = *reinterpret_cast<const Vec<TG, V>*>(__cvta_shared_to_generic(ring + slot + s * 512));
+        if (key != row) next_row(key);
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s) add_vec<TG, V>(acc[s], v[s]);
+        fetch(j + kAhead, slot);
+        slot = slot + kSlot == kAhead * kSlot ? 0 : slot + kSlot;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j, j * kSlot);
-    uint32_t slot = 0;
-    for (int j = 0; j < len; ++j) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-      const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
-      Vec<TG, V> v[kSlabs];
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s)
-        v[s] = *reinterpret_cast<const Vec<TG, V>*>(__cvta_shared_to_generic(ring + slot + s * 512));
-      if (key != row) next_row(key);
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s) add_vec<TG, V>(acc[s], v[s]);
-      fetch(j + kAhead, slot);
-      slot = slot + kSlot == kAhead * kSlot ? 0 : slot + kSlot;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
-    // Rows that are not aligned: the warp copies the 16-byte granules that a
-    // token's columns lie in, and the lanes read theirs from inside them.
-    unsigned char* ring = sum_smem + warp * ring_bytes;
-    const int bytes = min(kSumCols, a.dim - col0) * (int)sizeof(TG);
-    const char* from0 = reinterpret_cast<const char*>(a.grad + col0);
-    auto source = [&](int j) {
-      return from0 + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j & 31) * a.grad_stride * (int64_t)sizeof(TG);
-    };
-    auto fetch = [&](int j, int slot) {
-      const char* from = source(j);
-      if (j < len) {
-        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15);
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + slot * kSlot);
-        for (int g = lane * 16; g < off + bytes; g += 512) {
-          const int size = min(16, off + bytes - g);  // nothing past the row is read
-          const char* at = from - off + g;
-          if (at < reinterpret_cast<const char*>(a.grad)) {  // nor before the first one
-            for (int e = off; e < size; e += sizeof(TG))
-              *reinterpret_cast<TG*>(ring + slot * kSlot + e) = *reinterpret_cast<const TG*>(at + e);
-            continue;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // Rows that are not aligned: the warp copies the 16-byte granules that a
+      // token's columns lie in, and the lanes read theirs from inside them.
+      unsigned char* ring = sum_smem + warp * ring_bytes;
+      const int bytes = min(kSumCols, a.dim - col0) * (int)sizeof(TG);
+      const char* from0 = reinterpret_cast<const char*>(a.grad + col0);
+      auto source = [&](int j) {
+        return from0 + (int64_t)__shfl_sync(0xFFFFFFFFu, mine.y, j & 31) * a.grad_stride * (int64_t)sizeof(TG);
+      };
+      auto fetch = [&](int j, int slot) {
+        const char* from = source(j);
+        if (j < len) {
+          const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+          const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + slot * kSlot);
+          for (int g = lane * 16; g < off + bytes; g += 512) {
+            const int size = min(16, off + bytes - g);  // nothing past the row is read
+            const char* at = from - off + g;
+            if (at < reinterpret_cast<const char*>(a.grad)) {  // nor before the first one
+              for (int e = off; e < size; e += sizeof(TG))
+                *reinterpret_cast<TG*>(ring + slot * kSlot + e) = *reinterpret_cast<const TG*>(at + e);
+              continue;
+            }
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + g), "l"(at), "r"(size) : "memory");
           }
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + g), "l"(at), "r"(size) : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) fetch(j, j);
+      int slot = 0;
+      for (int j = 0; j < len; ++j) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();
+        const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
+        const int off = (int)(reinterpret_cast<uintptr_t>(source(j)) & 15);
+        const TG* v = reinterpret_cast<const TG*>(ring + slot * kSlot + off) + lane;
+        if (key != row) next_row(key);
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s)
+          if (s * 32 < cols) acc[s][0] += to_f32(v[s * 32]);
+        __syncwarp();
+        fetch(j + kAhead, slot);
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j, j);
-    int slot = 0;
-    for (int j = 0; j < len; ++j) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
-      const int32_t key = (int32_t)__shfl_sync(0xFFFFFFFFu, mine.x, j);
-      const TG* v = reinterpret_cast<const TG*>(ring + slot * kSlot + (reinterpret_cast<uintptr_t>(source(j)) & 15)) + lane;
-      if (key != row) next_row(key);
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s)
-        if (s * 32 < cols) acc[s][0] += to_f32(v[s * 32]);
-      __syncwarp();
-      fetch(j + kAhead, slot);
-      slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    from += 32;
+    if (len < 32 || from >= j1) break;
+    take(from);
   }
   // a run of one row has only the first part, an empty run none (key -1)
-  if (len > 0) stash(begun ? 1 : 0);
+  if (any) stash(begun ? 1 : 0);
   if (lane == 0) {
-    if (len == 0) part_key[warp][0] = -1;
+    if (!any) part_key[warp][0] = -1;
     if (!begun) part_key[warp][1] = -1;
   }
   __syncthreads();
@@ -596,22 +609,24 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
   extern __shared__ __align__(16) unsigned char sum_smem[];
   await_previous();
   let_next_begin();
-  sum_chunk<TG, TW, V>(a, a.sorted, sum_smem);
+  const int64_t c0 = (int64_t)blockIdx.x * kSumWarps * a.run;
+  sum_chunk<TG, TW, V>(a, a.sorted, c0, min(c0 + kSumWarps * a.run, a.n), a.run, sum_smem);
 }
 
 // Up to kSmallTokens tokens in one launch: blocks [0, chunks) rank the tokens
 // by comparing each with every other, all of them in each block, which is
-// sooner done than another kernel is begun, and sum their chunk; the others
-// zero rows without a token.
+// sooner done than another kernel is begun, and sum a chunk of whole rows; the
+// others zero rows without a token.
 template <class TG, class TW, int V>
-__global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a, FillArgs f, uint2* sorted_out,
-                                                              int64_t n_chunks, DevSmall* small) {
+__global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a, FillArgs f, int64_t n_chunks,
+                                                              DevSmall* small) {
   extern __shared__ __align__(16) unsigned char sum_smem[];
   __shared__ uint2 sorted[kSmallTokens];
   __shared__ __align__(16) uint32_t key[kSmallTokens];
-  let_next_begin();
+  __shared__ int bound[2];
   if (blockIdx.x >= n_chunks) {
-    if (blockIdx.y == 0) fill_rows(f, blockIdx.x - n_chunks, gridDim.x - n_chunks, *reinterpret_cast<FillSmem*>(sum_smem));
+    if (blockIdx.y == 0)
+      fill_rows(f, blockIdx.x - n_chunks, gridDim.x - n_chunks, *reinterpret_cast<FillSmem*>(sum_smem));
     return;
   }
   // key * kSmallTokens + token: distinct, and in sorted order
@@ -627,7 +642,6 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a,
     key[i] = k;
   }
   __syncthreads();
-  const int64_t c0 = (int64_t)blockIdx.x * kSumWarps * a.run, c1 = c0 + kSumWarps * a.run;
   for (int i = tid; i < n; i += kSumWarps * 32) {
     const uint32_t k = key[i];
     int rank = 0;
@@ -636,23 +650,30 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a,
       const uint4 o = *reinterpret_cast<const uint4*>(key + j);
       rank += (o.x < k) + (o.y < k) + (o.z < k) + (o.w < k);
     }
-    const uint2 t = make_uint2(k / kSmallTokens, (uint32_t)i);
-    sorted[rank] = t;
-    if (rank >= c0 && rank < c1 && blockIdx.y == 0) sorted_out[rank] = t;
+    sorted[rank] = make_uint2(k / kSmallTokens, (uint32_t)i);
   }
+  if (tid == 0) bound[0] = bound[1] = n;
   __syncthreads();
-  sum_chunk<TG, TW, V>(a, sorted, sum_smem);
+  // the block's share of the places, moved to where rows begin
+  const int c0 = (int)blockIdx.x * kSumWarps * a.run, c1 = c0 + kSumWarps * a.run;
+  for (int p = tid; p < n; p += kSumWarps * 32)
+    if (p == 0 || sorted[p].x != sorted[p - 1].x) {
+      if (p >= c0) atomicMin(&bound[0], p);
+      if (p >= c1) atomicMin(&bound[1], p);
+    }
+  __syncthreads();
+  const int b0 = bound[0], b1 = bound[1];
+  if (b0 < b1) sum_chunk<TG, TW, V>(a, sorted, b0, b1, (b1 - b0 + kSumWarps - 1) / kSumWarps, sum_smem);
 }
 
 // The parts of a row that reaches past a chunk, joined in order by the block
 // of the chunk that it begins in. A chunk's part is its second one if the row
-// begins inside it, and its first one otherwise. early: the sorted tokens are
-// older than the kernel before, so they are read before it ends.
+// begins inside it, and its first one otherwise. The sorted tokens are older
+// than the kernel before, so they are read before it ends.
 template <class TG, class TW, int V>
-__global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a, bool early) {
+__global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a) {
   constexpr int kPer = kSumCols / 32;
   __shared__ float part[kSumWarps][kSumCols];
-  if (!early) await_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t chunk = kSumWarps * a.run;
   const int64_t c = blockIdx.x, c0 = c * chunk, c1 = min(c0 + chunk, a.n);
@@ -669,7 +690,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a, 
       break;
     }
   }
-  if (early) await_previous();
+  await_previous();
   if (parts == 1 || r >= a.n_rows || (whole && before == r)) return;
   const int64_t per = (parts + kSumWarps - 1) / kSumWarps;
   const int64_t p0 = min(warp * per, parts), p1 = min(p0 + per, parts);
@@ -797,7 +818,7 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     f.stride_bytes = grad_weight_stride * f.element;
     const bool small = n_ids <= kSmallTokens && n_rows < kSmallRows;
     const bool rank = !small && n_ids <= kRankTokens && (n_rows + 1) * n_ids < (1ll << 32);
-    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of a sort: a cluster's barriers cost more than a few tokens gain
+    const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of a sort, where a few tokens' rows are too many to rank
     // Zeros beside the kernels that find and sum the tokens, fewer blocks where
     // each would have under 32 KB to write. Where they take longer than the
     // sort they go on a stream of their own, so that the sums need not wait
@@ -889,20 +910,20 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
           int rc = once_per_device(h->device, [=] {
             cudaError_t e = cudaFuncSetAttribute(k_emb_sum<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)kSmem);
-            return e != cudaSuccess ? e
-                                    : cudaFuncSetAttribute(k_emb_small<TG, TW, V>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+            if (e != cudaSuccess) return e;
+            return cudaFuncSetAttribute(k_emb_small<TG, TW, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)kSmallSmem);
           });
           if (rc) return rc;
           const dim3 grid((unsigned)n_chunks, (unsigned)groups);
           if (small) {
             k_emb_small<TG, TW, V><<<dim3((unsigned)(n_chunks + fillers), (unsigned)groups), kSumWarps * 32,
-                                     std::max(smem, sizeof(FillSmem)), st>>>(a, f, ping[0], n_chunks, h->d_small);
+                                     kSmallSmem, st>>>(a, f, n_chunks, h->d_small);
             CK(cudaGetLastError());
           } else {
             CK(launch_after(k_emb_sum<TG, TW, V>, grid, kSumWarps * 32, smem, st, a));
           }
-          if (n_chunks > 1) CK(launch_after(k_emb_join<TG, TW, V>, grid, kSumWarps * 32, 0, st, a, !small));
+          if (n_chunks > 1 && !small) CK(launch_after(k_emb_join<TG, TW, V>, grid, kSumWarps * 32, 0, st, a));
           if (aside) CK(cudaStreamWaitEvent(st, h->ev_join, 0));
           return (int)BPE_OK;
         };

@@ -37,7 +37,8 @@ struct LogTable {
   }
   __device__ __forceinline__ void clear(int chunk, bool by_output) const {
     const int words = chunk / 16 + (by_output ? packed ? chunk / 2 : chunk : 0);
-    for (int v = threadIdx.x; v < words / 4; v += kLogThreads) reinterpret_cast<uint4*>(bits)[v] = make_uint4(0, 0, 0, 0);
+    for (int v = threadIdx.x; v < words / 4; v += kLogThreads)
+      reinterpret_cast<uint4*>(bits)[v] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void see(int v) const { atomicOr(&bits[v >> 5], 1u << (v & 31)); }
   __device__ __forceinline__ void count(int v) const {
@@ -64,9 +65,11 @@ __device__ __forceinline__ LogRow log_row(const bpe_logits_args& a, int64_t b, b
   LogRow r{1.f, 0.f, 0.f, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, nullptr, false};
   if (table) {
     // all loads first, so that they overlap
-    const int64_t p0 = a.prompt_ids ? __ldg(a.prompt_offsets + b) : 0, p1 = a.prompt_ids ? __ldg(a.prompt_offsets + b + 1) : 0;
+    const int64_t p0 = a.prompt_ids ? __ldg(a.prompt_offsets + b) : 0;
+    const int64_t p1 = a.prompt_ids ? __ldg(a.prompt_offsets + b + 1) : 0;
     const int64_t len = a.output_ids ? __ldg(a.output_lens + b) : 0;
-    const int64_t b0 = a.bias_ids ? __ldg(a.bias_offsets + b) : 0, b1 = a.bias_ids ? __ldg(a.bias_offsets + b + 1) : 0;
+    const int64_t b0 = a.bias_ids ? __ldg(a.bias_offsets + b) : 0;
+    const int64_t b1 = a.bias_ids ? __ldg(a.bias_offsets + b + 1) : 0;
     if (a.repetition) r.rep = __ldg(a.repetition + b);
     if (a.frequency) r.freq = __ldg(a.frequency + b);
     if (a.presence) r.pres = __ldg(a.presence + b);
@@ -135,9 +138,20 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
       const int v = head + (g0 + q * kThreads) * kLogGroup;
       const uint32_t bits = mask ? log_open(mask, (int)v0 + v, words) : 0xFFFFFFFFu;
       Vec<TO, kLogGroup> o;
+      if constexpr (std::is_same_v<TI, TO> && sizeof(TI) == 2) {
+        // bits of pairs, without a conversion
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(x[q].x);
+        constexpr uint32_t kShut = std::is_same_v<TI, __half> ? 0xFC00FC00u : 0xFF80FF80u;  // twice -infinity
 #pragma unroll
-      for (int e = 0; e < kLogGroup; ++e)
-        o.x[e] = from_f32<TO>(bits >> e & 1 ? to_f32(x[q].x[e]) : -INFINITY);
+        for (int e = 0; e < kLogGroup / 2; ++e) {
+          const uint32_t open = (bits >> (2 * e) & 1 ? 0xFFFFu : 0u) | (bits >> (2 * e + 1) & 1 ? 0xFFFF0000u : 0u);
+          reinterpret_cast<uint32_t*>(o.x)[e] = (from[e] & open) | (kShut & ~open);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kLogGroup; ++e)
+          o.x[e] = from_f32<TO>(bits >> e & 1 ? to_f32(x[q].x[e]) : -INFINITY);
+      }
       o.store(out + v);
     }
   }
