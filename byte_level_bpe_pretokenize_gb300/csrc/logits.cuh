@@ -17,37 +17,78 @@ constexpr int kLogWarps = kLogThreads / 32;
 constexpr int kLogGroup = 8;         // tokens of a vector
 constexpr int kLogAhead = 2;         // vectors of a thread in flight
 constexpr int kLogIds = 2;           // 16-byte loads of ids of a thread in flight
+constexpr int kLogBlocks = 8;         // CTAs an SM at least, while chunks can be halved
 constexpr int kLogMinChunk = 2048;   // tokens of a CTA
-constexpr int kLogMaxChunk = 8192;
+constexpr int kLogMaxChunk = 16384;
+constexpr int kLogDenseChunk = 8192; // with a count for each token
 constexpr int kLogList = 1024;       // concerned tokens that a CTA lists at once
-constexpr int kLogBiases = 512;     // biases of a chunk that it lists
+constexpr int kLogBiases = 512;      // biases of a chunk that it lists
+constexpr int kLogSaid = 2048;       // output tokens of a chunk that it lists
 
 // What a row's history says about a chunk, in shared memory: a bit for each
-// token that occurs in it, and the times it occurs in the output, in 16 bits
-// where no output is longer than that. Both are only added to, without a look
-// at what was there, so nothing waits for shared memory.
+// token that occurs in it, one for each that has a bias, and the times a token
+// occurs in the output. Outputs of up to kLogSaid tokens are listed as they
+// are, with a bit for each token among them, and an occurrence is counted when
+// it is asked for; longer ones have a count for each token (in 16 bits where
+// that is enough), and shorter chunks. The bits and counts are added to without
+// a look at what was there, so nothing waits for shared memory.
 struct LogTable {
   uint32_t* bits;    // [chunk / 32]
-  uint32_t* biased;  // [chunk / 32] a bit for each token with a bias
-  uint32_t* counts;  // [chunk] or, packed, [chunk / 2]
-  bool packed;
+  uint32_t* biased;  // [chunk / 32]
+  uint32_t* twice;   // [chunk / 32] tokens with more than one bias
+  uint32_t* said;    // [chunk / 32], where the output is listed
+  uint16_t* list;    // [kLogSaid] the chunk's output tokens, in any order
+  int* listed;       // how many
+  uint32_t* counts;  // [chunk] or, in 16 bits, [chunk / 2]; where the output is counted
+  int wide;          // bits of a count; 0: the output is listed
 
-  static int bytes(int chunk, bool by_output, bool packed) {
-    return chunk / 4 + (by_output ? packed ? chunk * 2 : chunk * 4 : 0);
+  static constexpr int bytes(int chunk, bool by_output, int wide) {
+    return 3 * chunk / 8 + (!by_output ? 0 : wide ? chunk * wide / 8 : chunk / 8 + 2 * kLogSaid);
   }
+  __device__ __forceinline__ LogTable(uint32_t* smem, int chunk, int wide_, int* listed_)
+      : bits(smem), biased(smem + chunk / 32), twice(smem + 2 * chunk / 32), said(smem + 3 * chunk / 32),
+        list(reinterpret_cast<uint16_t*>(smem + 4 * chunk / 32)), listed(listed_), counts(smem + 3 * chunk / 32),
+        wide(wide_) {}
   __device__ __forceinline__ void clear(int chunk, bool by_output) const {
-    const int words = chunk / 16 + (by_output ? packed ? chunk / 2 : chunk : 0);
+    const int words = 3 * chunk / 32 + (!by_output ? 0 : wide ? chunk * wide / 32 : chunk / 32);
     for (int v = threadIdx.x; v < words / 4; v += kLogThreads)
       reinterpret_cast<uint4*>(bits)[v] = make_uint4(0, 0, 0, 0);
+    // no token of a chunk is 0xFFFF, which fills the last vector of the list
+    if (by_output && !wide)
+      for (int i = threadIdx.x; i < kLogSaid / 8; i += kLogThreads)
+        reinterpret_cast<uint4*>(list)[i] = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
+    if (threadIdx.x == 0) *listed = 0;
   }
   __device__ __forceinline__ void see(int v) const { atomicOr(&bits[v >> 5], 1u << (v & 31)); }
-  __device__ __forceinline__ void count(int v) const {
-    if (packed) atomicAdd(&counts[v >> 1], (v & 1) ? 0x10000u : 1u);
-    else atomicAdd(&counts[v], 1u);
+  __device__ __forceinline__ void say(int v) const {
+    see(v);
+    if (wide == 16) {
+      atomicAdd(&counts[v >> 1], (v & 1) ? 0x10000u : 1u);
+    } else if (wide) {
+      atomicAdd(&counts[v], 1u);
+    } else {
+      atomicOr(&said[v >> 5], 1u << (v & 31));
+      list[atomicAdd(listed, 1)] = (uint16_t)v;
+    }
   }
   __device__ __forceinline__ bool seen(int v) const { return bits[v >> 5] >> (v & 31) & 1; }
   __device__ __forceinline__ uint32_t times(int v) const {
-    return packed ? counts[v >> 1] >> ((v & 1) * 16) & 0xFFFFu : counts[v];
+    if (wide == 16) return counts[v >> 1] >> ((v & 1) * 16) & 0xFFFFu;
+    if (wide) return counts[v];
+    if (!(said[v >> 5] >> (v & 31) & 1)) return 0;
+    // eight entries a load; in x ^ (v, v) the half that is 0 is the one whose
+    // low 15 bits carry nothing into its top bit and whose top bit is 0
+    uint32_t k = 0;
+    const int vecs = (*listed + 7) / 8;
+    const uint32_t twice = (uint32_t)v * 0x10001u;
+    const uint4* from = reinterpret_cast<const uint4*>(list);
+    auto zeros = [](uint32_t x) { return (uint32_t)__popc(~(((x & 0x7FFF7FFFu) + 0x7FFF7FFFu) | x | 0x7FFF7FFFu)); };
+#pragma unroll 4
+    for (int i = 0; i < vecs; ++i) {
+      const uint4 p = from[i];
+      k += zeros(p.x ^ twice) + zeros(p.y ^ twice) + zeros(p.z ^ twice) + zeros(p.w ^ twice);
+    }
+    return k;
   }
 };
 
@@ -139,7 +180,7 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
       const uint32_t bits = mask ? log_open(mask, (int)v0 + v, words) : 0xFFFFFFFFu;
       Vec<TO, kLogGroup> o;
       if constexpr (std::is_same_v<TI, TO> && sizeof(TI) == 2) {
-        // bits of pairs, without a conversion
+        // pairs of bit patterns, without a conversion
         const uint32_t* from = reinterpret_cast<const uint32_t*>(x[q].x);
         constexpr uint32_t kShut = std::is_same_v<TI, __half> ? 0xFC00FC00u : 0xFF80FF80u;  // twice -infinity
 #pragma unroll
@@ -166,24 +207,28 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // A CTA takes `chunk` tokens of one row. With kTable, what the row's history
 // and biases say about them is gathered in shared memory, and after the pass
 // the few tokens that are concerned are written again, each once: the pass has
-// left a token that the mask shuts at -infinity, and in place it has
-// left the bits of every other one. Only integer atomics whose results nobody
-// takes, and biases listed in their order: nothing depends on timing.
+// left a token that the mask shuts at -infinity, and in place it has left the
+// bits of every other one. Bits and counts do not depend on the order in which
+// they are made, and biases are listed in theirs: nothing depends on timing.
 //
 // All CTAs of a row read its whole history, which is L2 traffic and a few
-// instructions an id. What was slower: testing for concerned tokens in the
-// pass (most warps hold one, and the whole warp waits for its division), a
-// hash table or lists filled by atomics that return a value (a chain of waits
-// for each id), warps that gather while others pass (too few to hide it), and
-// a second launch or the last CTA of a row for the gathering.
+// instructions an id. Bound by HBM for the pass (384 rows of 113,645 bf16:
+// 29.7 us, 5.9 TB/s; with a mask for each row 31.6) and, with a history, by the
+// latency of a CTA's steps: lists, barrier, pass, barrier, the tokens again
+// (56 us with 3,000 prompt and 450 output tokens a row on average). What was
+// slower for that case: a word for each token looked at in the pass (most warps
+// hold a concerned token, and the whole warp waits for its division: 135 us), a
+// hash table filled by atomics that return a value (a chain of waits for each
+// id: 84 us), warps that gather while others pass (152 us), the last CTA of a
+// row writing for all (119 us), a second launch a row (82 us).
 template <class TI, class TO, bool kTable, bool kBias>
-__global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, int chunk, bool packed, DevSmall* small) {
+__global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, int chunk, int wide, DevSmall* small) {
   extern __shared__ __align__(16) uint32_t log_smem[];
   __shared__ uint16_t list[kTable ? kLogList : 1];
   __shared__ uint16_t bias_token[kBias ? kLogBiases : 1];
   __shared__ float bias_value[kBias ? kLogBiases : 1];
-  __shared__ int warp_sum[kLogWarps], n_biases;
-  const LogTable t{log_smem, log_smem + chunk / 32, log_smem + chunk / 16, packed};
+  __shared__ int warp_sum[kLogWarps], n_biases, n_said;
+  const LogTable t(log_smem, chunk, wide, &n_said);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.y, v0 = (int64_t)blockIdx.x * chunk;
   const int n = (int)min((int64_t)chunk, a.n_vocab - v0);
@@ -191,19 +236,16 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
   bool bad = false;
   LogRow r;
   log_pass<TI, TO, kLogThreads>(a, b, v0, n, tid, [&] {
+    if (kTable) t.clear(chunk, a.output_ids != nullptr);
     r = log_row(a, b, kTable, &bad);
     if (!kTable || !r.concerned) return r.mask;
-    t.clear(chunk, a.output_ids != nullptr);
     __syncthreads();
     each_id<kLogIds>(r.prompt, r.n_prompt, tid, kLogThreads, [&](uint32_t id) {
       if (id - low < (uint32_t)n) t.see((int)(id - low));
       bad |= id >= vocab;
     });
     each_id<kLogIds>(r.output, r.n_output, tid, kLogThreads, [&](uint32_t id) {
-      if (id - low < (uint32_t)n) {
-        t.see((int)(id - low));
-        t.count((int)(id - low));
-      }
+      if (id - low < (uint32_t)n) t.say((int)(id - low));
       bad |= id >= vocab;
     });
     if (kBias && warp == kLogWarps - 1) {
@@ -227,7 +269,8 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
           const int at = m + __popc(in_chunk & ((1u << lane) - 1));
           if (id[q] != 0xFFFFFFFFu) {
             const int v = (int)(id[q] - low);
-            atomicOr(&t.biased[v >> 5], 1u << (v & 31));
+            const uint32_t bit = 1u << (v & 31);
+            if (atomicOr(&t.biased[v >> 5], bit) & bit) atomicOr(&t.twice[v >> 5], bit);
             if (at < kLogBiases) {
               bias_token[at] = (uint16_t)v;
               bias_value[at] = value[q];
@@ -293,10 +336,13 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
       const int v = bias_token[k];
       float sum = bias_value[k];
       bool first = true;
-      for (int o = 0; o < m; ++o) {
-        if (bias_token[o] != v) continue;
-        if (o < k) first = false;
-        if (o > k) sum += bias_value[o];
+      if (t.twice[v >> 5] >> (v & 31) & 1) {
+#pragma unroll 4
+        for (int o = 0; o < m; ++o) {
+          if (bias_token[o] != v) continue;
+          if (o < k) first = false;
+          if (o > k) sum += bias_value[o];
+        }
       }
       if (first && open(v)) out[v] = from_f32<TO>(penalised(v) + sum);
     }
@@ -305,13 +351,15 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
     for (int64_t k = tid; k < r.n_bias; k += kLogThreads) {
       const uint32_t id = (uint32_t)__ldg(r.bias_ids + k);
       if (id - low >= (uint32_t)n) continue;
-      float sum = __ldg(r.bias_values + k);
-      bool first = true;
-      for (int64_t o = 0; o < k && first; ++o) first = (uint32_t)__ldg(r.bias_ids + o) != id;
-      if (!first) continue;
-      for (int64_t o = k + 1; o < r.n_bias; ++o)
-        if ((uint32_t)__ldg(r.bias_ids + o) == id) sum += __ldg(r.bias_values + o);
       const int v = (int)(id - low);
+      float sum = __ldg(r.bias_values + k);
+      if (t.twice[v >> 5] >> (v & 31) & 1) {
+        bool first = true;
+        for (int64_t o = 0; o < k && first; ++o) first = (uint32_t)__ldg(r.bias_ids + o) != id;
+        if (!first) continue;
+        for (int64_t o = k + 1; o < r.n_bias; ++o)
+          if ((uint32_t)__ldg(r.bias_ids + o) == id) sum += __ldg(r.bias_values + o);
+      }
       if (open(v)) out[v] = from_f32<TO>(penalised(v) + sum);
     }
   }
@@ -354,10 +402,10 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
                        (a.output_ids && (a.repetition || a.frequency || a.presence));
     // Tokens of a CTA: long chunks read the history less often and hide its
     // latency behind a longer pass; short ones spread few rows over more SMs,
-    // and leave room for counts of 32 bits where an output may need them.
-    const bool packed = a.output_capacity <= 0xFFFF;
-    int chunk = table && !packed ? kLogMaxChunk / 2 : kLogMaxChunk;
-    while (chunk > kLogMinChunk && a.n_rows * ((a.n_vocab + chunk - 1) / chunk) < 2 * h->n_sms) chunk /= 2;
+    // and leave room for counts.
+    const int wide = !a.output_ids || a.output_capacity <= kLogSaid ? 0 : a.output_capacity <= 0xFFFF ? 16 : 32;
+    int chunk = !table || !wide ? kLogMaxChunk : wide == 16 ? kLogDenseChunk : kLogDenseChunk / 2;
+    while (chunk > kLogMinChunk && a.n_rows * ((a.n_vocab + chunk - 1) / chunk) < kLogBlocks * h->n_sms) chunk /= 2;
     const dim3 grid((unsigned)((a.n_vocab + chunk - 1) / chunk), (unsigned)a.n_rows);
     return with_type(a.logits_type, [&](auto i) {
       return with_type(a.out_type, [&](auto o) -> int {
@@ -365,13 +413,8 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
         using TO = decltype(o);
         auto launch = [&](auto with_table, auto with_bias) {
           constexpr bool kTable = decltype(with_table)::value, kBias = decltype(with_bias)::value;
-          const int smem = kTable ? LogTable::bytes(chunk, a.output_ids != nullptr, packed) : 0;
-          int rc = once_per_device(h->device, [] {
-            return cudaFuncSetAttribute(k_logits<TI, TO, kTable, kBias>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        LogTable::bytes(kLogMaxChunk, true, true));
-          });
-          if (rc) return rc;
-          k_logits<TI, TO, kTable, kBias><<<grid, kLogThreads, smem, st>>>(a, chunk, packed, h->d_small);
+          const int smem = kTable ? LogTable::bytes(chunk, a.output_ids != nullptr, wide) : 0;
+          k_logits<TI, TO, kTable, kBias><<<grid, kLogThreads, smem, st>>>(a, chunk, wide, h->d_small);
           CK(cudaGetLastError());
           return (int)BPE_OK;
         };
