@@ -146,7 +146,7 @@ __device__ __forceinline__ void plan_tokens(const PlanArgs& a, int64_t t0, int64
           else h = mid;
         }
       } else {
-        l = min(at + 1, count);
+        l = (int)min(t0 - first + at + 1, (int64_t)count);  // request t is token t's
       }
     }
     --l;

@@ -17,7 +17,7 @@ constexpr int kLogWarps = kLogThreads / 32;
 constexpr int kLogGroup = 8;         // tokens of a vector
 constexpr int kLogAhead = 2;         // vectors of a thread in flight
 constexpr int kLogIds = 2;           // 16-byte loads of ids of a thread in flight
-constexpr int kLogBlocks = 8;         // CTAs an SM at least, while chunks can be halved
+constexpr int kLogBlocks = 5;         // CTAs an SM at least, while chunks can be halved
 constexpr int kLogMinChunk = 2048;   // tokens of a CTA
 constexpr int kLogMaxChunk = 16384;
 constexpr int kLogDenseChunk = 8192; // with a count for each token

@@ -108,6 +108,16 @@ def test_single_tokens(tok, n, block, cached_most, share):
     assert run(tok, None, cached, table, free, block, n + 9) == list(want)
 
 
+@pytest.mark.parametrize("n", [513, 1208, 2048, 2049, 4097])
+@pytest.mark.parametrize("block", [1, 16])
+def test_single_tokens_of_several_tiles(tok, n, block):
+    """One launch up to 2048 requests and two above, with tiles that do not begin at the first request."""
+    rng = random.Random(n)
+    cached, _, table, free = make(rng, n, block, 1, 40, single=True)
+    want = plain(None, cached, table, free, block, n + 77, 1)
+    assert run(tok, None, cached, table, free, block, n + 77, 1) == list(want)
+
+
 def test_prompts_without_a_cache(tok):
     rng = random.Random(5)
     _, offsets, table, free = make(rng, 50, 16, 200, 0)
