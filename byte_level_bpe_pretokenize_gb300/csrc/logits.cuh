@@ -25,6 +25,14 @@ constexpr int kLogList = 1024;       // concerned tokens that a CTA lists at onc
 constexpr int kLogBiases = 512;      // biases of a chunk that it lists
 constexpr int kLogSaid = 2048;       // output tokens of a chunk that it lists
 
+// Bits 15 and 31 of word w of the result, moved down by w: whether the halves of
+// p's word w equal those of `twice`. (In their difference the half that is 0 is
+// the one whose low 15 bits carry nothing into its top bit, which is 0 too.)
+__device__ __forceinline__ uint32_t log_equal(const uint4& p, uint32_t twice) {
+  auto zero = [](uint32_t x) { return ~(((x & 0x7FFF7FFFu) + 0x7FFF7FFFu) | x | 0x7FFF7FFFu); };
+  return zero(p.x ^ twice) | zero(p.y ^ twice) >> 1 | zero(p.z ^ twice) >> 2 | zero(p.w ^ twice) >> 3;
+}
+
 // What a row's history says about a chunk, in shared memory: a bit for each
 // token that occurs in it, one for each that has a bias, and the times a token
 // occurs in the output. Outputs of up to kLogSaid tokens are listed as they
@@ -42,7 +50,7 @@ struct LogTable {
   uint32_t* counts;  // [chunk] or, in 16 bits, [chunk / 2]; where the output is counted
   int wide;          // bits of a count; 0: the output is listed
 
-  static constexpr int bytes(int chunk, bool by_output, int wide) {
+  __host__ __device__ static constexpr int bytes(int chunk, bool by_output, int wide) {
     return 3 * chunk / 8 + (!by_output ? 0 : wide ? chunk * wide / 8 : chunk / 8 + 2 * kLogSaid);
   }
   __device__ __forceinline__ LogTable(uint32_t* smem, int chunk, int wide_, int* listed_)
@@ -76,18 +84,12 @@ struct LogTable {
     if (wide == 16) return counts[v >> 1] >> ((v & 1) * 16) & 0xFFFFu;
     if (wide) return counts[v];
     if (!(said[v >> 5] >> (v & 31) & 1)) return 0;
-    // eight entries a load; in x ^ (v, v) the half that is 0 is the one whose
-    // low 15 bits carry nothing into its top bit and whose top bit is 0
     uint32_t k = 0;
     const int vecs = (*listed + 7) / 8;
     const uint32_t twice = (uint32_t)v * 0x10001u;
     const uint4* from = reinterpret_cast<const uint4*>(list);
-    auto zeros = [](uint32_t x) { return (uint32_t)__popc(~(((x & 0x7FFF7FFFu) + 0x7FFF7FFFu) | x | 0x7FFF7FFFu)); };
 #pragma unroll 4
-    for (int i = 0; i < vecs; ++i) {
-      const uint4 p = from[i];
-      k += zeros(p.x ^ twice) + zeros(p.y ^ twice) + zeros(p.z ^ twice) + zeros(p.w ^ twice);
-    }
+    for (int i = 0; i < vecs; ++i) k += __popc(log_equal(from[i], twice));
     return k;
   }
 };
@@ -132,6 +134,18 @@ __device__ __forceinline__ LogRow log_row(const bpe_logits_args& a, int64_t b, b
     else if (row >= 0) r.mask = a.mask + row * a.mask_stride;
   }
   return r;
+}
+
+// Adds x to sums[v], equal tokens in lane order; v < 0 for none. One warp.
+__device__ __noinline__ void log_add_bias(float* sums, int v, float x, int lane) {
+  const unsigned same = __match_any_sync(0xFFFFFFFFu, v);
+  float sum = v >= 0 ? sums[v] : 0.f;
+  for (unsigned m = v >= 0 ? same : 0; __any_sync(0xFFFFFFFFu, m); m &= m - 1) {
+    const float xk = __shfl_sync(0xFFFFFFFFu, x, m ? __ffs(m) - 1 : lane);
+    if (m) sum += xk;
+  }
+  if (v >= 0 && (same & ((1u << lane) - 1)) == 0) sums[v] = sum;
+  __syncwarp();
 }
 
 // The bits of the tokens from v on, 8 of them at least; `words` of the mask may
@@ -221,14 +235,16 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // hash table filled by atomics that return a value (a chain of waits for each
 // id: 84 us), warps that gather while others pass (152 us), the last CTA of a
 // row writing for all (119 us), a second launch a row (82 us).
-template <class TI, class TO, bool kTable, bool kBias>
+template <class TI, class TO, bool kTable, bool kBias, bool kByToken>
 __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, int chunk, int wide, DevSmall* small) {
   extern __shared__ __align__(16) uint32_t log_smem[];
   __shared__ uint16_t list[kTable ? kLogList : 1];
-  __shared__ uint16_t bias_token[kBias ? kLogBiases : 1];
-  __shared__ float bias_value[kBias ? kLogBiases : 1];
   __shared__ int warp_sum[kLogWarps], n_biases, n_said;
   const LogTable t(log_smem, chunk, wide, &n_said);
+  // biases: with kByToken (the shortest chunks) a sum for each token, else a list
+  float* bias_value = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(log_smem) +
+                                               LogTable::bytes(chunk, a.output_ids != nullptr, wide));
+  uint16_t* bias_token = reinterpret_cast<uint16_t*>(bias_value + kLogBiases);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.y, v0 = (int64_t)blockIdx.x * chunk;
   const int n = (int)min((int64_t)chunk, a.n_vocab - v0);
@@ -237,6 +253,8 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
   LogRow r;
   log_pass<TI, TO, kLogThreads>(a, b, v0, n, tid, [&] {
     if (kTable) t.clear(chunk, a.output_ids != nullptr);
+    if constexpr (kByToken)
+      for (int v = tid; v < kLogMinChunk; v += kLogThreads) bias_value[v] = 0.f;
     r = log_row(a, b, kTable, &bad);
     if (!kTable || !r.concerned) return r.mask;
     __syncthreads();
@@ -249,7 +267,7 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
       bad |= id >= vocab;
     });
     if (kBias && warp == kLogWarps - 1) {
-      // the chunk's biases in their order; past kLogBiases they are only counted
+      // the chunk's biases in their order: added up by token, or listed; past kLogBiases they are only counted
       int m = 0;
       constexpr int kLook = 4;
       for (int64_t j = lane; j - lane < r.n_bias; j += 32 * kLook) {
@@ -271,15 +289,19 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
             const int v = (int)(id[q] - low);
             const uint32_t bit = 1u << (v & 31);
             if (atomicOr(&t.biased[v >> 5], bit) & bit) atomicOr(&t.twice[v >> 5], bit);
-            if (at < kLogBiases) {
+            if (!kByToken && at < kLogBiases) {
               bias_token[at] = (uint16_t)v;
               bias_value[at] = value[q];
             }
           }
+          if constexpr (kByToken)
+            if (in_chunk) log_add_bias(bias_value, id[q] != 0xFFFFFFFFu ? (int)(id[q] - low) : -1, value[q], lane);
           m += __popc(in_chunk);
         }
       }
       if (lane == 0) n_biases = m;
+      // no token of a chunk is 0xFFFF, which fills the last vector of the list
+      if (!kByToken && m + lane < min((m + 7) & ~7, kLogBiases)) bias_token[m + lane] = 0xFFFF;
     }
     return r.mask;
   });
@@ -294,11 +316,11 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
     return t.seen(v) ? log_penalty(r, x, a.output_ids ? t.times(v) : 0) : x;
   };
   __syncthreads();
-  if (r.n_prompt + r.n_output > 0) {
-    // list the seen tokens, kLogThreads words of bits at most at a time, and share them out
+  if (r.n_prompt + r.n_output > 0 || kByToken) {
+    // list the tokens that are concerned but for those with a listed bias, kLogThreads words of bits at most at a time, and share them out
     for (int w0 = 0; w0 < chunk / 32; w0 += kLogThreads) {
       const int w = w0 + tid;
-      const uint32_t bits = w < chunk / 32 ? t.bits[w] & ~t.biased[w] : 0;
+      const uint32_t bits = w < chunk / 32 ? kByToken ? t.bits[w] | t.biased[w] : t.bits[w] & ~t.biased[w] : 0;
       const int mine = __popc(bits);
       int upto = mine;
 #pragma unroll
@@ -321,14 +343,14 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
         __syncthreads();
         for (int k = tid; k < min(total - k0, kLogList); k += kLogThreads) {
           const int v = list[k];
-          if (open(v)) out[v] = from_f32<TO>(penalised(v));
+          if (open(v)) out[v] = from_f32<TO>(kByToken ? penalised(v) + bias_value[v] : penalised(v));
         }
         __syncthreads();
       }
       __syncthreads();  // warp_sum is read by all before it is written again
     }
   }
-  if (!kBias) return;
+  if (!kBias || kByToken) return;
   const int m = n_biases;
   if (m <= kLogBiases) {
     // whoever has a token's first bias adds up all of them
@@ -337,11 +359,13 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
       float sum = bias_value[k];
       bool first = true;
       if (t.twice[v >> 5] >> (v & 31) & 1) {
-#pragma unroll 4
-        for (int o = 0; o < m; ++o) {
-          if (bias_token[o] != v) continue;
-          if (o < k) first = false;
-          if (o > k) sum += bias_value[o];
+        for (int o0 = 0; o0 < m && first; o0 += 8) {
+          if (!log_equal(*reinterpret_cast<const uint4*>(bias_token + o0), (uint32_t)v * 0x10001u)) continue;
+          for (int o = o0; o < min(o0 + 8, m); ++o) {
+            if (bias_token[o] != v) continue;
+            first &= o >= k;
+            if (o > k) sum += bias_value[o];
+          }
         }
       }
       if (first && open(v)) out[v] = from_f32<TO>(penalised(v) + sum);
@@ -406,21 +430,30 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
     const int wide = !a.output_ids || a.output_capacity <= kLogSaid ? 0 : a.output_capacity <= 0xFFFF ? 16 : 32;
     int chunk = !table || !wide ? kLogMaxChunk : wide == 16 ? kLogDenseChunk : kLogDenseChunk / 2;
     while (chunk > kLogMinChunk && a.n_rows * ((a.n_vocab + chunk - 1) / chunk) < kLogBlocks * h->n_sms) chunk /= 2;
+    // four times the mean biases of a chunk fit its list
+    if (by_bias)
+      while (chunk > kLogMinChunk &&
+             4 * (a.n_bias / a.n_rows) * chunk / std::max<int64_t>(a.n_vocab, chunk) > kLogBiases)
+        chunk /= 2;
     const dim3 grid((unsigned)((a.n_vocab + chunk - 1) / chunk), (unsigned)a.n_rows);
     return with_type(a.logits_type, [&](auto i) {
       return with_type(a.out_type, [&](auto o) -> int {
         using TI = decltype(i);
         using TO = decltype(o);
-        auto launch = [&](auto with_table, auto with_bias) {
-          constexpr bool kTable = decltype(with_table)::value, kBias = decltype(with_bias)::value;
-          const int smem = kTable ? LogTable::bytes(chunk, a.output_ids != nullptr, wide) : 0;
-          k_logits<TI, TO, kTable, kBias><<<grid, kLogThreads, smem, st>>>(a, chunk, wide, h->d_small);
+        auto launch = [&](auto with_table, auto with_bias, auto by_token) {
+          constexpr bool kTable = decltype(with_table)::value, kBias = decltype(with_bias)::value,
+                         kByToken = decltype(by_token)::value;
+          const int smem = (kTable ? LogTable::bytes(chunk, a.output_ids != nullptr, wide) : 0) +
+                           (!kBias ? 0 : kByToken ? 4 * kLogMinChunk : 6 * kLogBiases);
+          k_logits<TI, TO, kTable, kBias, kByToken><<<grid, kLogThreads, smem, st>>>(a, chunk, wide, h->d_small);
           CK(cudaGetLastError());
           return (int)BPE_OK;
         };
         using Yes = std::true_type;
         using No = std::false_type;
-        return !table ? launch(No{}, No{}) : by_bias ? launch(Yes{}, Yes{}) : launch(Yes{}, No{});
+        if (!table) return launch(No{}, No{}, No{});
+        if (!by_bias) return launch(Yes{}, No{}, No{});
+        return chunk <= kLogMinChunk ? launch(Yes{}, Yes{}, Yes{}) : launch(Yes{}, Yes{}, No{});
       });
     });
   });
