@@ -19,7 +19,13 @@ __device__ __forceinline__ bool emb_row_ok(int32_t id, int64_t n_rows) { return 
 
 // A block takes rows of tokens x tx threads: each thread holds kEmbRows tokens'
 // vectors of V elements in flight at one column and walks the columns in steps
-// of tx vectors.
+// of tx vectors. V is 8 where rows are aligned for it, else 2 or 1.
+//
+// One product an element: bound by HBM, and by the L2 from which frequent rows
+// come again, so rows are kept there and the output streams past. 65,536 tokens
+// of a Zipf law, 4,096 columns, f32 to bf16: 123 us for the 731 MB of distinct
+// rows and output, 5.9 TB/s. With blocks of 256 threads it took 131 us, with
+// more tokens a thread up to 152, with 512 threads 159.
 constexpr int kEmbRows = 2;
 
 template <class TW, class TO, int V>
@@ -72,7 +78,9 @@ constexpr int kFillThreads = 512;
 // Rows [r0, r1) without a token become zeros: the CTA reads every id and marks
 // the rows that are met; then each thread takes a row and stores its 16-byte
 // aligned inside in bulk from a page of zeros in shared memory, which leaves
-// the SM's issue slots free, and its ragged ends by element.
+// the SM's issue slots free, and its ragged ends by element. Alone, with eight
+// blocks an SM, 6.5 to 7.0 TB/s; with one 4.4, since SMs differ in what they
+// can write and one of two neighbours may get two blocks.
 struct FillArgs {
   const int32_t* ids;
   int64_t n, n_rows;
@@ -157,6 +165,10 @@ struct SortArgs {
 // distributed shared memory) and over digits gives each warp its first place
 // for each digit; then the warp walks its run again, 32 tokens at a time, and
 // a match of equal digits ranks them in token order.
+//
+// Bound by the latency of its steps, not by bytes: 65,536 tokens into 69,424
+// rows take 21 us, most of which the zeroing of rows hides. A cluster's barrier
+// costs less than the launches that it saves.
 __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
   extern __shared__ __align__(16) int32_t sort_smem[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -267,7 +279,8 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(SortArgs a) {
 // places of its own. It counts all tokens into buckets of neighbouring rows,
 // which gives each bucket's first place, and in its token's bucket it counts
 // the keys below the token's. All blocks count the same, but none waits for
-// another: the passes of a sort do, twice each.
+// another: the passes of a sort do, twice each. 9,001 tokens: 8.0 us, against
+// 20 for comparing every token with every other, without buckets.
 constexpr int kRankEach = 24;  // tokens of a thread
 constexpr int kRankThreads = 512;
 constexpr int kRankTokens = kRankEach * kRankThreads;
@@ -414,6 +427,12 @@ __device__ __forceinline__ void add_vec(float (&acc)[V], const Vec<T, V>& v) {
 //     and end inside its chunk;
 //   * what the chunk adds to a row that reaches past it goes to `partial`,
 //     which k_emb_join adds up in order.
+// Tokens come through a ring of asynchronous copies in shared memory (8 KB a
+// warp in flight without registers for them), and sums run two an instruction.
+// Bound by HBM: 65,536 tokens of 4,096 bf16 columns, 537 MB, and the rows that
+// they meet written once: 111 us, beside which the zeros of the other rows are
+// written (190 us in all, 1.1 GB). With one warp a row, and long rows cut in
+// pieces, the kernel before took 301 us.
 template <class TG, class TW, int V>
 __device__ __forceinline__ void sum_chunk(const SumArgs<TG, TW>& a, const uint2* sorted, int64_t c0, int64_t c1,
                                           int run, unsigned char* sum_smem) {
@@ -616,7 +635,9 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_sum(SumArgs<TG, TW> a) {
 // Up to kSmallTokens tokens in one launch: blocks [0, chunks) rank the tokens
 // by comparing each with every other, all of them in each block, which is
 // sooner done than another kernel is begun, and sum a chunk of whole rows; the
-// others zero rows without a token.
+// others zero rows without a token. 300 tokens of 512 f32 columns into 768
+// rows: 8.6 us, latency (14.8 as sort, sums and join); 7 tokens into 69,424 rows
+// of 1,600: 64 us, the rate of the zeros.
 template <class TG, class TW, int V>
 __global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a, FillArgs f, int64_t n_chunks,
                                                               DevSmall* small) {
@@ -669,7 +690,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_small(SumArgs<TG, TW> a,
 // The parts of a row that reaches past a chunk, joined in order by the block
 // of the chunk that it begins in. A chunk's part is its second one if the row
 // begins inside it, and its first one otherwise. The sorted tokens are older
-// than the kernel before, so they are read before it ends.
+// than the kernel before, so they are read before it ends. 11 us for the 256
+// chunks of 65,536 tokens, most of it the latency of a few dependent reads.
 template <class TG, class TW, int V>
 __global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a) {
   constexpr int kPer = kSumCols / 32;
@@ -796,7 +818,8 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     if (n_rows == 0 || dim == 0) return BPE_OK;
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
-    // Tokens of a warp: as many as leave a block for every SM.
+    // Tokens of a warp: as many as leave a block for every SM. At most 32:
+    // 65,536 tokens took 199 us with 16, which doubles the parts to join.
     const int64_t groups = (dim + kSumCols - 1) / kSumCols;
     int run = kSumMaxRun;
     while (run > 2 && (n_ids / (kSumWarps * run)) * groups < h->n_sms) run /= 2;
@@ -816,13 +839,17 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     f.element = (int)type_size(grad_weight_type);
     f.row_bytes = dim * f.element;
     f.stride_bytes = grad_weight_stride * f.element;
+    // The single launch's rank takes n^2 / 1,024 steps of a thread; placing by
+    // rank counts all keys in every block, n / 512 steps of a thread, which
+    // shared memory bounds too (8 us against the sort's 18 at 9,001).
     const bool small = n_ids <= kSmallTokens && n_rows < kSmallRows;
     const bool rank = !small && n_ids <= kRankTokens && (n_rows + 1) * n_ids < (1ll << 32);
     const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of a sort, where a few tokens' rows are too many to rank
     // Zeros beside the kernels that find and sum the tokens, fewer blocks where
     // each would have under 32 KB to write. Where they take longer than the
     // sort they go on a stream of their own, so that the sums need not wait
-    // for them; that costs four calls on the host.
+    // for them; that costs four calls on the host, 5 us (where tokens are
+    // placed by rank it would gain 1: 31.9 us against 32.8 for 9,001 tokens).
     const bool aside = !small && !rank && !accumulate && n_rows * f.row_bytes >= (64ll << 20);
     int64_t fillers = 0;
     if (!accumulate) {

@@ -229,7 +229,7 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // instructions an id. Bound by HBM for the pass (384 rows of 113,645 bf16:
 // 29.7 us, 5.9 TB/s; with a mask for each row 31.6) and, with a history, by the
 // latency of a CTA's steps: lists, barrier, pass, barrier, the tokens again
-// (56 us with 3,000 prompt and 450 output tokens a row on average). What was
+// (57 us with 3,000 prompt and 450 output tokens a row on average). What was
 // slower for that case: a word for each token looked at in the pass (most warps
 // hold a concerned token, and the whole warp waits for its division: 135 us), a
 // hash table filled by atomics that return a value (a chain of waits for each
@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
   };
   __syncthreads();
   if (r.n_prompt + r.n_output > 0 || kByToken) {
-    // list the tokens that are concerned but for those with a listed bias, kLogThreads words of bits at most at a time, and share them out
+    // list the tokens that are concerned but for those with a listed bias,
+    // kLogThreads words of bits at most at a time, and share them out
     for (int w0 = 0; w0 < chunk / 32; w0 += kLogThreads) {
       const int w = w0 + tid;
       const uint32_t bits = w < chunk / 32 ? kByToken ? t.bits[w] | t.biased[w] : t.bits[w] & ~t.biased[w] : 0;
