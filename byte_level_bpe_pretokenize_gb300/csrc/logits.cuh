@@ -35,30 +35,32 @@ __device__ __forceinline__ uint32_t log_equal(const uint4& p, uint32_t twice) {
 
 // What a row's history says about a chunk, in shared memory: a bit for each
 // token that occurs in it, one for each that has a bias, and the times a token
-// occurs in the output. Outputs of up to kLogSaid tokens are listed as they
-// are, with a bit for each token among them, and an occurrence is counted when
-// it is asked for; longer ones have a count for each token (in 16 bits where
-// that is enough), and shorter chunks. The bits and counts are added to without
-// a look at what was there, so nothing waits for shared memory.
+// occurs in the output. Outputs of up to kLogSaid tokens have a bit for a
+// token's first occurrence and one for whether there are more; those are listed
+// and counted when they are asked for. Longer outputs have a count for each
+// token (in 16 bits where that is enough), and shorter chunks. All but the first
+// bit are added to without a look at what was there, so that nothing waits for
+// shared memory.
 struct LogTable {
   uint32_t* bits;    // [chunk / 32]
   uint32_t* biased;  // [chunk / 32]
   uint32_t* twice;   // [chunk / 32] tokens with more than one bias
   uint32_t* said;    // [chunk / 32], where the output is listed
-  uint16_t* list;    // [kLogSaid] the chunk's output tokens, in any order
+  uint32_t* again;   // [chunk / 32] said more than once, likewise
+  uint16_t* list;    // [kLogSaid] the chunk's output tokens but for the first of each, in any order
   int* listed;       // how many
   uint32_t* counts;  // [chunk] or, in 16 bits, [chunk / 2]; where the output is counted
   int wide;          // bits of a count; 0: the output is listed
 
   __host__ __device__ static constexpr int bytes(int chunk, bool by_output, int wide) {
-    return 3 * chunk / 8 + (!by_output ? 0 : wide ? chunk * wide / 8 : chunk / 8 + 2 * kLogSaid);
+    return 3 * chunk / 8 + (!by_output ? 0 : wide ? chunk * wide / 8 : chunk / 4 + 2 * kLogSaid);
   }
   __device__ __forceinline__ LogTable(uint32_t* smem, int chunk, int wide_, int* listed_)
       : bits(smem), biased(smem + chunk / 32), twice(smem + 2 * chunk / 32), said(smem + 3 * chunk / 32),
-        list(reinterpret_cast<uint16_t*>(smem + 4 * chunk / 32)), listed(listed_), counts(smem + 3 * chunk / 32),
-        wide(wide_) {}
+        again(smem + 4 * chunk / 32), list(reinterpret_cast<uint16_t*>(smem + 5 * chunk / 32)), listed(listed_),
+        counts(smem + 3 * chunk / 32), wide(wide_) {}
   __device__ __forceinline__ void clear(int chunk, bool by_output) const {
-    const int words = 3 * chunk / 32 + (!by_output ? 0 : wide ? chunk * wide / 32 : chunk / 32);
+    const int words = 3 * chunk / 32 + (!by_output ? 0 : wide ? chunk * wide / 32 : chunk / 16);
     for (int v = threadIdx.x; v < words / 4; v += kLogThreads)
       reinterpret_cast<uint4*>(bits)[v] = make_uint4(0, 0, 0, 0);
     // no token of a chunk is 0xFFFF, which fills the last vector of the list
@@ -69,22 +71,24 @@ struct LogTable {
   }
   __device__ __forceinline__ void see(int v) const { atomicOr(&bits[v >> 5], 1u << (v & 31)); }
   __device__ __forceinline__ void say(int v) const {
-    see(v);
     if (wide == 16) {
       atomicAdd(&counts[v >> 1], (v & 1) ? 0x10000u : 1u);
     } else if (wide) {
       atomicAdd(&counts[v], 1u);
     } else {
-      atomicOr(&said[v >> 5], 1u << (v & 31));
-      list[atomicAdd(listed, 1)] = (uint16_t)v;
+      const uint32_t bit = 1u << (v & 31);
+      if (atomicOr(&said[v >> 5], bit) & bit) {
+        atomicOr(&again[v >> 5], bit);
+        list[atomicAdd(listed, 1)] = (uint16_t)v;
+      }
     }
   }
   __device__ __forceinline__ bool seen(int v) const { return bits[v >> 5] >> (v & 31) & 1; }
   __device__ __forceinline__ uint32_t times(int v) const {
     if (wide == 16) return counts[v >> 1] >> ((v & 1) * 16) & 0xFFFFu;
     if (wide) return counts[v];
-    if (!(said[v >> 5] >> (v & 31) & 1)) return 0;
-    uint32_t k = 0;
+    uint32_t k = said[v >> 5] >> (v & 31) & 1;
+    if (!(again[v >> 5] >> (v & 31) & 1)) return k;
     const int vecs = (*listed + 7) / 8;
     const uint32_t twice = (uint32_t)v * 0x10001u;
     const uint4* from = reinterpret_cast<const uint4*>(list);
@@ -161,6 +165,14 @@ __device__ __forceinline__ float log_penalty(const LogRow& r, float x, uint32_t 
   return times ? x - r.freq * (float)times - r.pres : x;
 }
 
+// A byte of x's top bit in each place, for the two bytes that kSelect names.
+template <uint32_t kSelect>
+__device__ __forceinline__ uint32_t log_halves(uint32_t x) {
+  uint32_t y;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(x), "n"(kSelect));
+  return y;
+}
+
 // Tokens [v0, v0 + n) of a row pass through registers once, 16 bytes of input
 // at a time, and leave with the mask applied; by kThreads threads, of which
 // this is tid. The first vectors are loaded before row() gives the row's mask.
@@ -174,6 +186,10 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
   int head = (int)((-reinterpret_cast<uintptr_t>(in) & 15) / sizeof(TI));
   if (reinterpret_cast<uintptr_t>(out + head) & 15) head = n;
   head = min(head, n);
+  if (!a.mask && a.logits == a.out) {  // in place, nothing to do but what row() prepares
+    row();
+    return;
+  }
   const int groups = (n - head) / kLogGroup;
   constexpr int kAhead = sizeof(TI) == 4 ? kLogAhead / 2 : kLogAhead;
   Vec<TI, kLogGroup> x[kAhead];
@@ -194,13 +210,17 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
       const uint32_t bits = mask ? log_open(mask, (int)v0 + v, words) : 0xFFFFFFFFu;
       Vec<TO, kLogGroup> o;
       if constexpr (std::is_same_v<TI, TO> && sizeof(TI) == 2) {
-        // pairs of bit patterns, without a conversion
+        // pairs of bit patterns, without a conversion; the product puts four
+        // bits into the top bits of its bytes, which become halves of a mask
         const uint32_t* from = reinterpret_cast<const uint32_t*>(x[q].x);
         constexpr uint32_t kShut = std::is_same_v<TI, __half> ? 0xFC00FC00u : 0xFF80FF80u;  // twice -infinity
 #pragma unroll
-        for (int e = 0; e < kLogGroup / 2; ++e) {
-          const uint32_t open = (bits >> (2 * e) & 1 ? 0xFFFFu : 0u) | (bits >> (2 * e + 1) & 1 ? 0xFFFF0000u : 0u);
-          reinterpret_cast<uint32_t*>(o.x)[e] = (from[e] & open) | (kShut & ~open);
+        for (int e = 0; e < kLogGroup / 2; e += 2) {
+          const uint32_t four = (bits >> (2 * e) & 15) * 0x10204080u;
+          const uint32_t open[2] = {log_halves<0x9988>(four), log_halves<0xBBAA>(four)};
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            reinterpret_cast<uint32_t*>(o.x)[e + f] = (from[e + f] & open[f]) | (kShut & ~open[f]);
         }
       } else {
 #pragma unroll
@@ -226,15 +246,18 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // they are made, and biases are listed in theirs: nothing depends on timing.
 //
 // All CTAs of a row read its whole history, which is L2 traffic and a few
-// instructions an id. Bound by HBM for the pass (384 rows of 113,645 bf16:
-// 29.7 us, 5.9 TB/s; with a mask for each row 31.6) and, with a history, by the
+// instructions an id. Bound by HBM for the pass (384 rows of 113,645 bf16 with a
+// mask for each: 28.5 us, 6.3 TB/s) and, with a history, by issue and by the
 // latency of a CTA's steps: lists, barrier, pass, barrier, the tokens again
-// (57 us with 3,000 prompt and 450 output tokens a row on average). What was
-// slower for that case: a word for each token looked at in the pass (most warps
-// hold a concerned token, and the whole warp waits for its division: 135 us), a
-// hash table filled by atomics that return a value (a chain of waits for each
-// id: 84 us), warps that gather while others pass (152 us), the last CTA of a
-// row writing for all (119 us), a second launch a row (82 us).
+// (53 us with 3,000 prompt and 450 output tokens a row on average; without the
+// last step 41). What was slower for that case: a word for each token looked at
+// in the pass (most warps hold a concerned token, and the whole warp waits for
+// its division: 135 us), a hash table filled by atomics that return a value (a
+// chain of waits for each id: 84 us), warps that gather while others pass
+// (152 us), the last CTA of a row writing for all (119 us), a second launch a
+// row (82 us), logits changed in shared memory between asynchronous copies and
+// one store (67 us, and 33 without a history: fewer CTAs fit an SM), all outputs
+// listed and not only the repeated ones (57 us).
 template <class TI, class TO, bool kTable, bool kBias, bool kByToken>
 __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, int chunk, int wide, DevSmall* small) {
   extern __shared__ __align__(16) uint32_t log_smem[];
@@ -258,12 +281,11 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
     r = log_row(a, b, kTable, &bad);
     if (!kTable || !r.concerned) return r.mask;
     __syncthreads();
-    each_id<kLogIds>(r.prompt, r.n_prompt, tid, kLogThreads, [&](uint32_t id) {
-      if (id - low < (uint32_t)n) t.see((int)(id - low));
-      bad |= id >= vocab;
-    });
-    each_id<kLogIds>(r.output, r.n_output, tid, kLogThreads, [&](uint32_t id) {
-      if (id - low < (uint32_t)n) t.say((int)(id - low));
+    each_id<kLogIds>(r.prompt, r.n_prompt, r.output, r.n_output, tid, kLogThreads, [&](uint32_t id, bool said) {
+      if (id - low < (uint32_t)n) {
+        t.see((int)(id - low));
+        if (said) t.say((int)(id - low));
+      }
       bad |= id >= vocab;
     });
     if (kBias && warp == kLogWarps - 1) {
@@ -425,6 +447,7 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
     const bool by_bias = a.bias_ids && a.n_bias > 0;
     const bool table = by_bias || (a.prompt_ids && a.repetition) ||
                        (a.output_ids && (a.repetition || a.frequency || a.presence));
+    if (!table && !a.mask && a.logits == a.out) return BPE_OK;
     // Tokens of a CTA: long chunks read the history less often and hide its
     // latency behind a longer pass; short ones spread few rows over more SMs,
     // and leave room for counts.

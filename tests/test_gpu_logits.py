@@ -269,6 +269,27 @@ def test_in_place(tok, dtype):
     assert got is s["logits"] and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("first,stride", [(0, 40_000), (1, 40_003), (3, 40_001)])
+def test_in_place_without_masks(tok, dtype, first, stride):
+    """Only the tokens that the history or a bias concerns are touched."""
+    import torch
+    n, vocab = 5, 40_000
+    s = make(n, vocab, 900, 300, 40, 0, 25, dtype)
+    whole = torch.randn(first + n * stride, device="cuda").to(dtypes()[dtype])
+    before = whole.clone()
+    view = torch.as_strided(whole, (n, vocab), (stride, 1), first)
+    s["logits"] = view.clone()
+    want = call(tok, s)
+    s["logits"] = view
+    assert call(tok, s, out=view) is view
+    assert torch.equal(view, want)
+    torch.as_strided(before, (n, vocab), (stride, 1), first).copy_(want)
+    assert torch.equal(whole, before)
+    nothing = {"logits": view, "mask": None}
+    assert torch.equal(call(tok, nothing, out=view), want)
+
+
 def test_logits_past_2_to_the_31_elements(tok):
     import torch
     n, vocab = 20_000, 113_645  # 2.27e9 elements
