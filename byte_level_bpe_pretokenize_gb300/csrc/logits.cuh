@@ -21,6 +21,7 @@ constexpr int kLogBlocks = 5;         // CTAs an SM at least, while chunks can b
 constexpr int kLogMinChunk = 2048;   // tokens of a CTA
 constexpr int kLogMaxChunk = 16384;
 constexpr int kLogDenseChunk = 8192; // with a count for each token
+constexpr int kLogWords = 2;         // words of bits of a thread
 constexpr int kLogList = 1024;       // concerned tokens that a CTA lists at once
 constexpr int kLogBiases = 512;      // biases of a chunk that it lists
 constexpr int kLogSaid = 2048;       // output tokens of a chunk that it lists
@@ -249,7 +250,7 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // instructions an id. Bound by HBM for the pass (384 rows of 113,645 bf16 with a
 // mask for each: 28.5 us, 6.3 TB/s) and, with a history, by issue and by the
 // latency of a CTA's steps: lists, barrier, pass, barrier, the tokens again
-// (53 us with 3,000 prompt and 450 output tokens a row on average; without the
+// (47.5 us with 3,000 prompt and 450 output tokens a row on average; without the
 // last step 41). What was slower for that case: a word for each token looked at
 // in the pass (most warps hold a concerned token, and the whole warp waits for
 // its division: 135 us), a hash table filled by atomics that return a value (a
@@ -339,45 +340,52 @@ __global__ void __launch_bounds__(kLogThreads, 8) k_logits(bpe_logits_args a, in
   };
   __syncthreads();
   if (r.n_prompt + r.n_output > 0 || kByToken) {
-    // list the tokens that are concerned but for those with a listed bias,
-    // kLogThreads words of bits at most at a time, and share them out
-    for (int w0 = 0; w0 < chunk / 32; w0 += kLogThreads) {
-      const int w = w0 + tid;
-      const uint32_t bits = w < chunk / 32 ? kByToken ? t.bits[w] | t.biased[w] : t.bits[w] & ~t.biased[w] : 0;
-      const int mine = __popc(bits);
-      int upto = mine;
+    // list the tokens that are concerned and not shut, but for those with a
+    // listed bias, from kLogWords words of bits a thread, and share them out
+    static_assert(kLogMaxChunk <= 32 * kLogWords * kLogThreads);
+    uint32_t bits[kLogWords];
+    int mine = 0;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-        if (lane >= d) upto += o;
-      }
-      if (lane == 31) warp_sum[warp] = upto;
+    for (int q = 0; q < kLogWords; ++q) {
+      const int w = tid + q * kLogThreads;
+      bits[q] = w >= (n + 31) / 32 ? 0 : kByToken ? t.bits[w] | t.biased[w] : t.bits[w] & ~t.biased[w];
+      if (r.mask && bits[q]) bits[q] &= __ldg(r.mask + (v0 >> 5) + w);
+      mine += __popc(bits[q]);
+    }
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int k = 0; k < kLogWarps; ++k) {
+      if (k < warp) upto += warp_sum[k];
+      total += warp_sum[k];
+    }
+    for (int k0 = 0; k0 < total; k0 += kLogList) {
+      int at = upto - mine - k0;
+#pragma unroll
+      for (int q = 0; q < kLogWords; ++q)
+        for (uint32_t m = bits[q]; m; m &= m - 1, ++at)
+          if ((uint32_t)at < kLogList) list[at] = (uint16_t)((tid + q * kLogThreads) * 32 + __ffs(m) - 1);
       __syncthreads();
-      int total = 0;
-#pragma unroll
-      for (int k = 0; k < kLogWarps; ++k) {
-        if (k < warp) upto += warp_sum[k];
-        total += warp_sum[k];
+      for (int k = tid; k < min(total - k0, kLogList); k += kLogThreads) {
+        const int v = list[k];
+        out[v] = from_f32<TO>(kByToken ? penalised(v) + bias_value[v] : penalised(v));
       }
-      for (int k0 = 0; k0 < total; k0 += kLogList) {
-        int at = upto - mine - k0;
-        for (uint32_t m = bits; m && at < kLogList; m &= m - 1, ++at)
-          if (at >= 0) list[at] = (uint16_t)(w * 32 + __ffs(m) - 1);
-        __syncthreads();
-        for (int k = tid; k < min(total - k0, kLogList); k += kLogThreads) {
-          const int v = list[k];
-          if (open(v)) out[v] = from_f32<TO>(kByToken ? penalised(v) + bias_value[v] : penalised(v));
-        }
-        __syncthreads();
-      }
-      __syncthreads();  // warp_sum is read by all before it is written again
+      if (k0 + kLogList < total) __syncthreads();
     }
   }
   if (!kBias || kByToken) return;
   const int m = n_biases;
   if (m <= kLogBiases) {
-    // whoever has a token's first bias adds up all of them
-    for (int k = tid; k < m; k += kLogThreads) {
+    // whoever has a token's first bias adds up all of them; from the last
+    // thread on, since the first ones have most of the list above
+    for (int k = kLogThreads - 1 - tid; k < m; k += kLogThreads) {
       const int v = bias_token[k];
       float sum = bias_value[k];
       bool first = true;
