@@ -17,7 +17,7 @@ constexpr int kLogWarps = kLogThreads / 32;
 constexpr int kLogGroup = 8;         // tokens of a vector
 constexpr int kLogAhead = 2;         // vectors of a thread in flight
 constexpr int kLogIds = 2;           // 16-byte loads of ids of a thread in flight
-constexpr int kLogBlocks = 5;         // CTAs an SM at least, while chunks can be halved
+constexpr int kLogBlocks = 2;        // CTAs an SM at least, while chunks can be halved
 constexpr int kLogMinChunk = 2048;   // tokens of a CTA
 constexpr int kLogMaxChunk = 16384;
 constexpr int kLogDenseChunk = 8192; // with a count for each token
@@ -250,7 +250,7 @@ __device__ __forceinline__ void log_pass(const bpe_logits_args& a, int64_t b, in
 // instructions an id. Bound by HBM for the pass (384 rows of 113,645 bf16 with a
 // mask for each: 28.5 us, 6.3 TB/s) and, with a history, by issue and by the
 // latency of a CTA's steps: lists, barrier, pass, barrier, the tokens again
-// (47.5 us with 3,000 prompt and 450 output tokens a row on average; without the
+// (48 us with 3,000 prompt and 450 output tokens a row on average; without the
 // last step 41). What was slower for that case: a word for each token looked at
 // in the pass (most warps hold a concerned token, and the whole warp waits for
 // its division: 135 us), a hash table filled by atomics that return a value (a
@@ -458,7 +458,9 @@ extern "C" int bpe_adjust_logits(bpe_handle* h, const bpe_logits_args* args, bpe
     if (!table && !a.mask && a.logits == a.out) return BPE_OK;
     // Tokens of a CTA: long chunks read the history less often and hide its
     // latency behind a longer pass; short ones spread few rows over more SMs,
-    // and leave room for counts.
+    // and leave room for counts. At least 2 CTAs an SM: 100 rows of 32,256 f16
+    // take 8.3 us, with 5 at least 9.4, with 1 9.2; 48 rows of 69,424 bf16 take
+    // 12.2 us either way, with 1 at least 14.
     const int wide = !a.output_ids || a.output_capacity <= kLogSaid ? 0 : a.output_capacity <= 0xFFFF ? 16 : 32;
     int chunk = !table || !wide ? kLogMaxChunk : wide == 16 ? kLogDenseChunk : kLogDenseChunk / 2;
     while (chunk > kLogMinChunk && a.n_rows * ((a.n_vocab + chunk - 1) / chunk) < kLogBlocks * h->n_sms) chunk /= 2;
