@@ -842,7 +842,7 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     // The single launch's rank takes n^2 / 1,024 steps of a thread; placing by
     // rank counts all keys in every block, n / 512 steps of a thread, which
     // shared memory bounds too (8 us against the sort's 18 at 9,001).
-    const bool small = n_ids <= kSmallTokens && n_rows < kSmallRows;
+    const bool small = n_ids <= kSmallTokens && (n_rows < kSmallRows || n_ids == 0);
     const bool rank = !small && n_ids <= kRankTokens && (n_rows + 1) * n_ids < (1ll << 32);
     const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of a sort, where a few tokens' rows are too many to rank
     // Zeros beside the kernels that find and sum the tokens, fewer blocks where

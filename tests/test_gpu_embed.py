@@ -232,6 +232,18 @@ def test_gradient_of_a_large_table(tok, grad, weight, dim):
     assert torch.equal(out, after)
 
 
+@pytest.mark.parametrize("n", [0, 1, 5])
+def test_gradient_of_few_tokens_in_more_than_2_to_the_23_rows(tok, n):
+    import torch
+    rows = 2 ** 23 + 3
+    ids = torch.tensor([rows - 1, 0, 7, 0, rows - 1][:n], dtype=torch.int32, device="cuda")
+    grad = torch.arange(1, 2 * n + 1, dtype=torch.float32, device="cuda").reshape(n, 2)
+    want = torch.zeros(rows, 2, device="cuda").index_add_(0, ids.long(), grad)  # whole numbers: exact in any order
+    out = torch.full((rows, 2), 5.0, device="cuda")
+    assert torch.equal(tok.embed_grad(ids, grad, rows, out=out), want)
+    assert torch.equal(tok.embed_grad(ids, grad, rows, out=out, accumulate=True), 2 * want)
+
+
 def test_gradient_skips(tok):
     import torch
     ids, g = make_ids(700, 20, "uniform"), rand((700, 40), "f32", 11)
