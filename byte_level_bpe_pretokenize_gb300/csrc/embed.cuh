@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kRankThreads) k_emb_rank(RankArgs a) {
 constexpr int kSumWarps = 8;
 constexpr int kSumCols = 512;     // columns of a block
 constexpr int kSumMaxRun = 32;    // tokens of a warp, at most
+constexpr int kSumMinRun = 2;     // and at least
 constexpr int kSmallTokens = 512; // most tokens of the single launch
 constexpr int64_t kSmallRows = (1ll << 32) / kSmallTokens - 1;  // and rows: a key and a token fit 32 bits
 constexpr int kSumRing = 8320;    // bytes of a warp's tokens in flight
@@ -744,6 +745,24 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_emb_join(SumArgs<TG, TW> a) 
   }
 }
 
+// Tokens of a warp of k_emb_sum: as many as leave a block for every SM, at most
+// 32 (65,536 tokens took 199 us with 16, which doubles the parts to join).
+int emb_run(int64_t n_ids, int64_t groups, int n_sms) {
+  int run = kSumMaxRun;
+  while (run > kSumMinRun && (n_ids / (kSumWarps * run)) * groups < n_sms) run /= 2;
+  return run;
+}
+
+// At least chunks * dim for the chunks that emb_run cuts, and never less for
+// fewer tokens or columns, so that the workspace of a call is enough for every
+// smaller one. Shorter runs, which fewer tokens get, make more chunks: below 32
+// tokens a run, twice the run would leave an SM without a block, which bounds
+// the chunks of all column groups by 2 n_sms + 3 groups.
+int64_t emb_chunk_columns(int64_t n_ids, int64_t dim, int64_t groups, int n_sms) {
+  auto chunks = [&](int64_t run) { return (n_ids + kSumWarps * run - 1) / (kSumWarps * run); };
+  return std::max(chunks(kSumMaxRun) * dim, std::min(chunks(kSumMinRun) * dim, (2 * n_sms + 3 * groups) * kSumCols));
+}
+
 int emb_check(const char* what, bpe_handle* h, const int32_t* ids, int64_t n_ids, const void* rows, int rows_type,
               int64_t n_rows, int64_t dim, int64_t rows_stride, const void* toks, int toks_type, int64_t toks_stride) {
   const std::string name(what);
@@ -818,18 +837,25 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     if (n_rows == 0 || dim == 0) return BPE_OK;
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
-    // Tokens of a warp: as many as leave a block for every SM. At most 32:
-    // 65,536 tokens took 199 us with 16, which doubles the parts to join.
     const int64_t groups = (dim + kSumCols - 1) / kSumCols;
-    int run = kSumMaxRun;
-    while (run > 2 && (n_ids / (kSumWarps * run)) * groups < h->n_sms) run /= 2;
+    const int run = emb_run(n_ids, groups, h->n_sms);
     const int64_t chunk = kSumWarps * run, n_chunks = (n_ids + chunk - 1) / chunk;
-    const size_t pair = align256((size_t)n_ids * 8), parts = align256((size_t)n_chunks * 2 * (size_t)dim * 4);
-    rc = ensure_ws(h, 2 * pair + parts);
-    if (rc) return rc;
-    unsigned char* ws = static_cast<unsigned char*>(h->d_ws);
-    uint2* const ping[2] = {reinterpret_cast<uint2*>(ws), reinterpret_cast<uint2*>(ws + pair)};
-    float* partial = reinterpret_cast<float*>(ws + 2 * pair);
+    // The single launch's rank takes n^2 / 1,024 steps of a thread; placing by
+    // rank counts all keys in every block, n / 512 steps of a thread, which
+    // shared memory bounds too (8 us against the sort's 18 at 9,001).
+    const bool small = n_ids <= kSmallTokens && (n_rows < kSmallRows || n_ids == 0);
+    const bool rank = !small && n_ids <= kRankTokens && (n_rows + 1) * n_ids < (1ll << 32);
+    uint2* ping[2] = {nullptr, nullptr};
+    float* partial = nullptr;
+    if (!small) {  // the single launch orders its tokens in shared memory and joins no parts
+      const size_t pair = align256((size_t)n_ids * 8);
+      rc = ensure_ws(h, 2 * pair + (size_t)emb_chunk_columns(n_ids, dim, groups, h->n_sms) * 2 * sizeof(float));
+      if (rc) return rc;
+      unsigned char* ws = static_cast<unsigned char*>(h->d_ws);
+      ping[0] = reinterpret_cast<uint2*>(ws);
+      ping[1] = reinterpret_cast<uint2*>(ws + pair);
+      partial = reinterpret_cast<float*>(ws + 2 * pair);
+    }
     FillArgs f{};
     f.ids = d_ids;
     f.n = n_ids;
@@ -839,11 +865,6 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     f.element = (int)type_size(grad_weight_type);
     f.row_bytes = dim * f.element;
     f.stride_bytes = grad_weight_stride * f.element;
-    // The single launch's rank takes n^2 / 1,024 steps of a thread; placing by
-    // rank counts all keys in every block, n / 512 steps of a thread, which
-    // shared memory bounds too (8 us against the sort's 18 at 9,001).
-    const bool small = n_ids <= kSmallTokens && (n_rows < kSmallRows || n_ids == 0);
-    const bool rank = !small && n_ids <= kRankTokens && (n_rows + 1) * n_ids < (1ll << 32);
     const int ctas = n_ids <= 2048 ? 1 : kSortCluster;  // of a sort, where a few tokens' rows are too many to rank
     // Zeros beside the kernels that find and sum the tokens, fewer blocks where
     // each would have under 32 KB to write. Where they take longer than the

@@ -423,8 +423,10 @@ int bpe_embed(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const void* d_
  * Sums are held in 32 bits and rounded once. Their order is fixed by the ids
  * alone, so equal inputs give equal bits. Tokens whose id is skip_id or out of
  * range add to no row (the latter are reported).
- * Workspace: 16 bytes a token, and for every 16 tokens or more 8 bytes a
- * column.
+ * Workspace: none up to 512 tokens (on a table of fewer than 2^23 - 1 rows),
+ * else 16 bytes a token, and 8 bytes a column for every 256 tokens or for
+ * every 16, up to 4 KB for twice the GPU's multiprocessors (and a little
+ * more); never more for fewer tokens or columns.
  */
 int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const void* d_grad_out, int grad_out_type,
                    int64_t grad_out_stride, float scale, int32_t skip_id, int64_t n_rows, int64_t dim,
