@@ -334,7 +334,13 @@ def bpe_destroy(handle: int) -> None:
 
 class Tokenizer:
     """A tokenizer on one GPU. Tensors are torch CUDA tensors on that GPU;
-    calls run on the current torch stream."""
+    calls run on the current torch stream.
+
+    All calls share one workspace on the GPU, so those made on different streams
+    (an encode that prefetches beside an embed_grad, say) must not overlap: let
+    one stream wait for the other, or use a Tokenizer each. Replays of a graph
+    that calls were captured in count as calls; they stay valid when a later
+    call outgrows the workspace, until close()."""
 
     def __init__(self, merges, vocab_bytes, vocab_offsets, device: int = 0):
         self.device = device

@@ -442,7 +442,7 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
       CK(cudaGetLastError());
       return BPE_OK;
     }
-    int rc = ensure_ws(h, (size_t)n_requests * sizeof(int64_t));
+    int rc = ensure_ws(h, (size_t)n_requests * sizeof(int64_t), st);
     if (rc) return rc;
     a.base = static_cast<int64_t*>(h->d_ws);
     k_plan_requests<<<kPlanCluster, kPlanSumThreads, 0, st>>>(a);

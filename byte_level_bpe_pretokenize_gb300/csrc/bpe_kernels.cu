@@ -1488,6 +1488,7 @@ int bpe_destroy(bpe_handle* h) {
   cudaFree(h->d_cache);
   cudaFree(h->d_small);
   cudaFree(h->d_ws);
+  for (void* p : h->kept_ws) cudaFree(p);
   for (auto& sl : h->slot) {
     cudaFree(sl.bytes);
     cudaFree(sl.offs);
@@ -1544,7 +1545,7 @@ int bpe_table_info(const bpe_handle* h, int64_t* n_merges, int64_t* n_vocab) {
 
 int bpe_workspace_bytes(const bpe_handle* h, int64_t* bytes) {
   if (!h || !bytes) return fail(BPE_ERR_INVALID_ARG, "bpe_workspace_bytes: bad arguments");
-  *bytes = (int64_t)h->ws_bytes;
+  *bytes = (int64_t)(h->ws_bytes + h->kept_bytes);
   return BPE_OK;
 }
 
@@ -1603,7 +1604,7 @@ int bpe_encode_batch(bpe_handle* h, const uint8_t* d_bytes, int64_t n_bytes, con
   // and the misses are every pre-token; queue indices must fit in 32 bits
   const bool memo = (h->call_memo == BPE_MEMO_ON || (h->call_memo == BPE_MEMO_AUTO && !h->cache_enabled)) &&
                     ws_sizes(n_bytes).miss_cap < (int64_t)UINT32_MAX;
-  int rc = ensure_ws(h, ws_sizes(n_bytes, memo).total);
+  int rc = ensure_ws(h, ws_sizes(n_bytes, memo).total, st);
   if (rc) return rc;
   if (!h->smem_set) {
     if ((rc = tiles_smem_setup())) return rc;
@@ -1734,7 +1735,7 @@ int bpe_encode_batch_host(bpe_handle* h, const uint8_t* h_bytes, int64_t n_bytes
     CK(cudaHostGetDevicePointer(reinterpret_cast<void**>(&h->d_totals), h->h_totals, 0));
     h->h_totals_cap = n_slices;
   }
-  int rc = ensure_ws(h, ws_sizes(h->slot_bytes).total);
+  int rc = ensure_ws(h, ws_sizes(h->slot_bytes).total, (cudaStream_t)stream);
   if (rc) return rc;
   if (!h->smem_set) {
     if ((rc = tiles_smem_setup())) return rc;
@@ -1821,7 +1822,7 @@ int bpe_decode_batch(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const i
   const int64_t n_tiles = n_ids / kDecIds + 1;
   const int64_t n_blocks = (n_tiles + kDecScanThreads - 1) / kDecScanThreads;
   const size_t a1 = align256((size_t)n_tiles * sizeof(uint64_t)), a2 = align256((size_t)n_blocks * sizeof(uint64_t));
-  int rc = ensure_ws(h, a1 + a2 + align256((size_t)n_tiles * sizeof(int64_t)));
+  int rc = ensure_ws(h, a1 + a2 + align256((size_t)n_tiles * sizeof(int64_t)), st);
   if (rc) return rc;
   uint64_t* tile_base = reinterpret_cast<uint64_t*>(h->d_ws);
   uint64_t* block_sum = reinterpret_cast<uint64_t*>(static_cast<unsigned char*>(h->d_ws) + a1);

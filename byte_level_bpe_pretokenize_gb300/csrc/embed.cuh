@@ -849,7 +849,8 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
     float* partial = nullptr;
     if (!small) {  // the single launch orders its tokens in shared memory and joins no parts
       const size_t pair = align256((size_t)n_ids * 8);
-      rc = ensure_ws(h, 2 * pair + (size_t)emb_chunk_columns(n_ids, dim, groups, h->n_sms) * 2 * sizeof(float));
+      const size_t parts = (size_t)emb_chunk_columns(n_ids, dim, groups, h->n_sms) * 2 * sizeof(float);
+      rc = ensure_ws(h, 2 * pair + parts, st);
       if (rc) return rc;
       unsigned char* ws = static_cast<unsigned char*>(h->d_ws);
       ping[0] = reinterpret_cast<uint2*>(ws);

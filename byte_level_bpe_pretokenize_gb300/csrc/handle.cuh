@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <exception>
 #include <string>
+#include <vector>
 
 #include "../../include/bpe_gb300.h"
 
@@ -87,6 +88,9 @@ struct bpe_handle {
   bpe_impl::DevSmall* h_small = nullptr;  // pinned
   void* d_ws = nullptr;
   size_t ws_bytes = 0;
+  bool ws_captured = false;    // a graph may hold d_ws
+  std::vector<void*> kept_ws;  // outgrown blocks that a graph may hold, freed with the handle
+  size_t kept_bytes = 0;
   bool smem_set = false;
   cudaEvent_t ev_start = nullptr, ev_stop = nullptr;
   cudaEvent_t* ev_phase = nullptr;  // BPE_ENCODE_LAUNCHES + 1 caller-owned events, or null
@@ -112,15 +116,31 @@ struct bpe_handle {
 
 namespace bpe_impl {
 
-// The handle's workspace, grown to at least `need` bytes.
-inline int ensure_ws(bpe_handle* h, size_t need) {
-  if (need <= h->ws_bytes) return BPE_OK;
-  size_t sz = need + need / 4 + 4096;
-  if (h->d_ws) CK(cudaFree(h->d_ws));
-  h->d_ws = nullptr;
-  h->ws_bytes = 0;
-  CK(cudaMalloc(&h->d_ws, sz));
-  h->ws_bytes = sz;
+// The handle's workspace, grown to at least `need` bytes, for a call on st. A
+// block that a call under stream capture has used stays until the handle is
+// destroyed, for the graph's replays use it again.
+inline int ensure_ws(bpe_handle* h, size_t need, cudaStream_t st) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  CK(cudaStreamIsCapturing(st, &capture));
+  if (need > h->ws_bytes) {
+    if (h->ws_captured) {
+      try {
+        h->kept_ws.push_back(h->d_ws);
+      } catch (const std::exception& e) {
+        return fail(BPE_ERR_INTERNAL, e.what());
+      }
+      h->kept_bytes += h->ws_bytes;
+    } else if (h->d_ws) {
+      CK(cudaFree(h->d_ws));
+    }
+    h->d_ws = nullptr;
+    h->ws_bytes = 0;
+    h->ws_captured = false;
+    const size_t sz = need + need / 4 + 4096;
+    CK(cudaMalloc(&h->d_ws, sz));
+    h->ws_bytes = sz;
+  }
+  if (capture != cudaStreamCaptureStatusNone && need > 0) h->ws_captured = true;
   return BPE_OK;
 }
 

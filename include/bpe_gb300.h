@@ -105,7 +105,8 @@ int bpe_build(const int32_t* merges, int64_t n_merges, const uint8_t* vocab_byte
  *   - with the per-call memo on (bpe_set_call_memo), 2 bytes per input byte
  *     more and a table of at most 128 MiB.
  * The workspace grows (cudaFree of the old one, then cudaMalloc) the first
- * time a larger batch is seen. No kernel of the call waits on another CTA.
+ * time a larger batch is seen; a block that a captured call has used is not
+ * freed before bpe_destroy. No kernel of the call waits on another CTA.
  */
 int bpe_encode_batch(bpe_handle* h, const uint8_t* d_bytes, int64_t n_bytes, const int64_t* d_doc_offsets,
                      int64_t n_docs, int32_t* d_out_ids, int64_t out_capacity, int64_t* d_out_offsets,
@@ -332,8 +333,12 @@ int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int6
  * what is concerned is left out as stated below, nothing is read or written
  * out of range, and the next bpe_sync_status() on the handle returns
  * BPE_ERR_BAD_INPUT. A call that finds its workspace too small grows it
- * (cudaFree, cudaMalloc); make a call of the largest size before any stream
- * capture.
+ * (cudaFree, cudaMalloc), which a stream capture does not allow: before a
+ * capture make a call of the largest size, of each kind that is captured. A
+ * block that captured calls use is kept until bpe_destroy, so a graph's replays
+ * stay valid when a later call on the handle, the encoder's included, grows
+ * the workspace. Replays use the handle like calls: they must not overlap
+ * others on the GPU.
  */
 #define BPE_F32 0
 #define BPE_F16 1
@@ -523,9 +528,10 @@ int bpe_merges_monotone(const int32_t* merges, int64_t n_merges, int64_t n_vocab
 /* bpe_merges_monotone of the table a handle was built from. */
 int bpe_table_monotone(const bpe_handle* h, int* monotone);
 
-/* Bytes of device workspace the handle holds now (0 until a call needs it):
- * bpe_encode_batch, bpe_encode_batch_host and bpe_decode_batch grow it;
- * bpe_encode_batch_noalloc never does. */
+/* Bytes of device workspace the handle holds now (0 until a call needs it),
+ * with outgrown blocks that are kept for captured graphs: bpe_encode_batch,
+ * bpe_encode_batch_host, bpe_decode_batch, bpe_plan_blocks and bpe_embed_grad
+ * grow it; bpe_encode_batch_noalloc never does. */
 int bpe_workspace_bytes(const bpe_handle* h, int64_t* bytes);
 
 /* Frees the handle's device memory. Waits for its device first. */
