@@ -8,6 +8,11 @@
 // blocks. They are dealt from the free list in request order: with
 // G_i = g_0 + .. + g_i and A blocks left in the list, request i is served if
 // g_i = 0 or G_i <= A, and takes the list's entries [G_i - g_i, G_i).
+//
+// Where offsets fall, a request that begins below an earlier offset is refused,
+// for its tokens may be another's too. One that is left begins at the largest
+// offset so far, and a search of these largest offsets finds its tokens as a
+// search of the offsets does where none falls.
 
 namespace {
 
@@ -37,6 +42,8 @@ struct PlanArgs {
   int32_t* positions;
   int64_t* info;
   int64_t* base;           // [n] workspace: G_i - g_i, or -1 where not served
+  int64_t* high;           // [n] workspace, where offsets fall: the largest of offsets[0 .. i]
+  int64_t* falls;          // [1] workspace: whether they do
   DevSmall* small;
 };
 
@@ -44,7 +51,7 @@ struct PlanRequest {
   int64_t first, fresh;       // first new token, new tokens
   int32_t cached;             // tokens in the cache
   uint32_t held, gets;        // blocks it has, blocks it needs
-  bool ok;
+  bool ok, falls;             // falls: its end is below its first token
 };
 
 __device__ __forceinline__ PlanRequest plan_request(const PlanArgs& a, int64_t i) {
@@ -52,7 +59,8 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanArgs& a, int64_t i
   const int64_t end = a.offsets ? __ldg(a.offsets + i + 1) : i + 1;
   r.first = a.offsets ? __ldg(a.offsets + i) : i;
   r.cached = a.cached ? __ldg(a.cached + i) : 0;
-  r.fresh = end - r.first;
+  r.fresh = (int64_t)((uint64_t)end - (uint64_t)r.first);  // of any two numbers
+  r.falls = end < r.first;
   // the sum below INT32_MAX - block + 1, so that rounding up to blocks stays below 2^31
   r.ok = r.first >= 0 && end >= r.first && end <= a.n_slots && r.cached >= 0 &&
          r.cached + r.fresh <= (int64_t)INT32_MAX - (int64_t)a.block.d + 1;
@@ -96,6 +104,28 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* total, int64_t*
   return warp > 0 ? x + below : x;
 }
 
+// The largest x of the threads before this one (INT64_MIN for the first), and of
+// a block of kWarps warps.
+template <int kWarps>
+__device__ __noinline__ int64_t plan_highest_before(int64_t x, int64_t* block_most, int64_t* warp_most) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x = max(x, o);
+  }
+  int64_t before = __shfl_up_sync(0xFFFFFFFFu, x, 1);
+  if (lane == 0) before = INT64_MIN;
+  __syncthreads();  // warp_most may still be read from the last call
+  if (lane == 31) warp_most[warp] = x;
+  __syncthreads();
+  *block_most = INT64_MIN;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before = max(before, warp_most[w]);
+    *block_most = max(*block_most, warp_most[w]);
+  }
+  return before;
+}
+
 // Raises *to to the largest x of the block's threads.
 __device__ __forceinline__ void plan_max(unsigned long long* to, unsigned long long x) {
 #pragma unroll
@@ -110,7 +140,7 @@ constexpr int kPlanList = 2048;                              // requests that a 
 
 // Consecutive requests, in shared memory.
 struct PlanList {
-  int32_t start[kPlanList + 1];  // first new token, relative to the tile's
+  int32_t start[kPlanList + 1];  // first new token (the largest offset so far), relative to the tile's
   int32_t cached[kPlanList];     // -1 - (what is in the cache) for a request that is not ok
   int32_t held[kPlanList];
   int32_t base[kPlanList];       // G_i - g_i, -1 where not served
@@ -213,6 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_one(PlanArgs a, int tile)
   const int per = (n + kPlanThreads - 1) / kPlanThreads;
   uint32_t gets[kPer];
   int64_t mine = 0;
+  bool falls = false;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     const int i = tid * per + q;
@@ -224,9 +255,31 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_one(PlanArgs a, int tile)
     gets[q] = r.gets;
     mine += r.gets;
     bad |= !r.ok;
+    falls |= r.falls;
     if (lead) a.seq_lens[i] = r.ok ? (int32_t)(r.cached + r.fresh) : max(r.cached, 0);
   }
   if (tid == 0) list.start[n] = plan_relative(a.offsets ? __ldg(a.offsets + n) : a.n, t0);
+  if (__syncthreads_or(falls)) {
+    int64_t high = INT64_MIN, most;
+    for (int i = tid * per; i < min(tid * per + per, n); ++i) high = max(high, __ldg(a.offsets + i));
+    high = plan_highest_before<kPlanThreads / 32>(high, &most, warp_sum);
+    mine = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = tid * per + q;
+      if (q >= per || i >= n) break;
+      const int64_t first = __ldg(a.offsets + i);
+      high = max(high, first);
+      list.start[i] = plan_relative(high, t0);
+      if (first < high) {
+        gets[q] = 0;
+        if (list.cached[i] >= 0) list.cached[i] = -1 - list.cached[i];
+        if (lead) a.seq_lens[i] = -1 - list.cached[i];
+      }
+      mine += gets[q];
+    }
+    if (tid == 0) list.start[n] = plan_relative(max(most, __ldg(a.offsets + n)), t0);
+  }
   int64_t total;
   int64_t upto = plan_scan<kPlanThreads / 32>(mine, &total, warp_sum) - mine;
   unsigned long long best = 0;
@@ -259,7 +312,8 @@ constexpr int kPlanSumThreads = 1024;
 __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanSumThreads) k_plan_requests(PlanArgs a) {
   constexpr int kWarps = kPlanSumThreads / 32;
   __shared__ int64_t warp_sum[kWarps];
-  __shared__ int64_t part;
+  __shared__ longlong2 part;  // blocks of this part's requests, and whether offsets fall in it
+  __shared__ int64_t part_high;
   __shared__ unsigned long long taken;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = (int)cluster.block_rank();
@@ -269,19 +323,57 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanSumT
   const int64_t per = (a.n + kPlanCluster - 1) / kPlanCluster;
   const int64_t i0 = min(rank * per, a.n), i1 = min(i0 + per, a.n);
   int64_t mine = 0, total;
-  for (int64_t i = i0 + tid; i < i1; i += kPlanSumThreads) mine += plan_request(a, i).gets;
+  bool falls = false;
+  for (int64_t i = i0 + tid; i < i1; i += kPlanSumThreads) {
+    const PlanRequest r = plan_request(a, i);
+    mine += r.gets;
+    falls |= r.falls;
+  }
   plan_scan<kWarps>(mine, &total, warp_sum);
+  const int any = __syncthreads_or(falls);
   if (tid == 0) {
-    part = total;
+    part = make_longlong2(total, any);
     taken = 0;
   }
   cluster.sync();
   int64_t carry = 0, all = 0;
+  falls = false;
 #pragma unroll
   for (int q = 0; q < kPlanCluster; ++q) {
-    const int64_t v = *cluster.map_shared_rank(&part, q);
-    all += v;
-    if (q < rank) carry += v;
+    const longlong2 v = *cluster.map_shared_rank(&part, q);
+    all += v.x;
+    if (q < rank) carry += v.x;
+    falls |= v.y != 0;
+  }
+  if (rank == 0 && tid == 0) *a.falls = falls;
+  if (falls) {
+    // the sums once more, without the requests that begin below an earlier offset
+    int64_t high = INT64_MIN, most;
+    for (int64_t i = i0 + tid; i < i1; i += kPlanSumThreads) high = max(high, __ldg(a.offsets + i));
+    plan_highest_before<kWarps>(high, &most, warp_sum);
+    if (tid == 0) part_high = most;
+    cluster.sync();
+    high = INT64_MIN;
+    for (int q = 0; q < rank; ++q) high = max(high, *cluster.map_shared_rank(&part_high, q));
+    mine = 0;
+    for (int64_t j = i0; j < i1; j += kPlanSumThreads) {
+      const int64_t i = j + tid, first = i < i1 ? __ldg(a.offsets + i) : INT64_MIN;
+      const int64_t before = max(high, plan_highest_before<kWarps>(first, &most, warp_sum));
+      high = max(high, most);
+      if (i < i1) {
+        a.high[i] = max(before, first);
+        if (first >= before) mine += plan_request(a, i).gets;
+      }
+    }
+    plan_scan<kWarps>(mine, &total, warp_sum);
+    if (tid == 0) part.x = total;  // all have read what was there: they are past a cluster barrier since
+    cluster.sync();
+    carry = all = 0;
+    for (int q = 0; q < kPlanCluster; ++q) {
+      const int64_t v = cluster.map_shared_rank(&part, q)->x;
+      all += v;
+      if (q < rank) carry += v;
+    }
   }
   unsigned long long best = 0;
   for (int64_t j = i0; j < i1; j += kPlanSumThreads) {
@@ -289,6 +381,7 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanSumT
     PlanRequest r{};
     if (i < i1) {
       r = plan_request(a, i);
+      if (falls && r.first < a.high[i]) r.ok = false, r.gets = 0;
       bad |= !r.ok;
     }
     const int64_t upto = carry + plan_scan<kWarps>(r.gets, &total, warp_sum);
@@ -361,25 +454,27 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_tokens(PlanArgs a, int ti
     list.start[count] = plan_relative(a.offsets ? __ldg(a.offsets + i) : i, t0);
   }
   await_previous();
+  const bool falls = __ldcg(a.falls) != 0;  // then the list may lack requests
   for (int k = tid; k < count; k += kPlanThreads) list.base[k] = (int32_t)__ldcg(a.base + first + k);
   __syncthreads();
   whole |= list.start[count] >= t1 - t0 || first + count >= a.n;
-  if (whole) {
+  if (whole && !falls) {
     plan_tokens(a, t0, t1, head, first, count, list);
     return;
   }
+  const int64_t* starts = falls ? a.high : a.offsets;
   for (int64_t t = t0 + tid; t < t1; t += kPlanThreads) {
     int64_t l = 0, h = a.n;
     while (l < h) {
       const int64_t mid = l + ((h - l) >> 1);
-      if (__ldg(a.offsets + mid) <= t) l = mid + 1;
+      if (__ldcg(starts + mid) <= t) l = mid + 1;
       else h = mid;
     }
     int64_t slot = -1, position = 0;
     const int64_t i = l - 1;
     if (i >= 0) {
       const PlanRequest r = plan_request(a, i);
-      if (r.ok && t >= r.first && t < r.first + r.fresh) {
+      if (r.ok && r.first >= __ldcg(starts + i) && t < r.first + r.fresh) {
         position = r.cached + (t - r.first);
         const int64_t base = __ldcg(a.base + i);
         if (base >= 0) {
@@ -432,7 +527,7 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
     PlanArgs a{d_offsets, d_cached, n_requests, n_free, max_blocks, table_stride, n_slots, FastDiv(block_size), d_free,
-               d_head, d_table, d_seq_lens, d_slots, d_positions, d_info, nullptr, h->d_small};
+               d_head, d_table, d_seq_lens, d_slots, d_positions, d_info, nullptr, nullptr, nullptr, h->d_small};
     // tokens of a thread: as few as leave at most two blocks an SM
     const int64_t each = (n_slots + kPlanThreads * 4 * h->n_sms - 1) / (kPlanThreads * 4 * h->n_sms);
     const int tile = 2 * kPlanThreads * (int)std::min<int64_t>(kPlanPairs, std::max<int64_t>(1, each));
@@ -442,9 +537,11 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
       CK(cudaGetLastError());
       return BPE_OK;
     }
-    int rc = ensure_ws(h, (size_t)n_requests * sizeof(int64_t), st);
+    int rc = ensure_ws(h, (2 * (size_t)n_requests + 1) * sizeof(int64_t), st);
     if (rc) return rc;
     a.base = static_cast<int64_t*>(h->d_ws);
+    a.high = a.base + n_requests;
+    a.falls = a.high + n_requests;
     k_plan_requests<<<kPlanCluster, kPlanSumThreads, 0, st>>>(a);
     CK(cudaGetLastError());
     if (tiles) CK(launch_after(k_plan_tokens, dim3(tiles), kPlanThreads, 0, st, a, tile));

@@ -381,11 +381,12 @@ int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int6
  * cached[i]); requests that need no block are always served. That is no
  * error: info[1] is how many blocks more would have served all.
  * Reported (BPE_ERR_BAD_INPUT) and not served: a request whose offsets are
- * not monotone in [0, n_slots], whose cached length is negative, that would
- * pass 2^31 - block_size tokens, or that needs more than max_blocks; a head
- * outside [0, n_free] counts as an empty list.
- * Sizes: n_requests and n_slots < 2^31 - 1, n_free < 2^31. Workspace: 8 bytes a request above
- * 2048 requests.
+ * not monotone in [0, n_slots], that begins below an earlier offset, whose
+ * cached length is negative, that would pass 2^31 - block_size tokens, or that
+ * needs more than max_blocks; a head outside [0, n_free] counts as an empty
+ * list. Tokens of such requests get slot -1 and position 0.
+ * Sizes: n_requests and n_slots < 2^31 - 1, n_free < 2^31. Workspace: 16 bytes
+ * a request above 2048 requests.
  */
 int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_cached, int64_t n_requests,
                     int64_t block_size, const int32_t* d_free, int64_t n_free, const int64_t* d_head,
