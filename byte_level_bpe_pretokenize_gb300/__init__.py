@@ -532,7 +532,8 @@ class Tokenizer:
         """scale * weight[ids] in weight's type, or in ``dtype``: ids int32 of
         any shape, weight [rows, dim] in 32 or 16 bits with any row stride.
         Tokens equal to skip_id get zeros. Differentiable with respect to
-        weight (its gradient runs embed_grad) unless ``out`` is given."""
+        weight, as often as wanted (its gradient runs embed_grad), unless
+        ``out`` is given."""
         torch, types, device = _torch(), _type_codes, self.device
         code = types.get(weight.dtype)
         if code is None or weight.get_device() != device or weight.dim() != 2:
@@ -547,7 +548,7 @@ class Tokenizer:
         out_stride = dim
         if out is None:
             if weight.requires_grad and torch.is_grad_enabled():
-                return _embed_function().apply(self, ids, weight, scale, skip_id, dtype or weight.dtype)
+                return _embed_functions()[0].apply(self, ids, weight, scale, skip_id, dtype or weight.dtype)
             out = torch.empty(shape, dtype=dtype or weight.dtype, device=weight.device)
         else:
             if out.get_device() != device or out.shape != shape:
@@ -575,7 +576,8 @@ class Tokenizer:
                    out=None, accumulate: bool = False):
         """The gradient [n_rows, dim] of embed's weight for the gradient
         ``grad`` [*ids.shape, dim] of its result, in grad's type or in
-        ``dtype``, or written into (accumulate: added to) ``out``."""
+        ``dtype``, or written into (accumulate: added to) ``out``.
+        Differentiable with respect to grad unless ``out`` is given."""
         torch, types, device = _torch(), _type_codes, self.device
         code = types.get(grad.dtype)
         if code is None or grad.get_device() != device:
@@ -589,6 +591,8 @@ class Tokenizer:
         dim = shape[-1]
         if shape[:-1] != ids.shape:
             raise ValueError("grad: needs the shape of ids and one more dimension")
+        if out is None and not accumulate and grad.requires_grad and torch.is_grad_enabled():
+            return _embed_functions()[1].apply(self, ids, grad, n_rows, scale, skip_id, dtype or grad.dtype)
         if len(shape) != 2:
             grad = grad.reshape(n, dim)
         stride, step = grad.stride()
@@ -637,14 +641,15 @@ def _torch():
     return _torch_module
 
 
-def _embed_function():
-    """The autograd function of Tokenizer.embed (made once: torch is imported
-    on first use only)."""
-    global _embed_fn
-    if _embed_fn is None:
+def _embed_functions():
+    """The autograd functions of Tokenizer.embed and Tokenizer.embed_grad (made
+    once: torch is imported on first use only). Both are linear, the one's
+    adjoint is the other, so derivatives of any order are calls of these two."""
+    global _embed_fns
+    if _embed_fns is None:
         import torch
 
-        class EmbedFunction(torch.autograd.Function):
+        class Embed(torch.autograd.Function):
             @staticmethod
             def forward(ctx, tok, ids, weight, scale, skip_id, dtype):
                 ctx.args = (tok, weight.shape[0], scale, skip_id, weight.dtype)
@@ -657,11 +662,24 @@ def _embed_function():
                 (ids,) = ctx.saved_tensors
                 return None, None, tok.embed_grad(ids, grad, n_rows, scale, skip_id, dtype), None, None, None
 
-        _embed_fn = EmbedFunction
-    return _embed_fn
+        class EmbedGrad(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, tok, ids, grad, n_rows, scale, skip_id, dtype):
+                ctx.args = (tok, scale, skip_id, grad.dtype)
+                ctx.save_for_backward(ids)
+                return tok.embed_grad(ids, grad.detach(), n_rows, scale, skip_id, dtype)
+
+            @staticmethod
+            def backward(ctx, grad):
+                tok, scale, skip_id, dtype = ctx.args
+                (ids,) = ctx.saved_tensors
+                return None, None, tok.embed(ids, grad, scale, skip_id, dtype), None, None, None, None
+
+        _embed_fns = Embed, EmbedGrad
+    return _embed_fns
 
 
-_embed_fn = None
+_embed_fns = None
 
 
 def pretokenize(data, offsets):

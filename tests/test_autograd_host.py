@@ -1,0 +1,78 @@
+"""Derivatives through the binding of the operators around the model, on the
+host (the library's calls by numpy): every order against torch's own indexing,
+or an error, never a number that lacks a term. Inputs are small whole numbers,
+so that every value is exact."""
+import pytest
+
+from tests.cpu_ops import tokenizer
+
+ROWS, DIM, SCALE, SKIP = 7, 3, 0.5, 2
+
+
+@pytest.fixture()
+def tok(monkeypatch):
+    return tokenizer(monkeypatch)
+
+
+def inputs(seed=0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, ROWS, (11,), generator=g, dtype=torch.int32)
+    return (ids, torch.randint(-3, 4, (ROWS, DIM), generator=g).float(),
+            torch.randint(-3, 4, (11, DIM), generator=g).float(), torch.randint(-3, 4, (ROWS, DIM), generator=g).float())
+
+
+def plain_embed(ids, weight):
+    import torch
+    return torch.where((ids == SKIP)[:, None], 0.0, weight[ids.long()] * SCALE)
+
+
+def embed(tok, ids, weight):
+    return tok.embed(ids, weight, scale=SCALE, skip_id=SKIP)
+
+
+def tied_loss(x, weight, c):
+    """A loss that is of third order in the table, through the lookup and beside it."""
+    return ((x * x) * c).sum() + (x @ weight.t()).pow(2).sum() + weight.pow(3).sum()
+
+
+@pytest.mark.parametrize("tied", [False, True])
+def test_second_and_third_derivatives(tok, tied):
+    import torch
+    ids, w0, c, v = inputs()
+    results = []
+    for look in (lambda w: embed(tok, ids, w), lambda w: plain_embed(ids, w)):
+        w = w0.clone().requires_grad_()
+        x = look(w)
+        loss = tied_loss(x, w, c) if tied else (x.pow(4) * c).sum()
+        (first,) = torch.autograd.grad(loss, w, create_graph=True)
+        (second,) = torch.autograd.grad((first * v).sum(), w, create_graph=True)  # the Hessian's product with v
+        (third,) = torch.autograd.grad((second * v).sum(), w)
+        results.append((x.detach(), first.detach(), second.detach(), third))
+    for name, got, want in zip(("value", "first", "second", "third"), *results):
+        assert torch.equal(got, want), name
+    assert tok._lib.calls.count("embed") >= 2 and tok._lib.calls.count("embed_grad") >= 2
+
+
+def test_gradient_penalty(tok):
+    """A penalty on the upstream gradient's image: a loss of embed_grad's result alone."""
+    import torch
+    ids, w0, c, _ = inputs(1)
+    results = []
+    for look in (lambda w: embed(tok, ids, w), lambda w: plain_embed(ids, w)):
+        w, u = w0.clone().requires_grad_(), c.clone().requires_grad_()
+        (first,) = torch.autograd.grad((look(w) * u * u).sum(), w, create_graph=True)
+        results.append(torch.autograd.grad(first.pow(2).sum(), u)[0])
+    assert torch.equal(*results)
+
+
+def test_embed_grad_is_differentiable(tok):
+    import torch
+    ids, _, c, v = inputs(2)
+    g = c.clone().requires_grad_()
+    out = tok.embed_grad(ids, g, ROWS, scale=SCALE, skip_id=SKIP)
+    (back,) = torch.autograd.grad((out * v).sum(), g)
+    assert torch.equal(back, plain_embed(ids, v))
+    with torch.no_grad():
+        assert not tok.embed_grad(ids, g, ROWS).requires_grad
+    assert not tok.embed_grad(ids, g, ROWS, out=torch.zeros(ROWS, DIM)).requires_grad
