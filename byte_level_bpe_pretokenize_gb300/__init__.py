@@ -532,8 +532,8 @@ class Tokenizer:
         """scale * weight[ids] in weight's type, or in ``dtype``: ids int32 of
         any shape, weight [rows, dim] in 32 or 16 bits with any row stride.
         Tokens equal to skip_id get zeros. Differentiable with respect to
-        weight, as often as wanted (its gradient runs embed_grad), unless
-        ``out`` is given."""
+        weight in backward and forward mode, as often as wanted (its gradient
+        runs embed_grad), unless ``out`` is given."""
         torch, types, device = _torch(), _type_codes, self.device
         code = types.get(weight.dtype)
         if code is None or weight.get_device() != device or weight.dim() != 2:
@@ -547,7 +547,7 @@ class Tokenizer:
         shape = (*ids.shape, dim)
         out_stride = dim
         if out is None:
-            if weight.requires_grad and torch.is_grad_enabled():
+            if weight.requires_grad and torch.is_grad_enabled() or _unpack_dual(weight).tangent is not None:
                 return _embed_functions()[0].apply(self, ids, weight, scale, skip_id, dtype or weight.dtype)
             out = torch.empty(shape, dtype=dtype or weight.dtype, device=weight.device)
         else:
@@ -591,7 +591,8 @@ class Tokenizer:
         dim = shape[-1]
         if shape[:-1] != ids.shape:
             raise ValueError("grad: needs the shape of ids and one more dimension")
-        if out is None and not accumulate and grad.requires_grad and torch.is_grad_enabled():
+        if out is None and not accumulate and (grad.requires_grad and torch.is_grad_enabled()
+                                               or _unpack_dual(grad).tangent is not None):
             return _embed_functions()[1].apply(self, ids, grad, n_rows, scale, skip_id, dtype or grad.dtype)
         if len(shape) != 2:
             grad = grad.reshape(n, dim)
@@ -626,16 +627,17 @@ class Tokenizer:
 _pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
 _type_codes = {}  # torch dtype -> BPE_* code
-_torch_module = _int32 = _int64 = _float32 = _raw_stream = None
+_torch_module = _int32 = _int64 = _float32 = _raw_stream = _unpack_dual = None
 
 
 def _torch():
     """torch, imported on first use, with what the calls above take from it."""
-    global _torch_module, _int32, _int64, _float32, _raw_stream
+    global _torch_module, _int32, _int64, _float32, _raw_stream, _unpack_dual
     if _torch_module is None:
         import torch
         _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
         _raw_stream = torch._C._cuda_getCurrentRawStream
+        _unpack_dual = torch.autograd.forward_ad.unpack_dual
         _type_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         _torch_module = torch
     return _torch_module
@@ -644,7 +646,8 @@ def _torch():
 def _embed_functions():
     """The autograd functions of Tokenizer.embed and Tokenizer.embed_grad (made
     once: torch is imported on first use only). Both are linear, the one's
-    adjoint is the other, so derivatives of any order are calls of these two."""
+    adjoint is the other, so derivatives of any order, backward and forward, are
+    calls of these two."""
     global _embed_fns
     if _embed_fns is None:
         import torch
@@ -652,28 +655,42 @@ def _embed_functions():
         class Embed(torch.autograd.Function):
             @staticmethod
             def forward(ctx, tok, ids, weight, scale, skip_id, dtype):
-                ctx.args = (tok, weight.shape[0], scale, skip_id, weight.dtype)
+                ctx.args = (tok, weight.shape[0], scale, skip_id, weight.dtype, dtype)
                 ctx.save_for_backward(ids)
+                ctx.save_for_forward(ids)
                 return tok.embed(ids, weight.detach(), scale, skip_id, dtype)
 
             @staticmethod
             def backward(ctx, grad):
-                tok, n_rows, scale, skip_id, dtype = ctx.args
+                tok, n_rows, scale, skip_id, dtype, _ = ctx.args
                 (ids,) = ctx.saved_tensors
                 return None, None, tok.embed_grad(ids, grad, n_rows, scale, skip_id, dtype), None, None, None
+
+            @staticmethod
+            def jvp(ctx, _tok, _ids, weight, *_):
+                tok, _, scale, skip_id, _, dtype = ctx.args
+                (ids,) = ctx.saved_tensors
+                return tok.embed(ids, weight, scale, skip_id, dtype)
 
         class EmbedGrad(torch.autograd.Function):
             @staticmethod
             def forward(ctx, tok, ids, grad, n_rows, scale, skip_id, dtype):
-                ctx.args = (tok, scale, skip_id, grad.dtype)
+                ctx.args = (tok, n_rows, scale, skip_id, grad.dtype, dtype)
                 ctx.save_for_backward(ids)
+                ctx.save_for_forward(ids)
                 return tok.embed_grad(ids, grad.detach(), n_rows, scale, skip_id, dtype)
 
             @staticmethod
             def backward(ctx, grad):
-                tok, scale, skip_id, dtype = ctx.args
+                tok, _, scale, skip_id, dtype, _ = ctx.args
                 (ids,) = ctx.saved_tensors
                 return None, None, tok.embed(ids, grad, scale, skip_id, dtype), None, None, None, None
+
+            @staticmethod
+            def jvp(ctx, _tok, _ids, grad, *_):
+                tok, n_rows, scale, skip_id, _, dtype = ctx.args
+                (ids,) = ctx.saved_tensors
+                return tok.embed_grad(ids, grad, n_rows, scale, skip_id, dtype)
 
         _embed_fns = Embed, EmbedGrad
     return _embed_fns

@@ -76,3 +76,32 @@ def test_embed_grad_is_differentiable(tok):
     with torch.no_grad():
         assert not tok.embed_grad(ids, g, ROWS).requires_grad
     assert not tok.embed_grad(ids, g, ROWS, out=torch.zeros(ROWS, DIM)).requires_grad
+
+
+def test_forward_mode(tok):
+    import torch
+    from torch.autograd import forward_ad
+    ids, w, c, v = inputs(3)
+    with forward_ad.dual_level(), torch.no_grad():
+        value, tangent = forward_ad.unpack_dual(embed(tok, ids, forward_ad.make_dual(w, v)))
+        assert torch.equal(value, plain_embed(ids, w)) and torch.equal(tangent, plain_embed(ids, v))
+        g = forward_ad.make_dual(c, c * c)
+        value, tangent = forward_ad.unpack_dual(tok.embed_grad(ids, g, ROWS, scale=SCALE))
+        assert torch.equal(value, tok.embed_grad(ids, c, ROWS, scale=SCALE))
+        assert torch.equal(tangent, tok.embed_grad(ids, c * c, ROWS, scale=SCALE))
+    with forward_ad.dual_level():
+        assert forward_ad.unpack_dual(embed(tok, ids, w)).tangent is None  # not a dual tensor
+
+
+def test_forward_over_reverse(tok):
+    import torch
+    from torch.autograd import forward_ad
+    ids, w0, c, v = inputs(4)
+    results = []
+    for look in (lambda w: embed(tok, ids, w), lambda w: plain_embed(ids, w)):
+        with forward_ad.dual_level():
+            w = forward_ad.make_dual(w0.clone().requires_grad_(), v)
+            (first,) = torch.autograd.grad(tied_loss(look(w), w, c), w, create_graph=True)
+            value, tangent = forward_ad.unpack_dual(first)
+            results.append((value.detach(), tangent.detach()))
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])

@@ -46,3 +46,14 @@ def test_embed_grad_is_differentiable(tok):
     out = tok.embed_grad(ids, g, 30, scale=2.0, dtype=torch.float32)
     (back,) = torch.autograd.grad((out * w).sum(), g)
     assert back.dtype is torch.bfloat16 and torch.equal(back, (w[ids.long()] * 2).to(torch.bfloat16))
+
+
+def test_forward_mode(tok):
+    import torch
+    from torch.autograd import forward_ad
+    ids, w, c, v = inputs(700, 50, 8)
+    with forward_ad.dual_level():
+        value, tangent = forward_ad.unpack_dual(tok.embed(ids, forward_ad.make_dual(w, v), scale=0.5))
+        assert torch.equal(value, w[ids.long()] * 0.5) and torch.equal(tangent, v[ids.long()] * 0.5)
+        _, tangent = forward_ad.unpack_dual(tok.embed_grad(ids, forward_ad.make_dual(c, c * c), 50))
+    assert torch.equal(tangent, torch.zeros_like(w).index_add_(0, ids.long(), c * c))
