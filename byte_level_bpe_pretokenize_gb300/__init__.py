@@ -460,9 +460,19 @@ class Tokenizer:
         repetition, frequency, presence: float32[n]; bias: (ids int32[m],
         values float32[m], offsets int64[n + 1]); mask: int32 or uint32
         [masks, ceil(vocab / 32)], bit v % 32 of word v / 32 set for an
-        allowed token; mask_rows: int32[n], each row's mask or -1."""
+        allowed token; mask_rows: int32[n], each row's mask or -1. Has no
+        derivative: a backward pass through its result raises, and ``out`` is
+        refused for inputs that torch records derivatives of."""
         torch, types, flat = _torch(), _type_codes, self._flat
         i32, i64, f32 = _int32, _int64, _float32
+        if _tracked(logits, repetition, frequency, presence, None if bias is None else bias[1]):
+            if out is not None:
+                raise ValueError("out: adjust_logits has no derivative, so it needs inputs without one "
+                                 "(torch.no_grad or detach)")
+            return _functions()[2].apply(
+                lambda: self.adjust_logits(logits, prompt, output, repetition, frequency, presence, bias, mask,
+                                           mask_rows, dtype), logits, repetition, frequency, presence,
+                None if bias is None else bias[1])
         code = types.get(logits.dtype)
         if code is None or logits.get_device() != self.device or logits.dim() != 2:
             self._refuse("logits", logits, types, dims=2)
@@ -547,8 +557,8 @@ class Tokenizer:
         shape = (*ids.shape, dim)
         out_stride = dim
         if out is None:
-            if weight.requires_grad and torch.is_grad_enabled() or _unpack_dual(weight).tangent is not None:
-                return _embed_functions()[0].apply(self, ids, weight, scale, skip_id, dtype or weight.dtype)
+            if _tracked(weight):
+                return _functions()[0].apply(self, ids, weight, scale, skip_id, dtype or weight.dtype)
             out = torch.empty(shape, dtype=dtype or weight.dtype, device=weight.device)
         else:
             if out.get_device() != device or out.shape != shape:
@@ -591,9 +601,8 @@ class Tokenizer:
         dim = shape[-1]
         if shape[:-1] != ids.shape:
             raise ValueError("grad: needs the shape of ids and one more dimension")
-        if out is None and not accumulate and (grad.requires_grad and torch.is_grad_enabled()
-                                               or _unpack_dual(grad).tangent is not None):
-            return _embed_functions()[1].apply(self, ids, grad, n_rows, scale, skip_id, dtype or grad.dtype)
+        if out is None and not accumulate and _tracked(grad):
+            return _functions()[1].apply(self, ids, grad, n_rows, scale, skip_id, dtype or grad.dtype)
         if len(shape) != 2:
             grad = grad.reshape(n, dim)
         stride, step = grad.stride()
@@ -627,29 +636,44 @@ class Tokenizer:
 _pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
 _type_codes = {}  # torch dtype -> BPE_* code
-_torch_module = _int32 = _int64 = _float32 = _raw_stream = _unpack_dual = None
+_torch_module = _int32 = _int64 = _float32 = _raw_stream = _forward_ad = None
 
 
 def _torch():
     """torch, imported on first use, with what the calls above take from it."""
-    global _torch_module, _int32, _int64, _float32, _raw_stream, _unpack_dual
+    global _torch_module, _int32, _int64, _float32, _raw_stream, _forward_ad
     if _torch_module is None:
         import torch
         _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
         _raw_stream = torch._C._cuda_getCurrentRawStream
-        _unpack_dual = torch.autograd.forward_ad.unpack_dual
+        _forward_ad = torch.autograd.forward_ad
         _type_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         _torch_module = torch
     return _torch_module
 
 
-def _embed_functions():
-    """The autograd functions of Tokenizer.embed and Tokenizer.embed_grad (made
-    once: torch is imported on first use only). Both are linear, the one's
-    adjoint is the other, so derivatives of any order, backward and forward, are
-    calls of these two."""
-    global _embed_fns
-    if _embed_fns is None:
+def _tracked(*tensors):
+    """Whether torch records derivatives, backward or forward, of one of the
+    tensors (or Nones)."""
+    if _torch_module.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    if _forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                return True
+    return False
+
+
+def _functions():
+    """The autograd functions of Tokenizer.embed, embed_grad and adjust_logits
+    (made once: torch is imported on first use only). The first two are linear
+    and each other's adjoint, so their derivatives of any order, backward and
+    forward, are calls of the two. The last has none, and says so when one is
+    asked for."""
+    global _function_list
+    if _function_list is None:
         import torch
 
         class Embed(torch.autograd.Function):
@@ -692,11 +716,24 @@ def _embed_functions():
                 (ids,) = ctx.saved_tensors
                 return tok.embed_grad(ids, grad, n_rows, scale, skip_id, dtype)
 
-        _embed_fns = Embed, EmbedGrad
-    return _embed_fns
+        class AdjustLogits(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, call, *inputs):
+                return call()
+
+            @staticmethod
+            def backward(ctx, grad):
+                raise RuntimeError("adjust_logits has no gradient")
+
+            @staticmethod
+            def jvp(ctx, *tangents):
+                raise RuntimeError("adjust_logits has no derivative")
+
+        _function_list = Embed, EmbedGrad, AdjustLogits
+    return _function_list
 
 
-_embed_fns = None
+_function_list = None
 
 
 def pretokenize(data, offsets):

@@ -105,3 +105,28 @@ def test_forward_over_reverse(tok):
             value, tangent = forward_ad.unpack_dual(first)
             results.append((value.detach(), tangent.detach()))
     assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+def test_adjust_logits_is_not_cut_off_silently(tok):
+    import torch
+    from torch.autograd import forward_ad
+    x = torch.ones(2, 5)
+    f = torch.ones(2)
+    bias = (torch.zeros(1, dtype=torch.int32), torch.ones(1), torch.tensor([0, 1, 1]))
+    cases = [(x.clone().requires_grad_(), {})]
+    cases += [(x, {name: f.clone().requires_grad_()}) for name in ("repetition", "frequency", "presence")]
+    cases += [(x, {"bias": (bias[0], bias[1].clone().requires_grad_(), bias[2])})]
+    for logits, more in cases:
+        got = tok.adjust_logits(logits, **more)
+        assert torch.equal(got, x * 0.5)  # the value is there, to sample from
+        with pytest.raises(RuntimeError, match="no gradient"):
+            got.sum().backward()
+        with pytest.raises(ValueError, match="derivative"):
+            tok.adjust_logits(logits, out=torch.zeros(2, 5), **more)
+        with torch.no_grad():
+            assert not tok.adjust_logits(logits, **more).requires_grad
+            tok.adjust_logits(logits.detach().clone(), out=torch.zeros(2, 5), **more)
+    with forward_ad.dual_level():
+        with pytest.raises(RuntimeError):
+            tok.adjust_logits(forward_ad.make_dual(x, x))
+    assert not tok.adjust_logits(x, repetition=f, bias=bias).requires_grad

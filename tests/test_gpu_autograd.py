@@ -57,3 +57,19 @@ def test_forward_mode(tok):
         assert torch.equal(value, w[ids.long()] * 0.5) and torch.equal(tangent, v[ids.long()] * 0.5)
         _, tangent = forward_ad.unpack_dual(tok.embed_grad(ids, forward_ad.make_dual(c, c * c), 50))
     assert torch.equal(tangent, torch.zeros_like(w).index_add_(0, ids.long(), c * c))
+
+
+def test_adjust_logits_raises_where_a_gradient_is_asked_for(tok):
+    import torch
+    x = torch.randn(3, 900, device="cuda").requires_grad_()
+    ids, off = torch.arange(6, dtype=torch.int32, device="cuda"), torch.tensor([0, 2, 4, 6], device="cuda")
+    rep = torch.full((3,), 1.5, device="cuda")
+    got = tok.adjust_logits(x, prompt=(ids, off), repetition=rep)
+    assert torch.equal(got, tok.adjust_logits(x.detach(), prompt=(ids, off), repetition=rep))
+    with pytest.raises(RuntimeError, match="no gradient"):
+        got.logsumexp(1).sum().backward()
+    with pytest.raises(ValueError):
+        tok.adjust_logits(x, prompt=(ids, off), repetition=rep, out=torch.empty_like(x))
+    with torch.no_grad():
+        y = tok.adjust_logits(x, prompt=(ids, off), repetition=rep, out=torch.empty_like(x))
+    assert torch.equal(y, got)
