@@ -363,10 +363,22 @@ class Tokenizer:
         import torch
         return torch.cuda.current_stream().cuda_stream
 
+    @staticmethod
+    def _writes(*tensors):
+        """Tells autograd that the library writes into the caller's tensors,
+        which it cannot see: a graph that has saved one of them (embed saves its
+        ids) refuses its backward pass from then on."""
+        _torch()
+        for t in tensors:
+            if t.requires_grad and _torch_module.is_grad_enabled():
+                raise ValueError("out: must not require a gradient")
+            _increment_version(t)
+
     def encode_into(self, data, offsets, out_ids, out_offsets, want_total: bool = True):
         """data uint8[N], offsets int64[D + 1] -> ids written into out_ids
         (int32, capacity >= N) and out_offsets (int64[D + 1]). Returns the
         token count when want_total (that waits for the stream)."""
+        self._writes(out_ids, out_offsets)
         return bpe_encode_batch(self.handle, data.data_ptr(), data.numel(), offsets.data_ptr(), offsets.numel() - 1,
                                 out_ids.data_ptr(), out_ids.numel(), out_offsets.data_ptr(), want_total,
                                 self._stream())
@@ -438,6 +450,7 @@ class Tokenizer:
         p_cached = None if cached is None else flat("cached", cached, i32, n)
         p_free = flat("free", free, i32, n_free)
         p_head = None if head is None else flat("head", head, i64, 1)
+        self._writes(table)
         empty, dev = torch.empty, table.device
         seq_lens = empty(n, dtype=i32, device=dev)
         slots = empty(n_slots, dtype=i64, device=dev)
@@ -492,6 +505,7 @@ class Tokenizer:
             out_stride, step = out.stride()
             if out.shape != logits.shape or (step != 1 and vocab > 1):
                 raise ValueError("out: needs the shape of logits, the elements of a row adjacent")
+            self._writes(out)
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)
@@ -569,6 +583,7 @@ class Tokenizer:
                     raise ValueError("out: the elements of a row must be adjacent")
             elif not out.is_contiguous():
                 raise ValueError("out: needs to be contiguous where ids is not one-dimensional")
+            self._writes(out)
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)
@@ -620,6 +635,7 @@ class Tokenizer:
             out_stride, step = out.stride()
             if out.shape != (n_rows, dim) or (step != 1 and dim > 1):
                 raise ValueError("out: needs n_rows rows of grad's columns, the elements of a row adjacent")
+            self._writes(out)
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)
@@ -636,17 +652,18 @@ class Tokenizer:
 _pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
 _type_codes = {}  # torch dtype -> BPE_* code
-_torch_module = _int32 = _int64 = _float32 = _raw_stream = _forward_ad = None
+_torch_module = _int32 = _int64 = _float32 = _raw_stream = _forward_ad = _increment_version = None
 
 
 def _torch():
     """torch, imported on first use, with what the calls above take from it."""
-    global _torch_module, _int32, _int64, _float32, _raw_stream, _forward_ad
+    global _torch_module, _int32, _int64, _float32, _raw_stream, _forward_ad, _increment_version
     if _torch_module is None:
         import torch
         _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _forward_ad = torch.autograd.forward_ad
+        _increment_version = torch.autograd.graph.increment_version
         _type_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         _torch_module = torch
     return _torch_module

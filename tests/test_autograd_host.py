@@ -130,3 +130,58 @@ def test_adjust_logits_is_not_cut_off_silently(tok):
         with pytest.raises(RuntimeError):
             tok.adjust_logits(forward_ad.make_dual(x, x))
     assert not tok.adjust_logits(x, repetition=f, bias=bias).requires_grad
+
+
+def test_what_is_written_counts_as_written(tok, monkeypatch):
+    """A backward pass through a tensor that a call has since overwritten raises, as torch's own writes make it."""
+    import torch
+
+    import byte_level_bpe_pretokenize_gb300 as bpe
+    ids, w0, c, _ = inputs(5)
+    i32 = dict(dtype=torch.int32)
+    monkeypatch.setattr(bpe, "bpe_encode_batch", lambda *a: None)
+    monkeypatch.setattr(bpe.Tokenizer, "_stream", staticmethod(lambda: 0))
+    tok._lib.bpe_plan_blocks = lambda *a: 0
+    table = torch.zeros(2, 3, **i32)
+
+    logits = torch.ones(2, 4)
+    rows, grad = torch.zeros(11, DIM), torch.zeros(ROWS, DIM)
+    for saved, write in ((logits, lambda: tok.adjust_logits(logits, out=logits)),
+                         (rows, lambda: tok.embed(ids, w0, out=rows)),
+                         (grad, lambda: tok.embed_grad(ids, c, ROWS, out=grad)),
+                         (grad, lambda: tok.embed_grad(ids, c, ROWS, out=grad, accumulate=True))):
+        one = torch.ones_like(saved).requires_grad_()
+        loss = (saved * one).sum()  # saves what is written below
+        with torch.no_grad():
+            write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    # the next batch's ids in the buffer of this one's
+    w = w0.clone().requires_grad_()
+    loss = embed(tok, ids, w).sum()
+    tok.encode_into(torch.zeros(3, dtype=torch.uint8), torch.zeros(2, dtype=torch.int64), ids,
+                    torch.zeros(2, dtype=torch.int64), False)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    before = table._version
+    tok.plan_blocks(None, None, table, torch.zeros(4, **i32), 16)
+    assert table._version > before
+
+
+def test_out_must_not_require_a_gradient(tok):
+    import torch
+    ids, w, c, _ = inputs(6)
+    hidden = torch.zeros(11, DIM).requires_grad_() * 1
+    with pytest.raises(ValueError, match="require a gradient"):
+        tok.embed(ids, w, out=hidden)
+    with pytest.raises(ValueError, match="require a gradient"):
+        tok.embed_grad(ids, c, ROWS, out=torch.zeros(ROWS, DIM).requires_grad_())
+    with pytest.raises(ValueError, match="require a gradient"):
+        tok.adjust_logits(c, out=hidden)
+    table = torch.zeros(ROWS, DIM).requires_grad_()
+    with torch.no_grad():  # an update by hand
+        tok.embed_grad(ids, c, ROWS, out=table)
+    assert torch.equal(table, tok.embed_grad(ids, c, ROWS))
+    with torch.inference_mode():
+        tok.embed(ids, w, out=torch.zeros(11, DIM))
+        tok.adjust_logits(c, out=hidden.detach())
