@@ -473,8 +473,9 @@ class Tokenizer:
         repetition, frequency, presence: float32[n]; bias: (ids int32[m],
         values float32[m], offsets int64[n + 1]); mask: int32 or uint32
         [masks, ceil(vocab / 32)], bit v % 32 of word v / 32 set for an
-        allowed token; mask_rows: int32[n], each row's mask or -1. Has no
-        derivative: a backward pass through its result raises, and ``out`` is
+        allowed token; mask_rows: int32[n], each row's mask or -1, needs mask
+        (which may have no rows where all are -1). An empty list of prompt,
+        output or bias ids counts as left out. Has no derivative: a backward pass through its result raises, and ``out`` is
         refused for inputs that torch records derivatives of."""
         torch, types, flat = _torch(), _type_codes, self._flat
         i32, i64, f32 = _int32, _int64, _float32
@@ -543,6 +544,13 @@ class Tokenizer:
             p_mask = mask.data_ptr()
             if mask_rows is not None:
                 p_rows = flat("mask rows", mask_rows, i32, n)
+            if not n_masks and n:
+                # torch gives an empty tensor no address, and without one the call would take every token as allowed
+                if mask_rows is None:
+                    raise BpeError(1, "adjust_logits: fewer masks than rows, and no mask_rows")
+                p_mask = p_rows
+        elif mask_rows is not None:
+            raise ValueError("mask_rows: there is no mask")
         rc = self._lib.bpe_adjust_logits(
             self.handle,
             _pack_logits(logits.data_ptr(), out.data_ptr(), code, out_code, stride, out_stride, n, vocab, p_ids, p_off,

@@ -1,0 +1,36 @@
+"""What the binding of the operators around the model refuses or hands to the
+library, on the host (see cpu_ops)."""
+import pytest
+
+from tests.cpu_ops import tokenizer
+
+
+@pytest.fixture()
+def tok(monkeypatch):
+    return tokenizer(monkeypatch)
+
+
+@pytest.fixture(scope="module")
+def bpe():
+    import byte_level_bpe_pretokenize_gb300 as m
+    return m
+
+
+def test_masks_without_rows(bpe, tok):
+    """An empty table of masks has no address; it must not pass for no mask at all."""
+    import torch
+    x, none = torch.ones(2, 40), torch.zeros(0, 2, dtype=torch.int32)
+    with pytest.raises(bpe.BpeError, match="fewer masks than rows") as e:
+        tok.adjust_logits(x, mask=none)
+    assert e.value.code == 1 and not tok._lib.calls
+    rows = torch.tensor([-1, 0], dtype=torch.int32)
+    tok.adjust_logits(x, mask=none, mask_rows=rows)
+    args = tok._lib.logits_args
+    assert args.mask and args.n_masks == 0 and args.mask_rows == rows.data_ptr()
+    assert tok.adjust_logits(torch.ones(0, 40), mask=none).shape == (0, 40)
+
+
+def test_mask_rows_need_masks(tok):
+    import torch
+    with pytest.raises(ValueError, match="no mask"):
+        tok.adjust_logits(torch.ones(2, 40), mask_rows=torch.zeros(2, dtype=torch.int32))
