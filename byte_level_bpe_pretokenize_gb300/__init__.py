@@ -507,6 +507,8 @@ class Tokenizer:
             if out.shape != logits.shape or (step != 1 and vocab > 1):
                 raise ValueError("out: needs the shape of logits, the elements of a row adjacent")
             self._writes(out)
+            if dtype is not None and dtype is not out.dtype:
+                raise ValueError(f"out: {out.dtype}, but dtype is {dtype}")
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)
@@ -592,6 +594,8 @@ class Tokenizer:
             elif not out.is_contiguous():
                 raise ValueError("out: needs to be contiguous where ids is not one-dimensional")
             self._writes(out)
+            if dtype is not None and dtype is not out.dtype:
+                raise ValueError(f"out: {out.dtype}, but dtype is {dtype}")
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)
@@ -644,6 +648,8 @@ class Tokenizer:
             if out.shape != (n_rows, dim) or (step != 1 and dim > 1):
                 raise ValueError("out: needs n_rows rows of grad's columns, the elements of a row adjacent")
             self._writes(out)
+            if dtype is not None and dtype is not out.dtype:
+                raise ValueError(f"out: {out.dtype}, but dtype is {dtype}")
         out_code = types.get(out.dtype)
         if out_code is None:
             self._refuse("out", out, types)

@@ -34,3 +34,16 @@ def test_mask_rows_need_masks(tok):
     import torch
     with pytest.raises(ValueError, match="no mask"):
         tok.adjust_logits(torch.ones(2, 40), mask_rows=torch.zeros(2, dtype=torch.int32))
+
+
+def test_dtype_and_out_must_agree(tok):
+    import torch
+    ids, w, x = torch.zeros(3, dtype=torch.int32), torch.ones(5, 4), torch.ones(3, 4)
+    for call, out in ((lambda **k: tok.embed(ids, w, **k), torch.zeros(3, 4)),
+                      (lambda **k: tok.embed_grad(ids, x, 5, **k), torch.zeros(5, 4)),
+                      (lambda **k: tok.adjust_logits(x, **k), torch.zeros(3, 4))):
+        with pytest.raises(ValueError, match="dtype"):
+            call(out=out, dtype=torch.bfloat16)
+        assert not tok._lib.calls
+        assert call(out=out, dtype=torch.float32) is out and len(tok._lib.calls) == 1
+        tok._lib.calls.clear()
