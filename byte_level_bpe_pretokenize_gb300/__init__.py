@@ -603,8 +603,7 @@ class Tokenizer:
             weight = weight.contiguous()
             stride = dim
         rc = self._lib.bpe_embed(self.handle, ids.data_ptr(), ids.numel(), weight.data_ptr(), code, n_rows, dim, stride,
-                                 scale, NO_ID if skip_id is None else skip_id, out.data_ptr(), out_code, out_stride,
-                                 _raw_stream(device))
+                                 scale, _skip(skip_id), out.data_ptr(), out_code, out_stride, _raw_stream(device))
         if rc:
             _check(rc)
         return out
@@ -654,11 +653,20 @@ class Tokenizer:
         if out_code is None:
             self._refuse("out", out, types)
         rc = self._lib.bpe_embed_grad(self.handle, ids.data_ptr(), n, grad.data_ptr(), code, stride, scale,
-                                      NO_ID if skip_id is None else skip_id, n_rows, dim, out.data_ptr(), out_code,
+                                      _skip(skip_id), n_rows, dim, out.data_ptr(), out_code,
                                       out_stride, accumulate, _raw_stream(device))
         if rc:
             _check(rc)
         return out
+
+
+def _skip(skip_id):
+    """skip_id for the library, in 32 bits: ctypes would cut what is longer, and skip another id."""
+    if skip_id is None:
+        return NO_ID
+    if not -2 ** 31 <= skip_id < 2 ** 31:
+        raise ValueError(f"skip_id: {skip_id} is no int32")
+    return skip_id
 
 
 # bpe_logits_args in native layout, for Tokenizer.adjust_logits: one pack takes
@@ -666,6 +674,7 @@ class Tokenizer:
 _pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
 _type_codes = {}  # torch dtype -> BPE_* code
+
 _torch_module = _int32 = _int64 = _float32 = _raw_stream = _forward_ad = _increment_version = None
 
 

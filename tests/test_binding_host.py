@@ -47,3 +47,15 @@ def test_dtype_and_out_must_agree(tok):
         assert not tok._lib.calls
         assert call(out=out, dtype=torch.float32) is out and len(tok._lib.calls) == 1
         tok._lib.calls.clear()
+
+
+def test_skip_id_is_not_cut_to_32_bits(tok):
+    import torch
+    ids, w, x = torch.tensor([1, 2, 3], dtype=torch.int32), torch.ones(5, 4), torch.ones(3, 4)
+    for skip in (2 ** 32 + 2, 2 ** 31, -2 ** 31 - 1, -2 ** 32 + 2):
+        with pytest.raises(ValueError, match="skip_id"):
+            tok.embed(ids, w, skip_id=skip)
+        with pytest.raises(ValueError, match="skip_id"):
+            tok.embed_grad(ids, x, 5, skip_id=skip)
+    assert tok.embed(ids, w, skip_id=2).sum(1).tolist() == [4, 0, 4]
+    assert tok.embed(ids, w, skip_id=-2 ** 31).sum(1).tolist() == tok.embed(ids, w).sum(1).tolist() == [4, 4, 4]
