@@ -81,8 +81,9 @@ __device__ __forceinline__ int64_t plan_head(const PlanArgs& a, bool* bad) {
   return *bad ? a.n_free : head;
 }
 
-// Inclusive sum over a block of kWarps warps, and the block's total.
-template <int kWarps>
+// Inclusive sum over a block of kWarps warps, and the block's total. kFirst: no
+// thread can still be reading warp_sum.
+template <int kWarps, bool kFirst = false>
 __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* total, int64_t* warp_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -90,7 +91,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* total, int64_t*
     const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
     if (lane >= d) x += o;
   }
-  __syncthreads();  // warp_sum may still be read from the last call
+  if (!kFirst) __syncthreads();  // warp_sum may still be read from the last call
   if (lane == 31) warp_sum[warp] = x;
   __syncthreads();
   int64_t w = lane < kWarps ? warp_sum[lane] : 0;
@@ -224,6 +225,27 @@ __device__ __forceinline__ void plan_tokens(const PlanArgs& a, int64_t t0, int64
   }
 }
 
+// Takes the requests that begin below an earlier offset out of a list of all n,
+// `per` a thread: their cached becomes -1 - cached. All starts become the
+// largest offset so far. seq_lens may be null.
+__device__ __noinline__ void plan_refuse(const int64_t* offsets, int32_t* seq_lens, int n, int per, int64_t t0,
+                                         PlanList& list, int64_t* warp_most) {
+  const int i0 = min((int)threadIdx.x * per, n), i1 = min(i0 + per, n);
+  int64_t high = INT64_MIN, most;
+  for (int i = i0; i < i1; ++i) high = max(high, __ldg(offsets + i));
+  high = plan_highest_before<kPlanThreads / 32>(high, &most, warp_most);
+  for (int i = i0; i < i1; ++i) {
+    const int64_t first = __ldg(offsets + i);
+    high = max(high, first);
+    list.start[i] = plan_relative(high, t0);
+    if (first >= high) continue;
+    if (list.cached[i] >= 0) list.cached[i] = -1 - list.cached[i];
+    if (seq_lens) seq_lens[i] = -1 - list.cached[i];
+  }
+  if (threadIdx.x == 0) list.start[n] = plan_relative(max(most, __ldg(offsets + n)), t0);
+  __syncthreads();  // warp_most is read
+}
+
 // Up to kPlanList requests: every block adds up all requests' blocks itself,
 // which takes less time than a launch, and plans its tile of tokens from the
 // list that it then has. Latency: 3.0 us for 8 single tokens, 3.8 us for 500
@@ -260,28 +282,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_one(PlanArgs a, int tile)
   }
   if (tid == 0) list.start[n] = plan_relative(a.offsets ? __ldg(a.offsets + n) : a.n, t0);
   if (__syncthreads_or(falls)) {
-    int64_t high = INT64_MIN, most;
-    for (int i = tid * per; i < min(tid * per + per, n); ++i) high = max(high, __ldg(a.offsets + i));
-    high = plan_highest_before<kPlanThreads / 32>(high, &most, warp_sum);
-    mine = 0;
+    plan_refuse(a.offsets, lead ? a.seq_lens : nullptr, n, per, t0, list, warp_sum);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      const int i = tid * per + q;
-      if (q >= per || i >= n) break;
-      const int64_t first = __ldg(a.offsets + i);
-      high = max(high, first);
-      list.start[i] = plan_relative(high, t0);
-      if (first < high) {
-        gets[q] = 0;
-        if (list.cached[i] >= 0) list.cached[i] = -1 - list.cached[i];
-        if (lead) a.seq_lens[i] = -1 - list.cached[i];
-      }
-      mine += gets[q];
+      if (q >= per || tid * per + q >= n || list.cached[tid * per + q] >= 0) continue;
+      mine -= gets[q];
+      gets[q] = 0;
     }
-    if (tid == 0) list.start[n] = plan_relative(max(most, __ldg(a.offsets + n)), t0);
   }
   int64_t total;
-  int64_t upto = plan_scan<kPlanThreads / 32>(mine, &total, warp_sum) - mine;
+  int64_t upto = plan_scan<kPlanThreads / 32, true>(mine, &total, warp_sum) - mine;
   unsigned long long best = 0;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
@@ -329,8 +339,8 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanSumT
     mine += r.gets;
     falls |= r.falls;
   }
-  plan_scan<kWarps>(mine, &total, warp_sum);
   const int any = __syncthreads_or(falls);
+  plan_scan<kWarps, true>(mine, &total, warp_sum);
   if (tid == 0) {
     part = make_longlong2(total, any);
     taken = 0;
@@ -528,7 +538,8 @@ int bpe_plan_blocks(bpe_handle* h, const int64_t* d_offsets, const int32_t* d_ca
     cudaStream_t st = (cudaStream_t)stream;
     PlanArgs a{d_offsets, d_cached, n_requests, n_free, max_blocks, table_stride, n_slots, FastDiv(block_size), d_free,
                d_head, d_table, d_seq_lens, d_slots, d_positions, d_info, nullptr, nullptr, nullptr, h->d_small};
-    // tokens of a thread: as few as leave at most two blocks an SM
+    // tokens of a thread: as few as leave at most two blocks an SM, and at most
+    // kPlanPairs pairs (1.5 million tokens: 733 blocks)
     const int64_t each = (n_slots + kPlanThreads * 4 * h->n_sms - 1) / (kPlanThreads * 4 * h->n_sms);
     const int tile = 2 * kPlanThreads * (int)std::min<int64_t>(kPlanPairs, std::max<int64_t>(1, each));
     const unsigned tiles = (unsigned)((n_slots + tile - 1) / tile);
