@@ -38,7 +38,7 @@ class BpeError(RuntimeError):
         self.code = code
 
 
-UNITS = ("bpe_kernels.cu", "model_ops.cu")  # translation units, compiled in parallel
+UNITS = ("bpe_kernels.cu", "model_ops.cu", "paged_ops.cu", "attend.cu")  # translation units, compiled in parallel
 
 
 def _sources():
@@ -72,7 +72,9 @@ _lib = None
 
 EXPORTS = ["bpe_build", "bpe_encode_batch", "bpe_encode_batch_host", "bpe_encode_batch_noalloc", "bpe_pretokenize_batch", "bpe_decode_batch", "bpe_set_word_cache",
            "bpe_set_timing_events", "bpe_set_phase_events", "bpe_set_call_memo", "bpe_sync_status", "bpe_table_info", "bpe_table_monotone", "bpe_merges_monotone",
-           "bpe_workspace_bytes", "bpe_train", "bpe_plan_blocks", "bpe_embed", "bpe_embed_grad", "bpe_adjust_logits", "bpe_destroy", "bpe_last_error"]
+           "bpe_workspace_bytes", "bpe_train", "bpe_plan_blocks", "bpe_embed", "bpe_embed_grad", "bpe_adjust_logits", "bpe_rotary_table",
+           "bpe_rotate", "bpe_cache_page_bytes", "bpe_cache_write", "bpe_cache_read", "bpe_attend", "bpe_destroy",
+           "bpe_last_error"]
 
 
 def lib():
@@ -124,6 +126,19 @@ def lib():
             L.bpe_plan_blocks.argtypes = [p, p, p, i64, i64, p, i64, p, p, i64, i64, p, p, p, i64, p, p]
             L.bpe_adjust_logits.restype = ctypes.c_int
             L.bpe_adjust_logits.argtypes = [p, p, p]
+            d = ctypes.c_double
+            L.bpe_rotary_table.restype = ctypes.c_int
+            L.bpe_rotary_table.argtypes = [p, i64, d, d, d, d, d, p]
+            L.bpe_rotate.restype = ctypes.c_int
+            L.bpe_rotate.argtypes = [p, p, i, i64, i64, i64, i64, i64, p, p, i64, i, i, f, p, i, i64, i64, p]
+            L.bpe_cache_page_bytes.restype = ctypes.c_int
+            L.bpe_cache_page_bytes.argtypes = [i64, i64, ctypes.POINTER(i64)]
+            L.bpe_cache_write.restype = ctypes.c_int
+            L.bpe_cache_write.argtypes = [p, p, i64, p, p, i, i64, i64, i64, i64, i64, i64, p, i64, i64, i64, p]
+            L.bpe_cache_read.restype = ctypes.c_int
+            L.bpe_cache_read.argtypes = [p, p, i64, p, i64, i64, i64, i64, i64, p, p, i, i64, i64, i64, i64, p]
+            L.bpe_attend.restype = ctypes.c_int
+            L.bpe_attend.argtypes = [p, p, p]
             L.bpe_workspace_bytes.restype = ctypes.c_int
             L.bpe_workspace_bytes.argtypes = [p, ctypes.POINTER(i64)]
             L.bpe_destroy.restype = ctypes.c_int
@@ -324,6 +339,67 @@ class LogitsArgs(ctypes.Structure):
 
 def bpe_adjust_logits(handle: int, args: LogitsArgs, stream: int) -> None:
     _check(lib().bpe_adjust_logits(handle, ctypes.byref(args), stream))
+
+
+def bpe_rotary_table(n_pairs: int, base: float = 10000.0, factor: float = 1.0, original: float = 0.0, low: float = 1.0,
+                     high: float = 4.0, frequencies=None) -> np.ndarray:
+    """Host-only: the turns a position of each pair as fractions of 2^64, uint64[n_pairs]."""
+    f = None if frequencies is None else np.ascontiguousarray(frequencies, dtype=np.float64)
+    if f is not None and f.shape != (n_pairs,):
+        raise ValueError(f"frequencies: {f.shape}, need ({n_pairs},)")
+    out = np.zeros(max(n_pairs, 0), dtype=np.uint64)
+    _check(lib().bpe_rotary_table(None if f is None else f.ctypes.data, n_pairs, base, factor, original, low, high,
+                                  out.ctypes.data))
+    return out
+
+
+def bpe_rotate(handle: int, d_x: int, x_type: int, n_tokens: int, n_heads: int, dim: int, x_token_stride: int,
+               x_head_stride: int, d_positions: int, d_turns: int, n_pairs: int, interleaved: bool, inverse: bool,
+               scale: float, d_out: int, out_type: int, out_token_stride: int, out_head_stride: int,
+               stream: int) -> None:
+    _check(lib().bpe_rotate(handle, d_x, x_type, n_tokens, n_heads, dim, x_token_stride, x_head_stride, d_positions,
+                            d_turns, n_pairs, 1 if interleaved else 0, 1 if inverse else 0, scale, d_out, out_type,
+                            out_token_stride, out_head_stride, stream))
+
+
+def bpe_cache_page_bytes(block_size: int, dim: int) -> int:
+    """Bytes of a page: one head's keys, or values, in one block of a cache in 4 bits."""
+    b = ctypes.c_int64()
+    _check(lib().bpe_cache_page_bytes(block_size, dim, ctypes.byref(b)))
+    return b.value
+
+
+def bpe_cache_write(handle: int, d_slots: int, n_tokens: int, d_keys: int, d_values: int, type: int, n_heads: int,
+                    dim: int, key_token_stride: int, key_head_stride: int, value_token_stride: int,
+                    value_head_stride: int, d_cache: int, n_blocks: int, block_stride: int, block_size: int,
+                    stream: int) -> None:
+    _check(lib().bpe_cache_write(handle, d_slots, n_tokens, d_keys, d_values, type, n_heads, dim, key_token_stride,
+                                 key_head_stride, value_token_stride, value_head_stride, d_cache, n_blocks,
+                                 block_stride, block_size, stream))
+
+
+def bpe_cache_read(handle: int, d_slots: int, n_tokens: int, d_cache: int, n_blocks: int, block_stride: int,
+                   block_size: int, n_heads: int, dim: int, d_keys: int, d_values: int, type: int,
+                   key_token_stride: int, key_head_stride: int, value_token_stride: int, value_head_stride: int,
+                   stream: int) -> None:
+    _check(lib().bpe_cache_read(handle, d_slots, n_tokens, d_cache, n_blocks, block_stride, block_size, n_heads, dim,
+                                d_keys, d_values, type, key_token_stride, key_head_stride, value_token_stride,
+                                value_head_stride, stream))
+
+
+class AttendArgs(ctypes.Structure):
+    """bpe_attend_args (device pointers as integers, None for NULL)."""
+    _fields_ = [(n, t) for names, t in (
+        ("queries out", ctypes.c_void_p), ("query_type out_type", ctypes.c_int),
+        ("query_token_stride query_head_stride out_token_stride out_head_stride n_tokens n_heads group dim",
+         ctypes.c_int64),
+        ("cache", ctypes.c_void_p), ("n_blocks block_stride block_size", ctypes.c_int64), ("table", ctypes.c_void_p),
+        ("max_blocks table_stride", ctypes.c_int64), ("seq_lens offsets", ctypes.c_void_p),
+        ("n_requests", ctypes.c_int64), ("scale", ctypes.c_float)) for n in names.split()]
+
+
+def bpe_attend(handle: int, args: AttendArgs, stream: int) -> None:
+    _check(lib().bpe_attend(handle, ctypes.byref(args), stream))
 
 
 def bpe_destroy(handle: int) -> None:
@@ -660,6 +736,215 @@ class Tokenizer:
         return out
 
 
+    # ---- a paged cache in 4 bits ----
+
+    def rotary_table(self, dim: int, base: float = 10000.0, factor: float = 1.0, original: float | None = None,
+                     low: float = 1.0, high: float = 4.0, frequencies=None):
+        """The table that rotate takes, for heads whose first ``dim`` elements
+        turn: int64[dim // 2] on the tokenizer's device (fractions of 2^64 of a
+        turn). Pair i turns base^(-2 i / dim) radians a position, or
+        ``frequencies``[i]; factor stretches contexts, by parts where the length
+        ``original`` that the model was trained on is given (see
+        bpe_rotary_table)."""
+        if dim < 0 or dim % 2:
+            raise ValueError(f"dim: {dim}, need an even number")
+        if original is not None and not original > 0:
+            raise ValueError(f"original: {original}, need a length above 0")
+        turns = bpe_rotary_table(dim // 2, base, factor, original or 0.0, low, high, frequencies)
+        return _torch().from_numpy(turns.view(np.int64)).to(f"cuda:{self.device}")
+
+    def rotate(self, x, positions, table, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
+               dtype=None, out=None):
+        """Rotary positions (see bpe_rotate) of x [tokens, heads, dim] in 32 or
+        16 bits: the first 2 * len(table) elements of each head turn, the rest
+        is copied; into a new tensor of x's type or ``dtype``, or into ``out``
+        (which may be x). positions int32[tokens]; table: from rotary_table;
+        interleaved: pairs lie next to each other, else half the turned part
+        apart; inverse turns back. Differentiable with respect to x in backward
+        and forward mode, as often as wanted; ``out`` is refused for inputs that
+        torch records derivatives of."""
+        torch, types, device = _torch(), _type_codes, self.device
+        code = types.get(x.dtype)
+        if code is None or x.get_device() != device or x.dim() != 3:
+            self._refuse("x", x, types, dims=3)
+        if _tracked(x):
+            if out is not None:
+                raise ValueError("out: needs an x without derivatives (torch.no_grad or detach)")
+            return _functions()[3].apply(self, x, positions, table, interleaved, scale, inverse, dtype or x.dtype)
+        n, heads, dim = x.shape
+        token_stride, head_stride, step = x.stride()
+        if step != 1 and dim > 1:
+            if out is x:
+                raise ValueError("out: the elements of a row must be adjacent")
+            x = x.contiguous()
+            token_stride, head_stride, _ = x.stride()
+        pairs = table.numel()
+        if 2 * pairs > dim:
+            raise ValueError(f"table: {pairs} pairs in heads of {dim} elements")
+        p_positions, p_table = self._flat("positions", positions, _int32, n), self._flat("table", table, _int64, pairs)
+        if out is None:
+            out = torch.empty((n, heads, dim), dtype=dtype or x.dtype, device=x.device)
+            out_token, out_head = heads * dim, dim
+        else:
+            out_token, out_head = self._rows_out(out, x.shape, dtype)
+        out_code = types.get(out.dtype)
+        if out_code is None:
+            self._refuse("out", out, types)
+        rc = self._lib.bpe_rotate(self.handle, x.data_ptr(), code, n, heads, dim, token_stride, head_stride,
+                                  p_positions, p_table, pairs, interleaved, inverse, scale, out.data_ptr(), out_code,
+                                  out_token, out_head, _raw_stream(device))
+        if rc:
+            _check(rc)
+        return out
+
+    def _rows_out(self, out, shape, dtype):
+        """The strides of a result [tokens, heads, dim] that the caller gives."""
+        if out.get_device() != self.device or out.shape != shape:
+            raise ValueError(f"out: needs the shape {tuple(shape)}, on the tokenizer's device")
+        token_stride, head_stride, step = out.stride()
+        if step != 1 and shape[2] > 1:
+            raise ValueError("out: the elements of a row must be adjacent")
+        if dtype is not None and dtype is not out.dtype:
+            raise ValueError(f"out: {out.dtype}, but dtype is {dtype}")
+        self._writes(out)
+        return token_stride, head_stride
+
+    def new_cache(self, n_blocks: int, block_size: int, heads: int, dim: int):
+        """A cache in 4 bits of n_blocks blocks of block_size slots, for keys and
+        values of ``heads`` heads of ``dim`` elements: uint8 [n_blocks, 2, heads,
+        page] of zeros, which stand for zeros."""
+        return _torch().zeros(n_blocks, 2, heads, bpe_cache_page_bytes(block_size, dim), dtype=_uint8,
+                              device=f"cuda:{self.device}")
+
+    def _cache(self, cache, dim, block_size):
+        """(address, blocks, bytes from block to block, heads) of a cache."""
+        if cache.dtype is not _uint8 or cache.get_device() != self.device or cache.dim() != 4:
+            self._refuse("cache", cache, (_uint8,), dims=4)
+        n_blocks, two, heads, page = cache.shape
+        block_stride, s1, s2, s3 = cache.stride()
+        want = _page_bytes.get((block_size, dim))
+        if want is None:
+            want = _page_bytes[block_size, dim] = bpe_cache_page_bytes(block_size, dim)
+        if two != 2 or page != want:
+            raise ValueError(f"cache: {tuple(cache.shape)}, need [blocks, 2, heads, {want}] for blocks of {block_size} "
+                             f"slots and rows of {dim}")
+        if s3 != 1 or s2 != page or s1 != heads * page:
+            raise ValueError("cache: the pages of a block must be adjacent")
+        return cache.data_ptr(), n_blocks, block_stride, heads
+
+    def write_cache(self, cache, slots, keys, values, block_size: int):
+        """Quantises keys and values [tokens, heads, dim], of one type in 32 or
+        16 bits, into the slots int64[tokens] of a cache (see bpe_cache_write):
+        -1 leaves a token out, the others must differ. Has no derivative, so it
+        needs inputs without one."""
+        torch, types = _torch(), _type_codes
+        code = types.get(keys.dtype)
+        if code is None or keys.get_device() != self.device or keys.dim() != 3:
+            self._refuse("keys", keys, types, dims=3)
+        if values.dtype is not keys.dtype or values.get_device() != self.device or values.shape != keys.shape:
+            raise ValueError("values: needs the type, the shape and the device of keys")
+        if _tracked(keys, values):
+            raise ValueError("write_cache has no derivative, so it needs inputs without one (torch.no_grad or detach)")
+        n, heads, dim = keys.shape
+        p_cache, n_blocks, block_stride, held = self._cache(cache, dim, block_size)
+        if held != heads:
+            raise ValueError(f"cache: {held} heads, keys have {heads}")
+        p_slots = self._flat("slots", slots, _int64, n)
+        if dim > 1:
+            if keys.stride(2) != 1:
+                keys = keys.contiguous()
+            if values.stride(2) != 1:
+                values = values.contiguous()
+        self._writes(cache)
+        kt, kh, _ = keys.stride()
+        vt, vh, _ = values.stride()
+        rc = self._lib.bpe_cache_write(self.handle, p_slots, n, keys.data_ptr(), values.data_ptr(), code, heads, dim,
+                                       kt, kh, vt, vh, p_cache, n_blocks, block_stride, block_size,
+                                       _raw_stream(self.device))
+        if rc:
+            _check(rc)
+
+    def read_cache(self, cache, slots, dim: int, block_size: int, dtype=None):
+        """What the rows of slots int64[tokens] of a cache stand for (see
+        bpe_cache_read): keys and values [tokens, heads, dim] in float32 or
+        ``dtype``; zeros for slot -1."""
+        torch = _torch()
+        p_cache, n_blocks, block_stride, heads = self._cache(cache, dim, block_size)
+        n = slots.numel()
+        p_slots = self._flat("slots", slots, _int64, n)
+        dtype = dtype or _float32
+        code = _type_codes.get(dtype)
+        if code is None:
+            raise ValueError(f"dtype: {dtype}, need {' or '.join(str(d) for d in _type_codes)}")
+        keys = torch.empty((n, heads, dim), dtype=dtype, device=cache.device)
+        values = torch.empty_like(keys)
+        rc = self._lib.bpe_cache_read(self.handle, p_slots, n, p_cache, n_blocks, block_stride, block_size, heads, dim,
+                                      keys.data_ptr(), values.data_ptr(), code, heads * dim, dim, heads * dim, dim,
+                                      _raw_stream(self.device))
+        if rc:
+            _check(rc)
+        return keys, values
+
+    def attend(self, queries, cache, table, seq_lens, block_size: int, offsets=None, scale: float | None = None,
+               dtype=None, out=None):
+        """Attention of new tokens over a cache in 4 bits (see bpe_attend):
+        queries [tokens, heads, dim] in 32 or 16 bits, their heads a multiple of
+        the cache's (neighbours share one); table int32[n, max_blocks] and
+        seq_lens int32[n] as plan_blocks leaves them; offsets int64[n + 1] of
+        the packed new tokens, or None for one new token each; scale: dim **
+        -0.5 unless given. Each token sees its request's tokens up to itself.
+        Returns [tokens, heads, dim] in queries' type or ``dtype``, or ``out``;
+        tokens of no request get zeros, or what was in out. Has no derivative: a
+        backward pass through its result raises, and ``out`` is refused for
+        inputs that torch records derivatives of."""
+        torch, types, device = _torch(), _type_codes, self.device
+        i32, i64 = _int32, _int64
+        code = types.get(queries.dtype)
+        if code is None or queries.get_device() != device or queries.dim() != 3:
+            self._refuse("queries", queries, types, dims=3)
+        if _tracked(queries):
+            if out is not None:
+                raise ValueError("out: attend has no derivative, so it needs inputs without one "
+                                 "(torch.no_grad or detach)")
+            return _functions()[4].apply(
+                lambda: self.attend(queries, cache, table, seq_lens, block_size, offsets, scale, dtype), queries)
+        n_tokens, rows, dim = queries.shape
+        p_cache, n_blocks, block_stride, heads = self._cache(cache, dim, block_size)
+        if rows == 0 or heads == 0 or rows % heads:
+            raise ValueError(f"queries: {rows} heads, the cache has {heads}")
+        if table.dtype is not i32 or table.get_device() != device or table.dim() != 2:
+            self._refuse("table", table, (i32,), dims=2)
+        n, width = table.shape
+        table_stride, step = table.stride()
+        if step != 1 and width > 1:
+            raise ValueError("table: the elements of a row must be adjacent")
+        p_lens = self._flat("seq_lens", seq_lens, i32, n)
+        p_offsets = 0 if offsets is None else self._flat("offsets", offsets, i64, n + 1)
+        token_stride, head_stride, step = queries.stride()
+        if step != 1 and dim > 1:
+            queries = queries.contiguous()
+            token_stride, head_stride, _ = queries.stride()
+        if out is None:
+            # without offsets every row is written, but those past the requests
+            make = torch.empty if offsets is None and n == n_tokens else torch.zeros
+            out = make((n_tokens, rows, dim), dtype=dtype or queries.dtype, device=queries.device)
+            out_token, out_head = rows * dim, dim
+        else:
+            out_token, out_head = self._rows_out(out, queries.shape, dtype)
+        out_code = types.get(out.dtype)
+        if out_code is None:
+            self._refuse("out", out, types)
+        rc = self._lib.bpe_attend(
+            self.handle,
+            _pack_attend(queries.data_ptr(), out.data_ptr(), code, out_code, token_stride, head_stride, out_token,
+                         out_head, n_tokens, heads, rows // heads, dim, p_cache, n_blocks, block_stride, block_size,
+                         table.data_ptr(), width, table_stride, p_lens, p_offsets, n,
+                         dim ** -0.5 if scale is None else scale), _raw_stream(device))
+        if rc:
+            _check(rc)
+        return out
+
+
 def _skip(skip_id):
     """skip_id for the library, in 32 bits: ctypes would cut what is longer, and skip another id."""
     if skip_id is None:
@@ -673,17 +958,20 @@ def _skip(skip_id):
 # a tenth of the time of filling a LogitsArgs field by field
 _pack_logits = struct.Struct("@PPiiqqqqPPqPPqqPPPPPPqPqqP").pack
 
+_pack_attend = struct.Struct("@PPiiqqqqqqqqPqqqPqqPPqf0P").pack  # bpe_attend_args, likewise
+_page_bytes = {}  # (block size, dim) -> bytes of a page of a cache
+
 _type_codes = {}  # torch dtype -> BPE_* code
 
-_torch_module = _int32 = _int64 = _float32 = _raw_stream = _forward_ad = _increment_version = None
+_torch_module = _int32 = _int64 = _float32 = _uint8 = _raw_stream = _forward_ad = _increment_version = None
 
 
 def _torch():
     """torch, imported on first use, with what the calls above take from it."""
-    global _torch_module, _int32, _int64, _float32, _raw_stream, _forward_ad, _increment_version
+    global _torch_module, _int32, _int64, _float32, _uint8, _raw_stream, _forward_ad, _increment_version
     if _torch_module is None:
         import torch
-        _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
+        _int32, _int64, _float32, _uint8 = torch.int32, torch.int64, torch.float32, torch.uint8
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _forward_ad = torch.autograd.forward_ad
         _increment_version = torch.autograd.graph.increment_version
@@ -707,11 +995,12 @@ def _tracked(*tensors):
 
 
 def _functions():
-    """The autograd functions of Tokenizer.embed, embed_grad and adjust_logits
-    (made once: torch is imported on first use only). The first two are linear
-    and each other's adjoint, so their derivatives of any order, backward and
-    forward, are calls of the two. The last has none, and says so when one is
-    asked for."""
+    """The autograd functions of Tokenizer.embed, embed_grad, adjust_logits,
+    rotate and attend (made once: torch is imported on first use only). The first
+    two are linear and each other's adjoint, and rotate is linear with the inverse
+    rotation as its adjoint, so their derivatives of any order, backward and
+    forward, are calls of them. adjust_logits and attend have none, and say so
+    when one is asked for."""
     global _function_list
     if _function_list is None:
         import torch
@@ -769,7 +1058,41 @@ def _functions():
             def jvp(ctx, *tangents):
                 raise RuntimeError("adjust_logits has no derivative")
 
-        _function_list = Embed, EmbedGrad, AdjustLogits
+        class Rotate(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, tok, x, positions, table, interleaved, scale, inverse, dtype):
+                ctx.args = (tok, interleaved, scale, inverse, x.dtype, dtype)
+                ctx.save_for_backward(positions, table)
+                ctx.save_for_forward(positions, table)
+                return tok.rotate(x.detach(), positions, table, interleaved, scale, inverse, dtype)
+
+            @staticmethod
+            def backward(ctx, grad):
+                tok, interleaved, scale, inverse, dtype, _ = ctx.args
+                positions, table = ctx.saved_tensors
+                return (None, tok.rotate(grad, positions, table, interleaved, scale, not inverse, dtype),
+                        *(None,) * 6)
+
+            @staticmethod
+            def jvp(ctx, _tok, x, *_):
+                tok, interleaved, scale, inverse, _, dtype = ctx.args
+                positions, table = ctx.saved_tensors
+                return tok.rotate(x, positions, table, interleaved, scale, inverse, dtype)
+
+        class Attend(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, call, queries):
+                return call()
+
+            @staticmethod
+            def backward(ctx, grad):
+                raise RuntimeError("attend has no gradient")
+
+            @staticmethod
+            def jvp(ctx, *tangents):
+                raise RuntimeError("attend has no derivative")
+
+        _function_list = Embed, EmbedGrad, AdjustLogits, Rotate, Attend
     return _function_list
 
 

@@ -16,19 +16,6 @@
 
 namespace {
 
-// Exact division of numbers below 2^31 by d in [1, 2^31): with 2^(l-1) < d <=
-// 2^l and m = ceil(2^(31+l) / d), the excess e = m d - 2^(31+l) is below 2^l,
-// so x m / 2^(31+l) = x / d + (x / 2^31) (e / 2^l) / d, which is less than 1/d
-// above x / d and has the same floor.
-struct FastDiv {
-  uint32_t d, m, l;
-  explicit FastDiv(int64_t by = 1) : d((uint32_t)by), l(0) {
-    while ((1ll << l) < by) ++l;
-    m = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return (uint32_t)(((uint64_t)x * m) >> (31 + l)); }
-};
-
 struct PlanArgs {
   const int64_t* offsets;  // [n + 1] or null: one new token each
   const int32_t* cached;   // [n] or null: none

@@ -325,6 +325,10 @@ int bpe_train(const uint8_t* word_bytes, const int64_t* word_offsets, const int6
  *   bpe_plan_blocks    block tables and cache slots of a batch of requests;
  *   bpe_embed          rows of an embedding table;
  *   bpe_embed_grad     its gradient;
+ *   bpe_rotate         rotary positions of queries and keys, and their gradient;
+ *   bpe_cache_write,   keys and values into the slots of a paged cache in 4
+ *   bpe_cache_read     bits, and back;
+ *   bpe_attend         attention over that cache;
  *   bpe_adjust_logits  penalties, biases and grammar masks, before the choice
  *                      of the next ids that bpe_decode_batch takes.
  * They use the handle's device, workspace and status; its vocabulary plays no
@@ -440,6 +444,164 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
                    bpe_stream_t stream);
 
 /*
+ * bpe_rotary_table — how far a position turns each pair of a head.
+ *
+ *   frequencies    host double[n_pairs], radians a position (any finite ones),
+ *                  or NULL: base^(-i / n_pairs) for pair i.
+ *   factor         > 0, how far contexts are stretched (1: not at all).
+ *   original       0: every frequency is divided by factor. Else the length
+ *                  that the model was trained on, and frequencies are stretched
+ *                  by parts: with r the turns that a pair makes over it, a
+ *                  pair with r >= high is kept, one with r <= low divided by
+ *                  factor, and between them f becomes
+ *                  f * (g + (1 - g) / factor), g = (r - low) / (high - low).
+ *   turns          host uint64[n_pairs], receives the turns a position as
+ *                  fractions of 2^64; a copy on the device is what bpe_rotate
+ *                  takes.
+ * Host-only: needs no GPU and no handle. n_pairs <= 32768.
+ */
+int bpe_rotary_table(const double* frequencies, int64_t n_pairs, double base, double factor, double original,
+                     double low, double high, uint64_t* turns);
+
+/*
+ * bpe_rotate — rotary positions: of each head of token t, the pairs (x1, x2) of
+ * its first 2 * n_pairs elements become
+ *   scale * (x1 cos a - x2 sin a, x1 sin a + x2 cos a),
+ * a = the pair's angle at d_positions[t], computed to 2^-25 of a half turn at
+ * every position; what is behind them is copied. One call takes the queries and
+ * keys of a fused projection together, as heads of one tensor.
+ *
+ *   d_x            device [n_tokens][n_heads][dim] of x_type, tokens
+ *                  x_token_stride and heads x_head_stride elements apart (any
+ *                  strides >= 0), elements adjacent.
+ *   d_positions    device int32[n_tokens], any values (bpe_plan_blocks writes
+ *                  them).
+ *   d_turns        device uint64[n_pairs], 2 * n_pairs <= dim.
+ *   interleaved    0: pair i is elements i and n_pairs + i; else 2 i and 2 i + 1.
+ *   inverse        not 0: turns by -a. With the same scale that is the gradient:
+ *                  of d_x for the gradient d_x of the result.
+ *   d_out          device, of out_type, like d_x; its rows must not overlap. It
+ *                  may be d_x itself (one type, the same strides), but must not
+ *                  overlap it otherwise.
+ * Computed in 32 bits and rounded once. Types are BPE_F32, BPE_F16 or BPE_BF16,
+ * in any pair. n_tokens < 2^31 - 1, n_heads <= 65536, dim <= 65536. No workspace.
+ */
+int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int64_t n_heads, int64_t dim,
+               int64_t x_token_stride, int64_t x_head_stride, const int32_t* d_positions, const uint64_t* d_turns,
+               int64_t n_pairs, int interleaved, int inverse, float scale, void* d_out, int out_type,
+               int64_t out_token_stride, int64_t out_head_stride, bpe_stream_t stream);
+
+/*
+ * A paged cache of keys and values in 4 bits, as bpe_plan_blocks plans it: slot
+ * t of block q is slot q * block_size + t.
+ *
+ * A row (a token's key or value of one head, of dim elements) is cut into
+ * groups of 32, the last one shorter; beyond four, the number of groups is
+ * rounded up to an even one. A group has a base and a step in bfloat16 and a
+ * code of 4 bits for each element:
+ *   base = bf16(smallest element)
+ *   step = bf16((largest / 2 - base / 2) / 7.5), 0 where that is below 2^-100
+ *   code = (x / 2 - base / 2) * (1 / (step / 2)), to the nearest whole number
+ *          in [0, 15]; 0 where step is 0
+ * (32-bit operations, to nearest even), and stands for base + step * code. A group
+ * with a NaN or an element beyond bfloat16's largest stands for NaNs.
+ *
+ * A block is [2][n_heads] pages, keys before values. A page holds the
+ * block_size rows' codes (16 bytes a group), then the rows' (step, base) words
+ * (step in the low half), one a group, and ends at a multiple of 16 bytes. The
+ * codes of 8 elements are a 32-bit word, the first in the lowest bits; of two
+ * groups j, j + 1 (j even) the four words each alternate, those of a last group
+ * without a partner are in order. bpe_cache_page_bytes says what a page takes;
+ * the cache is 16-byte aligned, its blocks block_stride bytes apart (a multiple
+ * of 16, at least 2 * n_heads pages: layers may share a block).
+ * Sizes: block_size <= 1048576, n_heads <= 65536, dim <= 256, fewer than 2^31
+ * blocks.
+ */
+#define BPE_CACHE_MAX_BLOCK 1048576
+#define BPE_CACHE_MAX_HEADS 65536
+#define BPE_CACHE_MAX_DIM 256
+int bpe_cache_page_bytes(int64_t block_size, int64_t dim, int64_t* bytes);
+
+/*
+ * bpe_cache_write — quantises keys and values into their slots.
+ *
+ *   d_slots        device int64[n_tokens], as bpe_plan_blocks writes them. A
+ *                  token with slot -1 is left out; other slots outside the
+ *                  cache are left out and reported (BPE_ERR_BAD_INPUT). Slots
+ *                  must differ: what two tokens leave in one slot is
+ *                  undefined, other slots are not touched.
+ *   d_keys, d_values   device [n_tokens][n_heads][dim] of one type, with
+ *                  strides of tokens and heads in elements (any >= 0).
+ */
+int bpe_cache_write(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, const void* d_keys, const void* d_values,
+                    int type, int64_t n_heads, int64_t dim, int64_t key_token_stride, int64_t key_head_stride,
+                    int64_t value_token_stride, int64_t value_head_stride, void* d_cache, int64_t n_blocks,
+                    int64_t block_stride, int64_t block_size, bpe_stream_t stream);
+
+/*
+ * bpe_cache_read — what the rows of slots stand for, computed in 32 bits and
+ * rounded once. Slot -1 gives zeros; other slots outside the cache give zeros
+ * and are reported. The rows of d_keys, and of d_values, must not overlap.
+ */
+int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, const void* d_cache, int64_t n_blocks,
+                   int64_t block_stride, int64_t block_size, int64_t n_heads, int64_t dim, void* d_keys,
+                   void* d_values, int type, int64_t key_token_stride, int64_t key_head_stride,
+                   int64_t value_token_stride, int64_t value_head_stride, bpe_stream_t stream);
+
+/*
+ * bpe_attend — attention of new tokens over the cache: of token i of the m new
+ * ones of a request with L tokens in the cache (its new ones among them), and
+ * of each query head g of the n_heads * group, over head g / group of the cache,
+ *   out = sum over t < L - m + i + 1 of p_t value_t,
+ *   p = softmax of scale * (query . key_t).
+ * A token that sees none (as of a request that bpe_plan_blocks did not serve)
+ * gets zeros.
+ *
+ * Every pointer is a device pointer.
+ *   queries        [n_tokens][n_heads * group][dim] of query_type, tokens and
+ *                  heads query_token_stride and query_head_stride elements
+ *                  apart.
+ *   out            the same of out_type; rows must not overlap, nor queries.
+ *                  Rows of no request are left as they are.
+ *   cache          n_blocks blocks of block_size slots (see above).
+ *   table          int32[n_requests][max_blocks], rows table_stride elements
+ *                  apart; seq_lens int32[n_requests], both as bpe_plan_blocks
+ *                  leaves them.
+ *   offsets        int64[n_requests + 1]: request r's new tokens are
+ *                  [offsets[r], offsets[r + 1]). NULL: one each (a decode
+ *                  step; n_tokens is then n_requests at least).
+ * Sums and the softmax are in 32 bits. Products run on the tensor cores with
+ * codes, which are exact there, and with queries and weights cut into parts of
+ * bfloat16: queries without loss, weights to 2^-17 (f32: 2^-25) of their value.
+ * Left out and reported (BPE_ERR_BAD_INPUT): requests whose offsets are not
+ * monotone in [0, n_tokens] (their rows are left as they are), those with a
+ * length outside [0, max_blocks * block_size], or
+ * above 2^31 - 65 (zeros), and tokens whose block
+ * is outside the cache (not seen). Where offsets fall, rows that several
+ * requests share hold what one of them gives.
+ * Sizes: n_requests and n_tokens < 2^31 - 1, n_tokens * n_heads * group < 2^31,
+ * group <= 256. Workspace: partial sums, at most BPE_ATTEND_PARTIALS * multiprocessors * (dim + 2) * 4
+ * bytes (dim rounded up to 32, 64, 96, 128, 192 or 256), for any lengths.
+ */
+#define BPE_ATTEND_PARTIALS 256
+typedef struct bpe_attend_args {
+  const void* queries;
+  void* out;
+  int query_type, out_type;
+  int64_t query_token_stride, query_head_stride, out_token_stride, out_head_stride;
+  int64_t n_tokens, n_heads, group, dim;
+  const void* cache;
+  int64_t n_blocks, block_stride, block_size;
+  const int32_t* table;
+  int64_t max_blocks, table_stride;
+  const int32_t* seq_lens;
+  const int64_t* offsets;
+  int64_t n_requests;
+  float scale;
+} bpe_attend_args;
+int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream);
+
+/*
  * bpe_adjust_logits — penalties for repeated tokens, biases and grammar masks
  * on a batch's logits. For row b and token v, with k the times v occurs in the
  * row's output:
@@ -531,8 +693,8 @@ int bpe_table_monotone(const bpe_handle* h, int* monotone);
 
 /* Bytes of device workspace the handle holds now (0 until a call needs it),
  * with outgrown blocks that are kept for captured graphs: bpe_encode_batch,
- * bpe_encode_batch_host, bpe_decode_batch, bpe_plan_blocks and bpe_embed_grad
- * grow it; bpe_encode_batch_noalloc never does. */
+ * bpe_encode_batch_host, bpe_decode_batch, bpe_plan_blocks, bpe_embed_grad
+ * and bpe_attend grow it; bpe_encode_batch_noalloc never does. */
 int bpe_workspace_bytes(const bpe_handle* h, int64_t* bytes);
 
 /* Frees the handle's device memory. Waits for its device first. */
