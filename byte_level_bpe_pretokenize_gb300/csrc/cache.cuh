@@ -48,7 +48,7 @@ struct CacheArgs {
   unsigned char* cache;
   int64_t block_stride, page_bytes, n_slots;
   FastDiv block;     // slots of a block
-  FastDiv words, heads;  // words of a row; heads of a token
+  FastDiv parts, heads;  // threads of a row; heads of a token
   int groups, dim;
   const int64_t* slots;
   DevSmall* small;
