@@ -6,23 +6,24 @@
 //
 // over the tokens t that the query sees, in one pass with the running maximum m.
 // With the codes n, the steps S and bases B of group j,
-//   query . key_t = sum_j 16 S_tj (sum_i q_i (1 + n_ti / 16)) + (B_tj - 16 S_tj) (sum_i q_i)
-//   out_i = sum_t (p_t 16 S_tj) (1 + n_ti / 16) + sum_t p_t (B_tj - 16 S_tj)
-// The sums over i and t in which codes take part run on the tensor cores:
-// 1 + n / 16 is a code with an exponent put before it, exact in 16 bits and made
-// by a shift and one logical operation for two codes; steps and bases stay
-// outside, in 32 bits.
+//   query . key_t = sum_j S_tj (sum_i q_i n_ti) + B_tj (sum_i q_i)
+//   out_i = sum_t (p_t S_tj) (n_ti - 8) + sum_t p_t (B_tj + 8 S_tj)
+// All sums over i and t run on the tensor cores. A code is its own bits there: a
+// mask leaves it in the lowest or the next four of a half's mantissa, where it
+// is the subnormal n 2^-24 or n 2^-20, exactly; queries and weights carry what
+// is lacking. Keys' steps stay outside, in 32 bits; values' steps go to the
+// weights, whose mean with n - 8 loses less to their rounding than with n.
 
 namespace {
 
-constexpr int kAttWarps = 8;
-constexpr int kAttThreads = kAttWarps * 32;
-constexpr int kUnit = 32;  // tokens of a step
+constexpr int kUnit = 32;      // tokens of a step
+constexpr int kItemCost = 3;   // what beginning and ending an item takes, in steps
+constexpr int kAttMaxWarps = 16;  // workers of an SM
 
 struct AttendArgs {
   const void* queries;
   void* out;
-  int out_type;
+  int q_type, out_type;
   int64_t q_token, q_head, o_token, o_head;
   int64_t n_tokens;
   int heads, dim;
@@ -37,6 +38,8 @@ struct AttendArgs {
   int n;
   float scale;            // times log2 e
   bool q_wide, o_wide;    // rows are aligned for vectors
+  bool centre;            // codes of values count from their middle
+  bool near;              // the cache lies within 2^32 times 16 bytes
   float* partial;
   int4* record;
   DevSmall* small;
@@ -58,23 +61,63 @@ __device__ __forceinline__ AttendRequest attend_request(const AttendArgs& a, int
   return q;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = a b, and d += a b. The first needs no zeros in registers.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 1 + n / 16 of the codes at bits 4 e and 16 + 4 e of a word, as two 16-bit floats.
-template <bool kHalf>
-__device__ __forceinline__ uint32_t codes_to_floats(uint32_t w, int e) {
-  if (kHalf) return ((e == 0 ? w << 6 : e == 1 ? w << 2 : e == 2 ? w >> 2 : w >> 6) & 0x03C003C0u) | 0x3C003C00u;
-  return ((e == 0 ? w << 3 : w >> (4 * e - 3)) & 0x00780078u) | 0x3F803F80u;
+// The codes of a word's halves, e = 0 and 1 of the word itself or e = 2 and 3 of
+// the word shifted by 8. As subnormal halves, n 2^-24 and n 2^-20, they cost one
+// operation, but the tensor cores cut sums off some 24 bits below a product's
+// exponent, which for a subnormal is 2^-14: that leaves 2^-15 of a sum, enough for
+// results of 16 bits. For 32-bit ones (P = 2) they become n - kFrom in the normal
+// range, two operations more.
+template <int P, int kFrom>
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
+  if (P == 1) return w & 0x000F000Fu;
+  const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + n
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.f + kFrom));
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
+template <int P, int kFrom>
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
+  if (P == 1) return w & 0x00F000F0u;
+  const uint32_t x = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 n
+  const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-64.f - kFrom));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// what brings them back
+template <int P>
+constexpr float kCodesEven = P == 1 ? 0x1p24f : 1.f;
+template <int P>
+constexpr float kCodesOdd = P == 1 ? 0x1p20f : 1.f;
+constexpr uint32_t kMinus8Even = 0x80088008u, kMinus8Odd = 0x80808080u;  // of the subnormals
+
+// 2^x for whole x in [-126, 127].
+__device__ __forceinline__ float power_of_2(int x) { return __int_as_float((x + 127) << 23); }
+
+__device__ __forceinline__ uint32_t pack_halves(float low, float high) {
+  const __half2 h = __floats2half2_rn(low, high);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -82,13 +125,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-template <int kBytes>
+template <int kBytes, bool kThere>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool there) {
-  const int size = there ? kBytes : 0;  // else zeros
-  if (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(kBytes), "r"(size) : "memory");
+  if constexpr (kThere) {
+    if constexpr (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes) : "memory");
+  } else {
+    const int size = there ? kBytes : 0;  // else zeros
+    if constexpr (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(kBytes), "r"(size) : "memory");
+  }
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
@@ -102,26 +152,25 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   return v;
 }
 
-// Cuts x into kParts bfloat16 numbers that add up to it (to 2^-9 of the last):
-// the leading ones by cutting bits off, the last rounded.
+// Cuts x and y into kParts halves each that add up to them: two leave 2^-24 of a
+// number that stays above 2^-2.
 template <int kParts>
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&part)[kParts]) {
-#pragma unroll
-  for (int p = 0; p + 1 < kParts; ++p) {
-    part[p] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-    x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-    y -= __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
+__device__ __forceinline__ void split_halves(float x, float y, uint32_t (&part)[kParts]) {
+  part[0] = pack_halves(x, y);
+  if (kParts == 2) {
+    const float2 lead = unpack_halves(part[0]);
+    part[kParts - 1] = pack_halves(x - lead.x, y - lead.y);
   }
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(part[kParts - 1]) : "f"(y), "f"(x));
 }
 
 // Where the tokens of all requests are cut. A request with new tokens has
 // heads x tiles items (a tile: 8 NT columns, a column a query head of a new
 // token), each of its tokens in steps of kUnit (one at least, so that every row
-// is written). The steps of all items in a row are dealt out evenly.
+// is written), before which kItemCost places count for its beginning and end.
+// The places of all items in a row are dealt out evenly.
 struct AttendCursor {
-  int r, h, tile, u;          // request, head, tile, step
-  int tiles, units;
+  int r, h, tile;    // request, head, tile
+  int tiles, units;  // of the request; steps of the item
   AttendRequest q;
 };
 
@@ -136,13 +185,12 @@ __device__ __forceinline__ int64_t attend_units(const AttendArgs& a, int r, bool
   AttendCursor c;
   c.q = attend_request(a, r, report);
   attend_sizes<kCols>(a, c);
-  return (int64_t)c.units * c.tiles * a.heads;
+  return (int64_t)(c.units + kItemCost) * c.tiles * a.heads;
 }
 
+// The next item.
 template <int kCols>
 __device__ __forceinline__ void attend_next(const AttendArgs& a, AttendCursor& c) {
-  if (++c.u < c.units) return;
-  c.u = 0;
   if (++c.tile < c.tiles) return;
   c.tile = 0;
   if (++c.h < a.heads) return;
@@ -158,19 +206,30 @@ __device__ __forceinline__ void attend_next(const AttendArgs& a, AttendCursor& c
 template <int G, int kParts, int NT>
 struct AttendShape {
   static constexpr int kCols = 8 * NT;
+  static constexpr int kUnits = (G + 1) / 2;                         // pairs of groups
   static constexpr int kRow = 16 * G, kPair = 4 * G;                 // bytes of a row's codes, of its pairs
   static constexpr int kHalfStage = kUnit * (kRow + kPair);          // keys, or values
   static constexpr int kStage = 2 * kHalfStage;
   static constexpr int kScores = NT * kUnit * 8 * 4;
-  static constexpr int kWarp = 2 * kStage + kScores;
-  static constexpr int kSmem = kAttWarps * kWarp;
+  static constexpr int kSteps = G * kUnit * 2;                       // values' steps as halves, and mids likewise
+  // As many warps an SM as registers allow: 8 x 2 of 128, 6 x 2 of 168 or 8 of 255. The queries, which only the first half of a
+  // step needs, stay in shared memory where it has room for them.
+  static constexpr bool kSmall = G <= 4 && NT == 1 && kParts == 1;
+  static constexpr bool kQueriesShared = kParts == 1 && G <= 6;
+  static constexpr int kQueries = kQueriesShared ? NT * G * 512 : 0;
+  static constexpr int kWarp = 2 * kStage + kScores + (1 + kParts) * kSteps + kQueries;
+  static constexpr int kBlocks = kSmall ? 2 : 1;
+  static constexpr int kWarps = kSmall && G == 4 ? 6 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kSmem = kWarps * kWarp;
   static constexpr int kPartial = kCols * (32 * G + 2);              // floats of an item's partial sums
+  static constexpr int kBaseMmas = (3 * kUnits + 7) / 8;             // products of keys' bases
 };
 
 // Rows of 64 and of 128 bytes lie on two and on one set of banks: their 32-byte
 // pieces are exchanged, so that the eight-byte loads of four rows meet no other.
 template <int G>
-__device__ __forceinline__ uint32_t attend_piece(int row, int piece) {
+__device__ __forceinline__ uint32_t attend_piece(uint32_t row, uint32_t piece) {
   if (G == 4) return piece ^ (row >> 1 & 1);
   if (G == 8) return piece ^ (row & 3);
   return piece;
@@ -197,6 +256,7 @@ __device__ __forceinline__ void attend_store(const AttendArgs& a, int64_t row, i
   else put(__nv_bfloat16{});
 }
 
+
 // A warp is a worker: it walks its share of the steps with the next step's codes
 // on their way into its own half of shared memory, and waits for no other warp.
 // What it has of an item that other workers share goes to the workspace
@@ -206,20 +266,25 @@ __device__ __forceinline__ void attend_store(const AttendArgs& a, int64_t row, i
 // of 8 columns of mma.sync leave little unused, where tcgen05 would take 128 rows
 // of keys from shared memory in 16 bits, four times the bytes that a code has
 // there.
-template <class TQ, int G, int NT>
-__global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) == 2) ? 2 : 1) k_attend(AttendArgs a) {
-  constexpr bool kHalf = std::is_same<TQ, __half>::value;
-  constexpr int QP = sizeof(TQ) == 4 ? 3 : 1;  // parts of a query
-  constexpr int PP = sizeof(TQ) == 4 ? 3 : 2;  // parts of a weight
-  using Shape = AttendShape<G, QP, NT>;
+//
+// P is 1 for 16-bit queries, which a half holds without loss once they are
+// scaled by a power of two, and 2 for 32-bit ones. Weights are halves too (P of
+// them): 2^-12 of a weight, which is what a result of 11 bits rounds away.
+template <int P, int G, int NT>
+__global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G, P, NT>::kBlocks) k_attend(AttendArgs a) {
+  using Shape = AttendShape<G, P, NT>;
+  constexpr int kWarps = Shape::kWarps, kThreads = Shape::kThreads;
+  constexpr int U = Shape::kUnits;
+  constexpr float kEven = kCodesEven<P>, kOdd = kCodesOdd<P>;
   constexpr int kCols = Shape::kCols;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ int64_t upto[kAttThreads + 1];
-  __shared__ int64_t warp_sum[kAttWarps];
+  __shared__ int64_t upto[kThreads + 1];
+  __shared__ int64_t warp_sum[kWarps];
+  __shared__ AttendCursor items[kWarps][2];  // each warp's, of its copies and of their use: seldom needed
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
   // steps of all requests: each thread adds up a run of them
-  const int each = (a.n + kAttThreads - 1) / kAttThreads;
+  const int each = (a.n + kThreads - 1) / kThreads;
   const int r0 = min(a.n, (int)threadIdx.x * each), r1 = min(a.n, r0 + each);
   int64_t sum = 0;
   for (int r = r0; r < r1; ++r) sum += attend_units<kCols>(a, r, blockIdx.x == 0);
@@ -235,20 +300,24 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
   upto[threadIdx.x + 1] = x;
   if (threadIdx.x == 0) upto[0] = 0;
   __syncthreads();
-  const int64_t total = upto[kAttThreads];
+  const int64_t total = upto[kThreads];
 
   // neighbours in the row of steps are on different SMs
-  const int64_t all = (int64_t)gridDim.x * kAttWarps, workers = min(all, total);
+  const int64_t all = (int64_t)gridDim.x * kWarps, workers = min(all, total);
   const int64_t me = (int64_t)warp * gridDim.x + blockIdx.x;
   if (lane < 2) a.record[2 * me + lane] = make_int4(-1, 0, 0, 0);
   __syncwarp();
   if (me >= workers) return;
-  const int64_t from = total * me / workers, count = total * (me + 1) / workers - from;
+  const int64_t from = total * me / workers;
+  const int count = (int)(total * (me + 1) / workers - from);  // places of this worker
 
-  AttendCursor use;
-  int64_t passed = 0;  // steps taken
+  AttendCursor* const item_ahead = &items[warp][0];
+  AttendCursor* const item = &items[warp][1];
+  int place;          // of the step, in this worker's share
+  int u, units;       // step of the item, of so many
   {
-    int lo = 0, hi = kAttThreads;  // upto[lo] <= from < upto[hi]
+    AttendCursor use;
+    int lo = 0, hi = kThreads;  // upto[lo] <= from < upto[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (upto[mid] <= from) lo = mid;
@@ -276,134 +345,280 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
     use.r = min(r, a.n - 1);
     use.q = attend_request(a, use.r, false);
     attend_sizes<kCols>(a, use);
-    const int64_t item = rest / use.units;
-    use.u = (int)(rest - item * use.units);
-    use.h = (int)(item / use.tiles);
-    use.tile = (int)(item - (int64_t)use.h * use.tiles);
+    const int64_t before = rest / (use.units + kItemCost);
+    units = use.units;
+    u = (int)(rest - before * (use.units + kItemCost)) - kItemCost;
+    place = max(0, -u);
+    u = max(0, u);
+    use.h = (int)(before / use.tiles);
+    use.tile = (int)(before - (int64_t)use.h * use.tiles);
+    if (lane < 2) items[warp][lane] = use;
+    __syncwarp();
   }
+  if (place >= count) return;  // the beginning of an item alone
 
+  // in registers for good: a quadruple made anew costs four moves at each of its products
+  uint32_t minus8[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("mov.b32 %0, %1;" : "=r"(minus8[i]) : "r"(i & 1 ? kMinus8Odd : kMinus8Even));
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * Shape::kWarp;
-  const uint32_t scores = ring + 2 * Shape::kStage;
+  const uint32_t scores = ring + 2 * Shape::kStage, steps = scores + Shape::kScores;
 
   // ---- the copies of a step, one ahead of its use ----
-  AttendCursor ahead = use;
+  const int64_t values = (int64_t)a.heads * a.page_bytes;
+  const uint64_t stride16 = (uint64_t)a.block_stride / 16;
+  uint64_t head16 = 0;  // the head's first page in a block
+  auto next_item = [&](AttendCursor* at) {
+    AttendCursor c = *at;
+    attend_next<kCols>(a, c);
+    __syncwarp();
+    if (lane == 0) *at = c;
+    __syncwarp();
+  };
+  int ahead_place = place, ahead_u = u, ahead_units = units, ahead_len = item_ahead->q.len;
+  head16 = (uint64_t)item_ahead->h * (uint64_t)(a.page_bytes / 16);
   int entry = 0;  // of the lane's token in the next step to copy
   auto look_up = [&] {
-    const int t = ahead.u * kUnit + lane;
-    entry = t < ahead.q.len ? __ldg(a.table + (int64_t)ahead.r * a.table_stride + a.block((uint32_t)t)) : -1;
+    const int t = ahead_u * kUnit + lane;
+    entry = t < ahead_len ? __ldg(a.table + (int64_t)item_ahead->r * a.table_stride + a.block((uint32_t)t)) : -1;
+  };
+  // Goes on to the next step, if this worker has one.
+  auto step_ahead = [&] {
+    const bool last = ahead_u + 1 == ahead_units;
+    ahead_place += last ? 1 + kItemCost : 1;
+    if (ahead_place >= count) return;
+    ++ahead_u;
+    if (last) {
+      next_item(item_ahead);
+      ahead_u = 0;
+      ahead_units = item_ahead->units;
+      ahead_len = item_ahead->q.len;
+      head16 = (uint64_t)item_ahead->h * (uint64_t)(a.page_bytes / 16);
+    }
+    look_up();
   };
   auto copy = [&](int stage) -> uint32_t {
-    const int t = ahead.u * kUnit + lane;
+    const int t = ahead_u * kUnit + lane;
     const bool there = (uint32_t)entry < (uint32_t)a.n_blocks && entry >= 0;
-    if (!there && t < ahead.q.len) atomicOr(&a.small->op_status, kStBadInput);
+    if (!there && t < ahead_len) atomicOr(&a.small->op_status, kStBadInput);
     const uint32_t row = (uint32_t)t - a.block((uint32_t)t) * a.block.d;
-    const unsigned char* page =
-        there ? a.cache + (int64_t)entry * a.block_stride + (int64_t)ahead.h * a.page_bytes : a.cache;
-    const int64_t values = there ? (int64_t)a.heads * a.page_bytes : 0;
-    const unsigned char* codes = there ? page + (int64_t)row * Shape::kRow : page;
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, there);
     const uint32_t to = ring + stage * Shape::kStage;
+    // Addresses are counted in 16 bytes from the cache's first, in 32 bits where it is below 64 GB.
+    auto get = [&](auto type, auto whole_tag) {
+      using T = decltype(type);
+      constexpr bool kWhole = decltype(whole_tag)::value;
+      constexpr bool kSteady = G != 3 && G != 6;  // a lane has the same chunk of rows 32 / G apart
+      const T head = (T)(there ? entry : 0) * (T)stride16 + (T)head16, codes = head + (T)row * G;
+      const unsigned char* pairs = a.cache + (uint64_t)head * 16 + (a.block.d * 4 + row) * (uint32_t)Shape::kPair;
+      const uint32_t d0 = to + (lane / G) * Shape::kRow + (attend_piece<G>(lane / G, lane % G >> 1) * 2 + (lane % G & 1)) * 16;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const int at = i * 32 + lane, src = at / G, chunk = at % G;
-      const unsigned char* p =
-          reinterpret_cast<const unsigned char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(codes), src));
-      const int64_t v = __shfl_sync(0xFFFFFFFFu, (unsigned long long)values, src);
-      const bool ok = v != 0;
-      const uint32_t d = to + src * Shape::kRow + (attend_piece<G>(src, chunk >> 1) * 2 + (chunk & 1)) * 16;
-      copy_async<16>(d, p + (ok ? chunk * 16 : 0), ok);
-      copy_async<16>(d + Shape::kHalfStage, p + (ok ? v + chunk * 16 : 0), ok);
-    }
-    const unsigned char* pairs =
-        there ? page + ((int64_t)a.block.d * 16 + (int64_t)row * 4) * G : page;
-    constexpr int kPiece = G % 4 == 0 ? 16 : G % 2 == 0 ? 8 : 4;
+      for (int i = 0; i < G; ++i) {
+        const int at = i * 32 + lane, src = at / G, chunk = at % G;
+        const uint64_t from = __shfl_sync(0xFFFFFFFFu, codes, src);
+        const bool ok = kWhole || (all >> src & 1);
+        const unsigned char* p = a.cache + chunk * 16 + from * 16;
+        const unsigned char* v = a.cache + values + chunk * 16 + from * 16;
+        const uint32_t d = kSteady ? d0 + i * (32 / G) * Shape::kRow
+                                   : to + src * Shape::kRow + (attend_piece<G>(src, chunk >> 1) * 2 + (chunk & 1)) * 16;
+        copy_async<16, kWhole>(d, ok ? p : a.cache, ok);
+        copy_async<16, kWhole>(d + Shape::kHalfStage, ok ? v : a.cache, ok);
+      }
+      const bool ok = kWhole || there;
+      constexpr int kPiece = G % 4 == 0 ? 16 : G % 2 == 0 ? 8 : 4;
 #pragma unroll
-    for (int i = 0; i < Shape::kPair / kPiece; ++i) {
-      const uint32_t d = to + kUnit * Shape::kRow + lane * Shape::kPair + i * kPiece;
-      copy_async<kPiece>(d, pairs + (there ? i * kPiece : 0), there);
-      copy_async<kPiece>(d + Shape::kHalfStage, pairs + (there ? values + i * kPiece : 0), there);
-    }
+      for (int i = 0; i < Shape::kPair / kPiece; ++i) {
+        const uint32_t d = to + kUnit * Shape::kRow + lane * Shape::kPair + i * kPiece;
+        copy_async<kPiece, kWhole>(d, ok ? pairs + i * kPiece : a.cache, ok);
+        copy_async<kPiece, kWhole>(d + Shape::kHalfStage, ok ? pairs + values + i * kPiece : a.cache, ok);
+      }
+    };
+    if (all == 0xFFFFFFFFu && a.near) get(uint32_t{}, std::true_type{});
+    else get(uint64_t{}, std::false_type{});
     asm volatile("cp.async.commit_group;" ::: "memory");
-    return __ballot_sync(0xFFFFFFFFu, there);
+    return all;
   };
 
   // ---- an item's state ----
-  uint32_t q[NT][G][QP][4];
-  float qsum[NT][G][2];   // of columns 2 c and 2 c + 1
+  uint32_t q_kept[NT][G][P][4];  // unless in shared memory
+  const uint32_t queries = steps + (1 + P) * Shape::kSteps + lane * 16;
+  uint32_t qbase[NT][Shape::kBaseMmas][2];  // sums of a group's query elements, in three parts of bfloat16
+  float to_score[NT];     // of column g: what makes a score of its products
   float acc[NT][2 * G][4];
-  float off[NT][G], top[NT], total_p[NT];  // of column g, this thread's tokens
+  float mid[NT][4];       // of group g (and nothing), columns 2 c and 2 c + 1
+  float top[NT], total_p[NT];  // of column g; the weights of this thread's tokens
   int sees[NT];           // tokens that column g sees
+  int power;              // weights are in units of 2^power, as large as the values met
   bool whole = false;     // the item begins with this worker's first step of it
+  // the pairs of groups whose bases this thread has in the products of bases
+  auto base_unit = [&](int m, int half) { return (m * 8 + half * 4 + c) % U; };
 
   auto begin = [&] {
+    const AttendCursor use = *item;
+    power = -120;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = use.tile * kCols + 8 * n + g;
       const bool real = col < use.q.fresh * (int)a.group.d;
       const int token = (int)a.group((uint32_t)col), head = use.h * (int)a.group.d + col - token * (int)a.group.d;
-      const TQ* row = static_cast<const TQ*>(a.queries) + (int64_t)(use.q.first + token) * a.q_token + head * a.q_head;
-      sees[n] = real ? use.q.len - use.q.fresh + token + 1 : INT32_MAX;  // columns without a token ask for no masks
+      const int64_t row = (int64_t)(use.q.first + token) * a.q_token + head * a.q_head;
+      // columns without a token ask for no masks
+      sees[n] = real ? use.q.len - use.q.fresh + token + 1 : INT32_MAX;
       top[n] = -INFINITY;
       total_p[n] = 0.f;
+      float e[G][8], most = 0.f;
 #pragma unroll
       for (int j = 0; j < G; ++j) {
-        float e[8];
         const int at = 32 * j + 8 * c;
-        if (real && a.q_wide && at < a.dim) {
-          Vec<TQ, 8> v;
-          v.template load<true>(row + at);
+        auto get = [&](auto type) {
+          using T = decltype(type);
+          const T* from = static_cast<const T*>(a.queries) + row;
+          if (real && a.q_wide && at < a.dim) {
+            Vec<T, 8> v;
+            v.template load<true>(from + at);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = to_f32(v.x[i]);
-        } else {
+            for (int i = 0; i < 8; ++i) e[j][i] = to_f32(v.x[i]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = real && at + i < a.dim ? to_f32(row[at + i]) : 0.f;
+            for (int i = 0; i < 8; ++i) e[j][i] = real && at + i < a.dim ? to_f32(from[at + i]) : 0.f;
+          }
+        };
+        if (P == 2) get(float{});
+        else if (a.q_type == BPE_F16) get(__half{});
+        else get(__nv_bfloat16{});
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(e[j][i]));
+      }
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+      // the largest element in [2^14, 2^15): elements down to 2^-28 of it are normal halves
+      const int by = min(14 - ((__float_as_int(most) >> 23) - 127), 126);
+      const float scale = power_of_2(max(by, -113));
+      to_score[n] = a.scale * kEven / scale;
+      float sum[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[j][i] *= scale;
+          s += e[j][i];
         }
-        float s = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
         s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-        qsum[n][j][0] = __shfl_sync(0xFFFFFFFFu, s, 8 * c);
-        qsum[n][j][1] = __shfl_sync(0xFFFFFFFFu, s, 8 * c + 4);
+        sum[j] = s * (1.f / kEven);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (kHalf) {
-            const __half2 h = __floats2half2_rn(e[i], e[i + 4]);
-            q[n][j][0][i] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            uint32_t part[QP];
-            split_pair<QP>(e[i], e[i + 4], part);
+          const float f = i & 1 ? kOdd / kEven : 1.f;
+          uint32_t part[P];
+          split_halves<P>(e[j][i] * f, e[j][i + 4] * f, part);
 #pragma unroll
-            for (int p = 0; p < QP; ++p) q[n][j][p][i] = part[p];
-          }
+          for (int p = 0; p < P; ++p) q_kept[n][j][p][i] = part[p];
         }
-        off[n][j] = 0.f;
-#pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][2 * j + s2][i] = 0.f;
+        if (Shape::kQueriesShared)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(queries + (n * G + j) * 512), "r"(q_kept[n][j][0][0]),
+                       "r"(q_kept[n][j][0][1]), "r"(q_kept[n][j][0][2]), "r"(q_kept[n][j][0][3])
+                       : "memory");
       }
+      // the products of bases: part s / U of the sums of groups 2 (s % U) and the next, in place s
+#pragma unroll
+      for (int m = 0; m < Shape::kBaseMmas; ++m) qbase[n][m][0] = qbase[n][m][1] = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x = sum[2 * u], y = 2 * u + 1 < G ? sum[(2 * u + 1) % G] : 0.f;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const int s = p * U + u;
+          uint32_t w;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+          x -= bf16_low(w);
+          y -= bf16_high(w);
+          if (c == s % 4) qbase[n][s / 8][s / 4 % 2] = w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * G; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][j][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mid[n][i] = 0.f;
     }
   };
 
   // ---- a step ----
+  // Its values are added up by themselves and then to those before it: the tensor
+  // cores cut sums off where an addition rounds them, so that a long row of
+  // weights above zero would lose a little at each of its products (f32, 700
+  // tokens: 9e-6 of the result).
   auto step = [&](uint32_t at, uint32_t there, auto partial_tag) {
     constexpr bool kPartial = decltype(partial_tag)::value;
+    constexpr bool kOddGroups = G % 2 == 1;
+    uint32_t q[NT][G][P][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        if (Shape::kQueriesShared) {
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(q[n][j][0][0]), "=r"(q[n][j][0][1]), "=r"(q[n][j][0][2]), "=r"(q[n][j][0][3])
+                       : "r"(queries + (n * G + j) * 512));
+        } else {
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[n][j][p][i] = q_kept[n][j][p][i];
+        }
+      }
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-      const int k0 = tile * 16 + g, k1 = k0 + 8;
-      float s[NT][4] = {};
+      const uint32_t k0 = tile * 16 + g, k1 = k0 + 8;
+      const uint32_t pairs = at + kUnit * Shape::kRow;
+      float s[NT][4];
 #pragma unroll
-      for (int u = 0; u < (G + 1) / 2; ++u) {
-        constexpr bool kOdd = G % 2 == 1;
-        const bool pair = !kOdd || u < G / 2;
-        uint2 w0, w1, p0, p1;
-        const uint32_t codes = at, pairs = at + kUnit * Shape::kRow;
-        if (pair) {
-          w0 = lds64(codes + k0 * Shape::kRow + attend_piece<G>(k0, u) * 32 + c * 8);
-          w1 = lds64(codes + k1 * Shape::kRow + attend_piece<G>(k1, u) * 32 + c * 8);
-        } else {
-          w0.x = lds32(codes + k0 * Shape::kRow + u * 32 + c * 4);
-          w1.x = lds32(codes + k1 * Shape::kRow + u * 32 + c * 4);
+      for (int m = 0; m < Shape::kBaseMmas; ++m) {
+        uint32_t b[4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1 && 4 % U == 0) {  // the same pair of groups again
+            b[2] = b[0];
+            b[3] = b[1];
+            break;
+          }
+          const int u = base_unit(m, half);
+          if (!kOddGroups) {
+            const uint2 x = lds64(pairs + k0 * Shape::kPair + u * 8), y = lds64(pairs + k1 * Shape::kPair + u * 8);
+            b[2 * half] = __byte_perm(x.x, x.y, 0x7632);
+            b[2 * half + 1] = __byte_perm(y.x, y.y, 0x7632);
+          } else {
+            const uint32_t x = lds32(pairs + k0 * Shape::kPair + u * 8), y = lds32(pairs + k1 * Shape::kPair + u * 8);
+            uint32_t x2 = 0, y2 = 0;
+            if (u + 1 < U) {
+              x2 = lds32(pairs + k0 * Shape::kPair + u * 8 + 4);
+              y2 = lds32(pairs + k1 * Shape::kPair + u * 8 + 4);
+            }
+            b[2 * half] = __byte_perm(x, x2, 0x7632);
+            b[2 * half + 1] = __byte_perm(y, y2, 0x7632);
+          }
         }
-        if (!kOdd) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (m == 0) mma_bf16_first(s[n], b, qbase[n][m][0], qbase[n][m][1]);
+          else mma_bf16(s[n], b, qbase[n][m][0], qbase[n][m][1]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool pair = !kOddGroups || u < G / 2;
+        uint2 w0 = {}, w1 = {}, p0 = {}, p1 = {};
+        if (pair) {
+          w0 = lds64(at + k0 * Shape::kRow + attend_piece<G>(k0, u) * 32 + c * 8);
+          w1 = lds64(at + k1 * Shape::kRow + attend_piece<G>(k1, u) * 32 + c * 8);
+        } else {
+          w0.x = lds32(at + k0 * Shape::kRow + u * 32 + c * 4);
+          w1.x = lds32(at + k1 * Shape::kRow + u * 32 + c * 4);
+        }
+        if (!kOddGroups) {
           p0 = lds64(pairs + k0 * Shape::kPair + u * 8);
           p1 = lds64(pairs + k1 * Shape::kPair + u * 8);
         } else {
@@ -419,34 +634,26 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
           const int j = 2 * u + half;
           if (j >= G) break;
           const uint32_t x0 = half ? w0.y : w0.x, x1 = half ? w1.y : w1.x;
-          const uint32_t y0 = half ? p0.y : p0.x, y1 = half ? p1.y : p1.x;
-          const float s0 = 16.f * bf16_low(y0), s1 = 16.f * bf16_low(y1);
-          const float b0 = bf16_high(y0) - s0, b1 = bf16_high(y1) - s1;
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            lo[2 * i] = codes_to_floats<kHalf>(x0, i);
-            lo[2 * i + 1] = codes_to_floats<kHalf>(x1, i);
-            hi[2 * i] = codes_to_floats<kHalf>(x0, i + 2);
-            hi[2 * i + 1] = codes_to_floats<kHalf>(x1, i + 2);
-          }
+          const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
+          const float s0 = bf16_low(half ? p0.y : p0.x), s1 = bf16_low(half ? p1.y : p1.x);
+          const uint32_t lo[4] = {codes_even<P, 0>(x0), codes_even<P, 0>(x1), codes_odd<P, 0>(x0), codes_odd<P, 0>(x1)};
+          const uint32_t hi[4] = {codes_even<P, 0>(z0), codes_even<P, 0>(z1), codes_odd<P, 0>(z0), codes_odd<P, 0>(z1)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            float d[4];
+            mma_f16_first(d, lo, q[n][j][P - 1][0], q[n][j][P - 1][1]);
+            mma_f16(d, hi, q[n][j][P - 1][2], q[n][j][P - 1][3]);
+            if (P == 2) {  // leading parts by themselves
+              float d0[4], d1[4];
+              mma_f16_first(d0, lo, q[n][j][0][0], q[n][j][0][1]);
+              mma_f16_first(d1, hi, q[n][j][0][2], q[n][j][0][3]);
 #pragma unroll
-            for (int p = 0; p < QP; ++p) {
-              if (kHalf) {
-                mma_f16(d, lo, q[n][j][p][0], q[n][j][p][1]);
-                mma_f16(d, hi, q[n][j][p][2], q[n][j][p][3]);
-              } else {
-                mma_bf16(d, lo, q[n][j][p][0], q[n][j][p][1]);
-                mma_bf16(d, hi, q[n][j][p][2], q[n][j][p][3]);
-              }
+              for (int i = 0; i < 4; ++i) d[i] += d0[i] + d1[i];
             }
-            s[n][0] += s0 * d[0] + b0 * qsum[n][j][0];
-            s[n][1] += s0 * d[1] + b0 * qsum[n][j][1];
-            s[n][2] += s1 * d[2] + b1 * qsum[n][j][0];
-            s[n][3] += s1 * d[3] + b1 * qsum[n][j][1];
+            s[n][0] += s0 * d[0];
+            s[n][1] += s0 * d[1];
+            s[n][2] += s1 * d[2];
+            s[n][3] += s1 * d[3];
           }
         }
       }
@@ -456,6 +663,26 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
         asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + k0 * 32), "f"(s[n][0]), "f"(s[n][1]) : "memory");
         asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + k1 * 32), "f"(s[n][2]), "f"(s[n][3]) : "memory");
       }
+    }
+    // the pairs of values of token `lane`, meanwhile
+    const uint32_t codes = at + Shape::kHalfStage, value_pairs = codes + kUnit * Shape::kRow + lane * Shape::kPair;
+    uint32_t z[G];
+    if (!kOddGroups) {
+#pragma unroll
+      for (int u = 0; u < G / 2; ++u) {
+        const uint2 x = lds64(value_pairs + u * 8);
+        z[2 * u] = x.x;
+        z[(2 * u + 1) % G] = x.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < G; ++j) z[j] = lds32(value_pairs + j * 4);
+    }
+    float size = 0.f;  // of what they stand for
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
+      if (!kPartial || most < INFINITY) size = fmaxf(size, most);
     }
     __syncwarp();
     // from here on a thread has column g and tokens c, c + 4, .. of the step
@@ -469,9 +696,9 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
       float m = top[n];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[n][i] = a.scale * __uint_as_float(lds32(scores + n * (kUnit * 32) + (c + 4 * i) * 32 + g * 4));
+        p[n][i] = to_score[n] * __uint_as_float(lds32(scores + n * (kUnit * 32) + (c + 4 * i) * 32 + g * 4));
         if (kPartial) {
-          const bool see = use.u * kUnit + c + 4 * i < sees[n] && (there >> (c + 4 * i) & 1);
+          const bool see = u * kUnit + c + 4 * i < sees[n] && (there >> (c + 4 * i) & 1);
           if (see) seen[n] |= 1u << i;
           else p[n][i] = -INFINITY;
         }
@@ -489,8 +716,8 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
         top[n] = most[n];
         total_p[n] *= f;
         const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * c), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * c + 4);
-#pragma unroll
-        for (int j = 0; j < G; ++j) off[n][j] *= f;
+        mid[n][0] *= f0;
+        mid[n][1] *= f1;
 #pragma unroll
         for (int j = 0; j < 2 * G; ++j) {
           acc[n][j][0] *= f0;
@@ -500,77 +727,208 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
         }
       }
     }
+    // weights of at most 2^7: those down to 2^-21 of the largest are normal halves
+    uint32_t ph[NT][P][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float m = top[n] == -INFINITY ? 0.f : top[n];
+      const float m = (top[n] == -INFINITY ? 0.f : top[n]) - 7.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         p[n][i] = exp2_fast(p[n][i] - m);
         total_p[n] += p[n][i];
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t part[P];
+        split_halves<P>(p[n][2 * i], p[n][2 * i + 1], part);
+#pragma unroll
+        for (int k = 0; k < P; ++k) ph[n][k][i] = part[k];
+      }
     }
-    const uint32_t codes = at + Shape::kHalfStage, pairs = codes + kUnit * Shape::kRow;
-    const uint32_t select = g & 1 ? 0x7632 : 0x5410;
+
+    // Values by the tokens of `mask`: with one unit for all of them, and all of the step's at once, but
+    // where some columns see tokens that others do not and whose values are far larger, which would leave
+    // those nothing of theirs.
+    auto values = [&](uint32_t mask) {
+      const bool mine = !kPartial || (mask >> lane & 1);
+      const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, mine ? __float_as_uint(size) : 0u);
+      const int need = max((int)(largest >> 23) - 127 - 7, -120);
+      if (need > power) {
+        const float f = power - need < -126 ? 0.f : power_of_2(power - need);
+        power = need;
 #pragma unroll
-    for (int tile = 0; tile < 2; ++tile) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int u = 0; u < (G + 1) / 2; ++u) {
-        constexpr bool kOdd = G % 2 == 1;
-        const bool pair = !kOdd || u < G / 2;
-        uint2 w[4], y[4];
+          for (int j = 0; j < 2 * G; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = tile * 16 + c + 4 * i;
-          if (pair) w[i] = lds64(codes + t * Shape::kRow + attend_piece<G>(t, u) * 32 + (g >> 1) * 8);
-          else w[i].x = lds32(codes + t * Shape::kRow + u * 32 + (g >> 1) * 4);
-          if (!kOdd) {
-            y[i] = lds64(pairs + t * Shape::kPair + u * 8);
-          } else {
-            y[i].x = lds32(pairs + t * Shape::kPair + u * 8);
-            if (pair) y[i].y = lds32(pairs + t * Shape::kPair + u * 8 + 4);
+            for (int i = 0; i < 4; ++i) acc[n][j][i] *= f;
+          mid[n][0] *= f;
+          mid[n][1] *= f;
+        }
+      }
+      const float unit = power_of_2(-power), middle = P == 2 || a.centre ? 8.f : 0.f;
+      // in the order of a thread's tokens: c, c + 4, c + 8, c + 12 of each half of the step are neighbours
+      const uint32_t place = ((lane & 16) | (lane & 3) << 2 | (lane >> 2 & 3)) * 2;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const float st = bf16_low(z[j]), ba = bf16_high(z[j]);
+        float m = (ba + middle * st) * unit, w = st * unit;
+        if (kPartial) {
+          // what is no number comes in with the steps, by the weights of those that see it
+          const bool good = mine && fabsf(ba) + 16.f * st < INFINITY;
+          m = good ? m : 0.f;
+          w = good ? w : mine ? NAN : 0.f;
+        }
+        const uint32_t to = steps + j * (kUnit * 2) + place;
+        const __half wh = __float2half_rn(w), mh = __float2half_rn(m);
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__half_as_ushort(wh)) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + Shape::kSteps), "h"(__half_as_ushort(mh)) : "memory");
+        if (P == 2) {
+          const __half ml = __float2half_rn(m - __half2float(mh));
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * Shape::kSteps), "h"(__half_as_ushort(ml)) : "memory");
+        }
+      }
+      __syncwarp();
+      float om[NT][4];
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        const uint32_t row = steps + Shape::kSteps + (G < 8 ? min(g, G - 1) : g) * (kUnit * 2) + tile * 32 + c * 8;
+        const uint2 x = lds64(row);
+        const uint32_t lead[4] = {x.x, 0u, x.y, 0u};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (tile == 0 && k == 0) mma_f16_first(om[n], lead, ph[n][k][2 * tile], ph[n][k][2 * tile + 1]);
+            else mma_f16(om[n], lead, ph[n][k][2 * tile], ph[n][k][2 * tile + 1]);
+          }
+        if (P == 2) {
+          const uint2 y = lds64(row + Shape::kSteps);
+          const uint32_t rest[4] = {y.x, 0u, y.y, 0u};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(om[n], rest, ph[n][0][2 * tile], ph[n][0][2 * tile + 1]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mid[n][0] += om[n][0];
+        mid[n][1] += om[n][1];
+      }
+      const uint32_t select = g & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float o[NT][4][4];
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          const bool pair = !kOddGroups || u < G / 2;
+          uint2 w[4] = {};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t t = tile * 16 + c + 4 * i;
+            if (pair) w[i] = lds64(codes + t * Shape::kRow + attend_piece<G>(t, u) * 32 + (g >> 1) * 8);
+            else w[i].x = lds32(codes + t * Shape::kRow + u * 32 + (g >> 1) * 4);
+          }
+          uint32_t b0[NT][2][P], b1[NT][2][P];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int j = 2 * u + half;
+            if (j >= G) break;
+            const uint2 st = lds64(steps + j * (kUnit * 2) + tile * 32 + c * 8);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (P == 1) {
+                const __half2 w0 = __hmul2(*reinterpret_cast<const __half2*>(&ph[n][0][2 * tile]),
+                                           *reinterpret_cast<const __half2*>(&st.x));
+                const __half2 w1 = __hmul2(*reinterpret_cast<const __half2*>(&ph[n][0][2 * tile + 1]),
+                                           *reinterpret_cast<const __half2*>(&st.y));
+                b0[n][half][0] = *reinterpret_cast<const uint32_t*>(&w0);
+                b1[n][half][0] = *reinterpret_cast<const uint32_t*>(&w1);
+              } else {
+                const float2 s0 = unpack_halves(st.x), s1 = unpack_halves(st.y);
+                split_halves<P>(p[n][4 * tile] * s0.x, p[n][4 * tile + 1] * s0.y, b0[n][half]);
+                split_halves<P>(p[n][4 * tile + 2] * s1.x, p[n][4 * tile + 3] * s1.y, b1[n][half]);
+              }
+              if (kPartial) {  // whatever the steps of tokens are that a column does not see
+                const uint32_t bits = seen[n] >> (4 * tile);
+                const uint32_t m0 = (bits & 1 ? 0xFFFFu : 0u) | (bits & 2 ? 0xFFFF0000u : 0u);
+                const uint32_t m1 = (bits & 4 ? 0xFFFFu : 0u) | (bits & 8 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                  b0[n][half][k] &= m0;
+                  b1[n][half][k] &= m1;
+                }
+              }
+            }
+            const uint32_t x0 = __byte_perm(half ? w[0].y : w[0].x, half ? w[1].y : w[1].x, select);
+            const uint32_t x1 = __byte_perm(half ? w[2].y : w[2].x, half ? w[3].y : w[3].x, select);
+            const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
+            const uint32_t lo[4] = {codes_even<P, 8>(x0), codes_odd<P, 8>(x0), codes_even<P, 8>(x1), codes_odd<P, 8>(x1)};
+            const uint32_t hi[4] = {codes_even<P, 8>(z0), codes_odd<P, 8>(z0), codes_even<P, 8>(z1), codes_odd<P, 8>(z1)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              auto add = [&](float (&d)[4], const uint32_t (&codes)[4], int k) {
+                if (tile == 0) mma_f16_first(d, codes, b0[n][half][k], b1[n][half][k]);
+                else mma_f16(d, codes, b0[n][half][k], b1[n][half][k]);
+              };
+              add(o[n][2 * half], lo, P - 1);
+              add(o[n][2 * half + 1], hi, P - 1);
+              if (P == 2) {  // leading parts by themselves
+                float lead[2][4];
+                mma_f16_first(lead[0], lo, b0[n][half][0], b1[n][half][0]);
+                mma_f16_first(lead[1], hi, b0[n][half][0], b1[n][half][0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  o[n][2 * half][i] += lead[0][i];
+                  o[n][2 * half + 1][i] += lead[1][i];
+                }
+              }
+            }
+          }
+          if (P == 1 && a.centre) {  // n to n - 8
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (4 * u + i < 2 * G) mma_f16(o[n][i], minus8, b0[n][i / 2][0], b1[n][i / 2][0]);
           }
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int j = 2 * u + half;
-          if (j >= G) break;
-          const uint32_t x0 = __byte_perm(half ? w[0].y : w[0].x, half ? w[1].y : w[1].x, select);
-          const uint32_t x1 = __byte_perm(half ? w[2].y : w[2].x, half ? w[3].y : w[3].x, select);
-          uint32_t v[2][4];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int s2 = 0; s2 < 2; ++s2) {
-            v[s2][0] = codes_to_floats<false>(x0, 2 * s2);
-            v[s2][1] = codes_to_floats<false>(x0, 2 * s2 + 1);
-            v[s2][2] = codes_to_floats<false>(x1, 2 * s2);
-            v[s2][3] = codes_to_floats<false>(x1, 2 * s2 + 1);
-          }
-          float st[4], ba[4];
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t z = half ? y[i].y : y[i].x;
-            st[i] = 16.f * bf16_low(z);
-            ba[i] = bf16_high(z) - st[i];
-          }
+            for (int e = 0; e < 4; ++e)
+              if (4 * u + i < 2 * G) acc[n][4 * u + i][e] += o[n][i][e];
+      }
+    };
+    if (!kPartial) {
+      values(0xFFFFFFFFu);
+    } else {
+      int least = INT32_MAX, furthest = 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float wt[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w1 = p[n][4 * tile + i];
-              wt[i] = w1 * st[i];
-              float b = w1 * ba[i];
-              if (kPartial && !(seen[n] >> (4 * tile + i) & 1)) wt[i] = b = 0.f;  // whatever is stored there
-              off[n][j] += b;
-            }
-            uint32_t b0[PP], b1[PP];
-            split_pair<PP>(wt[0], wt[1], b0);
-            split_pair<PP>(wt[2], wt[3], b1);
-#pragma unroll
-            for (int k = 0; k < PP; ++k) {
-              mma_bf16(acc[n][2 * j], v[0], b0[k], b1[k]);
-              mma_bf16(acc[n][2 * j + 1], v[1], b0[k], b1[k]);
-            }
-          }
+      for (int n = 0; n < NT; ++n) {
+        least = min(least, sees[n]);
+        if (sees[n] != INT32_MAX) furthest = max(furthest, sees[n]);
+      }
+      auto first_tokens = [&](int limit) {
+        const int k = limit - u * kUnit;
+        return k >= kUnit ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
+      };
+      const uint32_t all = there & first_tokens(__reduce_max_sync(0xFFFFFFFFu, furthest));
+      const uint32_t common = all & first_tokens(__reduce_min_sync(0xFFFFFFFFu, least));
+      const bool counts = (all >> lane & 1) && size > 0.f;
+      const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, counts ? __float_as_uint(size) : 0u);
+      const uint32_t smallest = __reduce_min_sync(0xFFFFFFFFu, counts ? __float_as_uint(size) : 0xFFFFFFFFu);
+      if (common == all || largest <= smallest || largest - smallest < (8u << 23)) {
+        values(all);
+      } else {
+        uint32_t left = all & ~common, now = common;
+        while (true) {  // at most 33 times
+          if (now) values(now);
+          __syncwarp();
+          if (!left) break;
+          now = left & (0u - left);
+          left &= left - 1;
         }
       }
     }
@@ -578,8 +936,10 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
 
   // ---- an item's end, or the end of this worker's share of it ----
   auto finish = [&](bool last) {
+    const AttendCursor use = *item;
     const bool done = whole && last;
     float* part = a.partial + (2 * me + (whole ? 1 : 0)) * Shape::kPartial;
+    const float unit = power_of_2(power);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float l = total_p[n];
@@ -590,36 +950,29 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
         part[kCols * (32 * G + 1) + 8 * n + g] = l;
       }
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
-        off[n][j] += __shfl_xor_sync(0xFFFFFFFFu, off[n][j], 1);
-        off[n][j] += __shfl_xor_sync(0xFFFFFFFFu, off[n][j], 2);
-      }
-#pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int from_lane = 8 * c + 4 * e;
-        const float sum_p = __shfl_sync(0xFFFFFFFFu, l, from_lane);
-        const float by = sum_p == 0.f ? 0.f : 1.f / sum_p;
+        const float sum_p = __shfl_sync(0xFFFFFFFFu, l, 8 * c + 4 * e);
+        const float by = sum_p == 0.f ? 0.f : unit / sum_p;
         const int col = use.tile * kCols + 8 * n + 2 * c + e;
         const bool real = col < use.q.fresh * (int)a.group.d;
         const int token = (int)a.group((uint32_t)col), head = use.h * (int)a.group.d + col - token * (int)a.group.d;
         const int64_t row = (int64_t)(use.q.first + token) * a.o_token + head * a.o_head;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const float o = __shfl_sync(0xFFFFFFFFu, off[n][j], from_lane);
-          float4 r = make_float4(acc[n][2 * j][e] + o, acc[n][2 * j][2 + e] + o, acc[n][2 * j + 1][e] + o,
-                                 acc[n][2 * j + 1][2 + e] + o);
-          if (!done) {
-            *reinterpret_cast<float4*>(part + (8 * n + 2 * c + e) * 32 * G + 32 * j + 4 * g) = r;
-          } else if (real) {
-            r.x *= by, r.y *= by, r.z *= by, r.w *= by;
-            attend_store(a, row, 32 * j + 4 * g, r);
-          }
+          const float m = __shfl_sync(0xFFFFFFFFu, mid[n][e], 4 * j + c);
+          float4 r = make_float4(acc[n][2 * j][e] * kEven + m, acc[n][2 * j][2 + e] * kOdd + m,
+                                 acc[n][2 * j + 1][e] * kEven + m, acc[n][2 * j + 1][2 + e] * kOdd + m);
+          const float f = done ? by : unit;
+          r.x *= f, r.y *= f, r.z *= f, r.w *= f;
+          if (!done) *reinterpret_cast<float4*>(part + (8 * n + 2 * c + e) * 32 * G + 32 * j + 4 * g) = r;
+          else if (real) attend_store(a, row, 32 * j + 4 * g, r);
         }
       }
     }
     if (!done && lane == 0) {
       // the workers among which the item's steps lie
-      const int64_t i0 = from + passed - use.u, i1 = i0 + use.units - 1;
+      const int64_t total = upto[kThreads], workers = min((int64_t)gridDim.x * kWarps, total);
+      const int64_t i0 = total * me / workers + place - u, i1 = i0 + use.units - 1;
       a.record[2 * me + (whole ? 1 : 0)] =
           make_int4((int)(((i0 + 1) * workers - 1) / total), (int)(((i1 + 1) * workers - 1) / total), use.r,
                     use.h * use.tiles + use.tile);
@@ -627,20 +980,14 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
   };
   look_up();
   uint32_t there = copy(0), there_next = 0;
-  if (count > 1) {
-    attend_next<kCols>(a, ahead);
-    look_up();
-  }
+  step_ahead();
   begin();
-  whole = use.u == 0;
-  for (; passed < count; ++passed) {
-    const int stage = passed & 1;
-    if (passed + 1 < count) {
+  whole = u == 0;
+  for (int stage = 0;; stage ^= 1) {
+    const bool more = ahead_place < count;
+    if (more) {
       there_next = copy(stage ^ 1);
-      if (passed + 2 < count) {
-        attend_next<kCols>(a, ahead);
-        look_up();
-      }
+      step_ahead();
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -648,19 +995,23 @@ __global__ void __launch_bounds__(kAttThreads, (G <= 4 && NT == 1 && sizeof(TQ) 
     __syncwarp();
     bool part = there != 0xFFFFFFFFu;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) part |= sees[n] < (use.u + 1) * kUnit;
+    for (int n = 0; n < NT; ++n) part |= sees[n] < (u + 1) * kUnit;
     if (__any_sync(0xFFFFFFFFu, part)) step(ring + stage * Shape::kStage, there, std::true_type{});
     else step(ring + stage * Shape::kStage, there, std::false_type{});
     __syncwarp();  // before the stage is filled again
     there = there_next;
-    const bool last = use.u + 1 == use.units;
-    if (last || passed + 1 == count) finish(last);
-    if (passed + 1 < count) {
-      attend_next<kCols>(a, use);
-      if (last) {
-        begin();
-        whole = true;
-      }
+    const bool last = u + 1 == units;
+    if (last || !more) finish(last);
+    if (!more) return;
+    ++place;
+    ++u;
+    if (last) {
+      place += kItemCost;
+      next_item(item);
+      u = 0;
+      units = item->units;
+      begin();
+      whole = true;
     }
   }
 }
@@ -774,7 +1125,7 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
     const int64_t groups = cache_groups(p.dim);
-    const size_t records = align256((size_t)h->n_sms * 2 * kAttWarps * 2 * sizeof(int4));
+    const size_t records = align256((size_t)h->n_sms * kAttMaxWarps * 2 * sizeof(int4));
     rc = ensure_ws(h, records + (size_t)h->n_sms * BPE_ATTEND_PARTIALS * (32 * groups + 2) * sizeof(float), st);
     if (rc) return rc;
     auto fits = [&](const void* q, int64_t token, int64_t head, int64_t size, int64_t V) {
@@ -783,7 +1134,7 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
     };
     // absent tokens are zeros copied from nowhere, but from an address that is one
     const void* cache = p.cache ? p.cache : h->d_ws;
-    AttendArgs a{p.queries, p.out, p.out_type, p.query_token_stride, p.query_head_stride, p.out_token_stride,
+    AttendArgs a{p.queries, p.out, p.query_type, p.out_type, p.query_token_stride, p.query_head_stride, p.out_token_stride,
                  p.out_head_stride, p.n_tokens, (int)p.n_heads, (int)p.dim, FastDiv(p.group),
                  static_cast<const unsigned char*>(cache), p.n_blocks, p.block_stride,
                  cache_page_bytes(p.block_size, p.dim), FastDiv(p.block_size), p.table, p.table_stride,
@@ -791,32 +1142,33 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
                  p.scale * 1.4426950408889634f,
                  fits(p.queries, p.query_token_stride, p.query_head_stride, type_size(p.query_type), 8),
                  fits(p.out, p.out_token_stride, p.out_head_stride, type_size(p.out_type), 4),
+                 p.query_type != BPE_BF16 || p.out_type != BPE_BF16,
+                 std::max(p.block_stride, 2 * p.n_heads * cache_page_bytes(p.block_size, p.dim)) / 16 <=
+                     (int64_t)UINT32_MAX / std::max<int64_t>(1, p.n_blocks),
                  reinterpret_cast<float*>(static_cast<char*>(h->d_ws) + records), static_cast<int4*>(h->d_ws), h->d_small};
     // 16 columns share the work on a code; a request with at most 8 has no use for the second half
     const bool wide = p.query_type != BPE_F32 &&
                       (p.offsets ? p.n_tokens * p.group > 8 * p.n_requests : p.group > 8);
     return with_groups(groups, [&](auto gs) {
-      return with_type(p.query_type, [&](auto tq) -> int {
-        constexpr int G = decltype(gs)::value;
-        using TQ = decltype(tq);
-        auto launch = [&](auto nt) -> int {
-          constexpr int NT = decltype(nt)::value;
-          constexpr int kSmem = AttendShape<G, 1, NT>::kSmem;
-          constexpr int kBlocks = (G <= 4 && NT == 1 && sizeof(TQ) == 2) ? 2 : 1;
-          int ok = once_per_device(h->device, [&] {
-            return cudaFuncSetAttribute(k_attend<TQ, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-          });
-          if (ok) return ok;
-          const unsigned blocks = (unsigned)h->n_sms * kBlocks;
-          k_attend<TQ, G, NT><<<blocks, kAttThreads, kSmem, st>>>(a);
-          CK(cudaGetLastError());
-          CK(launch_after(k_attend_join<G, NT>, dim3(blocks * kAttWarps - 1), kJoinThreads, 0, st, a));
-          return BPE_OK;
-        };
-        if constexpr (sizeof(TQ) == 2)
-          if (wide) return launch(std::integral_constant<int, 2>{});
-        return launch(std::integral_constant<int, 1>{});
-      });
+      constexpr int G = decltype(gs)::value;
+      auto launch = [&](auto parts, auto nt) -> int {
+        constexpr int P = decltype(parts)::value, NT = decltype(nt)::value;
+        constexpr int kSmem = AttendShape<G, P, NT>::kSmem;
+        int ok = once_per_device(h->device, [&] {
+          return cudaFuncSetAttribute(k_attend<P, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        });
+        if (ok) return ok;
+        using Shape = AttendShape<G, P, NT>;
+        const unsigned blocks = (unsigned)(h->n_sms * Shape::kBlocks);
+        k_attend<P, G, NT><<<blocks, Shape::kThreads, kSmem, st>>>(a);
+        CK(cudaGetLastError());
+        CK(launch_after(k_attend_join<G, NT>, dim3(blocks * Shape::kWarps - 1), kJoinThreads, 0, st, a));
+        return BPE_OK;
+      };
+      constexpr std::integral_constant<int, 1> one{};
+      constexpr std::integral_constant<int, 2> two{};
+      if (p.query_type == BPE_F32) return launch(two, one);
+      return wide ? launch(one, two) : launch(one, one);
     });
   });
 }
