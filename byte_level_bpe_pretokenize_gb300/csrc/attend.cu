@@ -1,5 +1,7 @@
-// Attention over a paged cache in 4 bits (attend.cuh). A translation unit of
-// its own: its kernels take longest to compile.
+// Attention over a paged cache in 4 bits: single tokens and short runs of new
+// ones (attend.cuh), long runs (attend_wide.cuh), and what chooses between them
+// (attend_entry.cuh). A translation unit of its own: its kernels take longest to
+// compile.
 
 #include <cmath>
 
@@ -7,3 +9,5 @@
 #include "vec.cuh"
 #include "cache.cuh"
 #include "attend.cuh"
+#include "attend_wide.cuh"
+#include "attend_entry.cuh"

@@ -19,6 +19,7 @@ namespace {
 constexpr int kUnit = 32;      // tokens of a step
 constexpr int kItemCost = 3;   // what beginning and ending an item takes, in steps
 constexpr int kAttMaxWarps = 16;  // workers of an SM
+constexpr int kWideMin = 64;      // columns of a request from which attend_wide.cuh takes it
 
 struct AttendArgs {
   const void* queries;
@@ -42,6 +43,7 @@ struct AttendArgs {
   bool near;              // the cache lies within 2^32 times 16 bytes
   float* partial;
   int4* record;
+  const int* redo;        // requests of kWideMin columns on that are computed here all the same; null: all of them
   DevSmall* small;
 };
 
@@ -58,6 +60,13 @@ __device__ __forceinline__ AttendRequest attend_request(const AttendArgs& a, int
   q.fresh = ok ? (int)(end - first) : 0;
   if (!fits) q.len = 0;
   if (report && !(ok && fits)) atomicOr(&a.small->op_status, kStBadInput);
+  return q;
+}
+
+// The request as far as it is computed here.
+__device__ __forceinline__ AttendRequest attend_mine(const AttendArgs& a, int r, bool report) {
+  AttendRequest q = attend_request(a, r, report);
+  if (a.redo && (int64_t)q.fresh * a.group.d >= kWideMin && !__ldg(a.redo + r)) q.fresh = 0;
   return q;
 }
 
@@ -183,7 +192,7 @@ __device__ __forceinline__ void attend_sizes(const AttendArgs& a, AttendCursor& 
 template <int kCols>
 __device__ __forceinline__ int64_t attend_units(const AttendArgs& a, int r, bool report) {
   AttendCursor c;
-  c.q = attend_request(a, r, report);
+  c.q = attend_mine(a, r, report);
   attend_sizes<kCols>(a, c);
   return (int64_t)(c.units + kItemCost) * c.tiles * a.heads;
 }
@@ -198,7 +207,7 @@ __device__ __forceinline__ void attend_next(const AttendArgs& a, AttendCursor& c
   do {
     ++c.r;
     c.q.fresh = 0;
-    if (c.r < a.n) c.q = attend_request(a, c.r, false);
+    if (c.r < a.n) c.q = attend_mine(a, c.r, false);
   } while (c.q.fresh == 0 && c.r < a.n);
   attend_sizes<kCols>(a, c);
 }
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
       rest -= __shfl_sync(0xFFFFFFFFu, s, 31);
     }
     use.r = min(r, a.n - 1);
-    use.q = attend_request(a, use.r, false);
+    use.q = attend_mine(a, use.r, false);
     attend_sizes<kCols>(a, use);
     const int64_t before = rest / (use.units + kItemCost);
     units = use.units;
@@ -1017,160 +1026,112 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
 }
 
 // Adds up the partial sums of items that lie in several workers' shares, in the
-// order of the shares. Block b looks at the border between workers b and b + 1;
-// of an item that spans k borders each of their blocks takes columns.
+// order of the shares or by a fixed tree. Block b looks at the border between
+// workers b and b + 1; of an item that spans k borders each of their blocks takes
+// columns. With few parts a thread reads all parts of its four elements; with
+// many, parts are spread over the threads, their factors first.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinFew = 8;
 template <int G, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
   using Shape = AttendShape<G, 1, NT>;
   constexpr int kCols = Shape::kCols, kVecs = 8 * G;  // vectors of 4 of a column
-  __shared__ float4 part_sum[kJoinThreads];
-  __shared__ float part_total[kJoinThreads];
+  constexpr int kTop = kCols * 32 * G, kTotal = kTop + kCols;
   await_previous();
   const int64_t b = blockIdx.x + 1;
   const int4 rec = a.record[2 * b];
   if (rec.x < 0) return;
   const int w0 = rec.x, w1 = rec.y, parts = w1 - w0 + 1;
-  const AttendRequest q = attend_request(a, rec.z, false);
   AttendCursor cur;
-  cur.q = q;
+  cur.q = attend_mine(a, rec.z, false);
   attend_sizes<kCols>(a, cur);
   const int h = rec.w / cur.tiles, tile = rec.w - h * cur.tiles, group = (int)a.group.d;
-  const int cols = min(kCols, q.fresh * group - tile * kCols);
-  // this block's columns, and for each of its vectors as many threads as there are
-  const int first = (int)b - w0 - 1, step = w1 - w0;
-  if (first >= cols) return;
-  const int mine = (cols - first + step - 1) / step;
-  const int slices = max(1, min(parts, kJoinThreads / (mine * kVecs)));
-  const int lanes = min(mine * kVecs, kJoinThreads);
-  for (int base = 0; base < mine * kVecs; base += lanes) {
-    const int slice = threadIdx.x / lanes, item = base + threadIdx.x % lanes;
-    const bool here = slice < slices && item < mine * kVecs;
-    const int col = first + (item / kVecs) * step, at = 4 * (item % kVecs);
-    auto slot = [&](int k) { return a.partial + (2 * (int64_t)(w0 + k) + (k == 0 ? 1 : 0)) * Shape::kPartial; };
-    float top = -INFINITY;
-    if (here)
-#pragma unroll 8
-      for (int k = 0; k < parts; ++k) top = fmaxf(top, slot(k)[kCols * 32 * G + col]);
-    const float m = top == -INFINITY ? 0.f : top;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 0.f;
-    if (here)
-#pragma unroll 4
-      for (int k = slice; k < parts; k += slices) {
-        const float* p = slot(k);
-        const float f = exp2_fast(p[kCols * 32 * G + col] - m);
-        const float4 v = *reinterpret_cast<const float4*>(p + col * 32 * G + at);
-        sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
-        total += f * p[kCols * (32 * G + 1) + col];
+  const int cols = min(kCols, cur.q.fresh * group - tile * kCols);
+  // this block's columns
+  const int first = (int)b - w0 - 1, step = w1 - w0, tid = threadIdx.x;
+  auto part = [&](int k) { return a.partial + (2 * (int64_t)(w0 + k) + (k == 0 ? 1 : 0)) * Shape::kPartial; };
+  auto put = [&](int col, int vec, float4 sum, float total) {
+    const float by = total == 0.f ? 0.f : 1.f / total;
+    sum.x *= by, sum.y *= by, sum.z *= by, sum.w *= by;
+    const int at = tile * kCols + col, token = at / group, head = h * group + at - token * group;
+    attend_store(a, (int64_t)(cur.q.first + token) * a.o_token + head * a.o_head, 4 * vec, sum);
+  };
+  auto add = [](float4& sum, float f, const float* from) {
+    const float4 v = *reinterpret_cast<const float4*>(from);
+    sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
+  };
+  if (parts <= kJoinFew) {
+    const int mine = (cols - first + step - 1) / step;  // none where first >= cols
+    for (int i = tid; i < mine * kVecs; i += kJoinThreads) {
+      const int col = first + i / kVecs * step, vec = i % kVecs;
+      float top[kJoinFew], m = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinFew; ++k) {
+        top[k] = k < parts ? part(k)[kTop + col] : -INFINITY;
+        m = fmaxf(m, top[k]);
       }
-    part_sum[threadIdx.x] = sum;
-    part_total[threadIdx.x] = total;
-    __syncthreads();
-    if (here && slice == 0) {
-      for (int k = 1; k < slices; ++k) {
-        const float4 v = part_sum[threadIdx.x + k * lanes];
-        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        total += part_total[threadIdx.x + k * lanes];
+      if (m == -INFINITY) m = 0.f;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kJoinFew; ++k) {
+        if (k >= parts) break;
+        const float f = exp2_fast(top[k] - m);
+        total += f * part(k)[kTotal + col];
+        add(sum, f, part(k) + col * 32 * G + 4 * vec);
       }
-      const float by = total == 0.f ? 0.f : 1.f / total;
-      sum.x *= by, sum.y *= by, sum.z *= by, sum.w *= by;
-      const int at_col = tile * kCols + col, token = at_col / group, head = h * group + at_col - token * group;
-      attend_store(a, (int64_t)(q.first + token) * a.o_token + head * a.o_head, at, sum);
+      put(col, vec, sum, total);
     }
-    __syncthreads();
+    return;
   }
-}
-
-template <class F>
-int with_groups(int64_t groups, F f) {
-  using std::integral_constant;
-  switch (groups) {
-    case 1: return f(integral_constant<int, 1>{});
-    case 2: return f(integral_constant<int, 2>{});
-    case 3: return f(integral_constant<int, 3>{});
-    case 4: return f(integral_constant<int, 4>{});
-    case 6: return f(integral_constant<int, 6>{});
-    default: return f(integral_constant<int, 8>{});
+  constexpr int kSlices = kJoinThreads / kVecs, kRound = 512;  // parts whose factors are held at once
+  __shared__ float factor[kRound];
+  __shared__ float of_warp[kJoinThreads / 32];
+  __shared__ float4 sums[kJoinThreads];
+  const int slice = tid / kVecs, vec = tid % kVecs;
+  auto all_of = [&](float x, auto join) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = join(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+    __syncthreads();  // of_warp and sums may still be read
+    if (tid % 32 == 0) of_warp[tid / 32] = x;
+    __syncthreads();
+    x = of_warp[0];
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 32; ++w) x = join(x, of_warp[w]);
+    return x;
+  };
+  for (int col = first; col < cols; col += step) {
+    float m = -INFINITY;
+    for (int k = tid; k < parts; k += kJoinThreads) m = fmaxf(m, part(k)[kTop + col]);
+    m = all_of(m, [](float x, float y) { return fmaxf(x, y); });
+    if (m == -INFINITY) m = 0.f;
+    float total = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += kRound) {
+      if (k0) __syncthreads();  // factors may still be read
+      for (int k = k0 + tid; k < min(parts, k0 + kRound); k += kJoinThreads) {
+        const float f = exp2_fast(part(k)[kTop + col] - m);
+        factor[k - k0] = f;
+        total += f * part(k)[kTotal + col];
+      }
+      __syncthreads();
+      if (slice < kSlices) {
+        const int end = min(parts, k0 + kRound);
+#pragma unroll 8
+        for (int k = k0 + slice; k < end; k += kSlices) add(sum, factor[k - k0], part(k) + col * 32 * G + 4 * vec);
+      }
+    }
+    total = all_of(total, [](float x, float y) { return x + y; });
+    sums[tid] = sum;
+    __syncthreads();
+    if (slice == 0) {
+#pragma unroll
+      for (int s = 1; s < kSlices; ++s) {
+        const float4 v = sums[vec + s * kVecs];
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+      }
+      put(col, vec, sum, total);
+    }
   }
 }
 
 }  // namespace
-
-extern "C" {
-
-int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) {
-  return guarded("bpe_attend", [&]() -> int {
-    auto bad = [&](const char* what) { return fail(BPE_ERR_INVALID_ARG, std::string("bpe_attend: ") + what); };
-    if (!h) return bad("null handle");
-    if (!args) return bad("null arguments");
-    const bpe_attend_args& p = *args;
-    int rc = cache_check("bpe_attend", h, p.cache, p.n_blocks, p.block_stride, p.block_size, p.n_heads, p.dim);
-    if (rc) return rc;
-    if (!type_ok(p.query_type) || !type_ok(p.out_type)) return bad("unknown element type");
-    if (p.n_requests < 0 || p.n_requests >= INT32_MAX || p.n_tokens < 0 || p.n_tokens >= INT32_MAX || p.group < 1 ||
-        p.group > 256 || p.n_tokens * p.group >= INT32_MAX / p.n_heads || p.max_blocks < 0 || p.max_blocks > INT32_MAX ||
-        p.query_token_stride < 0 || p.query_head_stride < 0 || p.out_token_stride < 0 || p.out_head_stride < 0)
-      return bad("a size or stride is negative or too large");
-    if (!std::isfinite(p.scale)) return bad("scale is not finite");
-    if (p.n_requests > 1 && p.table_stride < p.max_blocks) return bad("table rows overlap");
-    if (!p.offsets && p.n_tokens < p.n_requests) return bad("n_tokens is below one new token a request");
-    if (p.n_requests == 0 || p.n_tokens == 0) return BPE_OK;
-    if (!p.queries || !p.out || !p.seq_lens || (p.max_blocks > 0 && !p.table)) return bad("null pointer");
-    if (!aligned(p.queries, type_size(p.query_type)) || !aligned(p.out, type_size(p.out_type)) ||
-        !aligned(p.table, 4) || !aligned(p.seq_lens, 4) || !aligned(p.offsets, 8))
-      return bad("a pointer is not aligned to its elements");
-    const int64_t n_rows = p.n_heads * p.group;
-    if (rows_meet(p.n_tokens, p.out_token_stride, n_rows, p.out_head_stride, p.dim)) return bad("output rows overlap");
-    DeviceGuard g(h->device);
-    cudaStream_t st = (cudaStream_t)stream;
-    const int64_t groups = cache_groups(p.dim);
-    const size_t records = align256((size_t)h->n_sms * kAttMaxWarps * 2 * sizeof(int4));
-    rc = ensure_ws(h, records + (size_t)h->n_sms * BPE_ATTEND_PARTIALS * (32 * groups + 2) * sizeof(float), st);
-    if (rc) return rc;
-    auto fits = [&](const void* q, int64_t token, int64_t head, int64_t size, int64_t V) {
-      return p.dim % V == 0 && vec_ok(q, p.n_tokens > 1 ? token : 0, size, V) &&
-             vec_ok(q, n_rows > 1 ? head : 0, size, V);
-    };
-    // absent tokens are zeros copied from nowhere, but from an address that is one
-    const void* cache = p.cache ? p.cache : h->d_ws;
-    AttendArgs a{p.queries, p.out, p.query_type, p.out_type, p.query_token_stride, p.query_head_stride, p.out_token_stride,
-                 p.out_head_stride, p.n_tokens, (int)p.n_heads, (int)p.dim, FastDiv(p.group),
-                 static_cast<const unsigned char*>(cache), p.n_blocks, p.block_stride,
-                 cache_page_bytes(p.block_size, p.dim), FastDiv(p.block_size), p.table, p.table_stride,
-                 std::min<int64_t>(p.max_blocks * p.block_size, INT32_MAX - 2 * kUnit), p.seq_lens, p.offsets, (int)p.n_requests,
-                 p.scale * 1.4426950408889634f,
-                 fits(p.queries, p.query_token_stride, p.query_head_stride, type_size(p.query_type), 8),
-                 fits(p.out, p.out_token_stride, p.out_head_stride, type_size(p.out_type), 4),
-                 p.query_type != BPE_BF16 || p.out_type != BPE_BF16,
-                 std::max(p.block_stride, 2 * p.n_heads * cache_page_bytes(p.block_size, p.dim)) / 16 <=
-                     (int64_t)UINT32_MAX / std::max<int64_t>(1, p.n_blocks),
-                 reinterpret_cast<float*>(static_cast<char*>(h->d_ws) + records), static_cast<int4*>(h->d_ws), h->d_small};
-    // 16 columns share the work on a code; a request with at most 8 has no use for the second half
-    const bool wide = p.query_type != BPE_F32 &&
-                      (p.offsets ? p.n_tokens * p.group > 8 * p.n_requests : p.group > 8);
-    return with_groups(groups, [&](auto gs) {
-      constexpr int G = decltype(gs)::value;
-      auto launch = [&](auto parts, auto nt) -> int {
-        constexpr int P = decltype(parts)::value, NT = decltype(nt)::value;
-        constexpr int kSmem = AttendShape<G, P, NT>::kSmem;
-        int ok = once_per_device(h->device, [&] {
-          return cudaFuncSetAttribute(k_attend<P, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        });
-        if (ok) return ok;
-        using Shape = AttendShape<G, P, NT>;
-        const unsigned blocks = (unsigned)(h->n_sms * Shape::kBlocks);
-        k_attend<P, G, NT><<<blocks, Shape::kThreads, kSmem, st>>>(a);
-        CK(cudaGetLastError());
-        CK(launch_after(k_attend_join<G, NT>, dim3(blocks * Shape::kWarps - 1), kJoinThreads, 0, st, a));
-        return BPE_OK;
-      };
-      constexpr std::integral_constant<int, 1> one{};
-      constexpr std::integral_constant<int, 2> two{};
-      if (p.query_type == BPE_F32) return launch(two, one);
-      return wide ? launch(one, two) : launch(one, one);
-    });
-  });
-}
-
-}  // extern "C"

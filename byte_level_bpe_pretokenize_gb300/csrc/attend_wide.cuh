@@ -1,0 +1,568 @@
+// Attention of long runs of new tokens over a paged cache in 4 bits: the same
+// sums as attend.cuh, on tcgen05 tensor cores.
+//
+// Included once by attend.cu, behind attend.cuh; not a standalone header.
+//
+// A block takes up to 2 x 128 columns (a column: a query head of a new token) of
+// one cache head. Keys and values become halves in shared memory, 128 tokens at
+// a time; scores, weights (as the left factor of the values' product) and
+// results live in tensor memory, a row a column.
+//
+//   scores [128 columns x 128 tokens] = queries x keys^T
+//   results [128 columns x dim] += weights x values
+//
+// A value is a half of its own 2^-12, in units of 2^e that the first 128 tokens
+// give. What does not fit that (an infinity, a NaN, sizes 2^15 apart) marks the
+// request, which attend.cuh then computes again: so masked tokens spoil no
+// column here that may not see them.
+
+namespace {
+
+constexpr int kWideTile = 128;
+constexpr int kWideThreads = 17 * 32;  // two softmax groups of 4 warps, keys' and values' 4 each, one that issues products
+constexpr uint64_t kPatience = 2000000000;  // nanoseconds of a wait, which lasts microseconds
+
+__device__ __forceinline__ void barrier_init(uint32_t at, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(at), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint32_t at) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(at) : "memory");
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Whether the phase of this parity ended; gives up after kPatience or when
+// another thread of the block gave up.
+__device__ __forceinline__ bool barrier_wait(uint32_t at, uint32_t parity, volatile int* gave_up) {
+  uint64_t since = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*gave_up) return false;
+    if (i % 16 == 15) {
+      const uint64_t now = now_ns();
+      if (since == 0) since = now;
+      if (now - since > kPatience) break;
+    }
+  }
+  *gave_up = 1;
+  return false;
+}
+
+// Matrix in shared memory in rows of 128 bytes, swizzled in groups of 8 rows.
+// K-major (a row: 64 elements of the summed dimension): groups of rows are
+// 1024 bytes apart. MN-major (a row: 64 elements of the other one): groups of 8
+// along the sum 1024 bytes, blocks of 64 elements `block` bytes apart.
+__device__ __forceinline__ uint64_t matrix_at(uint32_t at, uint32_t block) {
+  return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void product_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      : "memory");
+}
+// Arrives at a barrier when the products issued so far are done.
+__device__ __forceinline__ void products_done(uint32_t barrier) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(barrier) : "memory");
+}
+
+// 32 columns of a thread's row of tensor memory.
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// What this thread wrote to shared memory is there for the tensor cores.
+__device__ __forceinline__ void publish() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int G>
+struct WideShape {
+  static constexpr int kTiles = G <= 4 ? 2 : 1;   // of 128 columns
+  static constexpr int kStages = G <= 4 ? 2 : 1;  // of 128 tokens
+  static constexpr int kSubs = (G + 1) / 2;       // blocks of 64 elements
+  static constexpr int kSub = kWideTile * 128;    // bytes of one
+  static constexpr int kBytes = kSubs * kSub;     // of 128 rows
+  static constexpr int kDim = 32 * G;
+  static constexpr int kQueries = 0, kKeys = kTiles * kBytes, kValues = kKeys + kStages * kBytes;
+  static constexpr int kEnd = kValues + kStages * kBytes;
+  // more than half of an SM's, for a block has all of its tensor memory
+  static constexpr int kSmem = (kEnd > 118 * 1024 ? kEnd : 118 * 1024) + 1024;
+  static constexpr int kScoresAt = 0, kResultsAt = kTiles * kWideTile;  // columns of tensor memory
+};
+
+struct WideShared {
+  uint64_t keys_full[2], keys_empty[2], values_full[2], values_empty[2];
+  uint64_t scores_full[2], weights_full[2], results_full[2], queries_full, units_full, drained;
+  uint32_t tmem;
+  int power[2];      // of keys and of values: they are stored in units of 2^power
+  float largest[2][4];
+  int gave_up;
+};
+
+// Keys (or values) of 128 tokens at a time, a thread a token: codes to halves.
+// A code gets the exponent of 1024 before it, becomes n by one exact operation,
+// and base + step n by another that rounds.
+template <int G>
+__device__ void wide_fill(const AttendArgs& a, WideShared& sm, int which, uint32_t tile0, const AttendRequest& q, int r,
+                          int h, int limit, int n_tiles, int* redo) {
+  using Shape = WideShape<G>;
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const uint32_t full = (uint32_t)__cvta_generic_to_shared(which ? sm.values_full : sm.keys_full);
+  const uint32_t empty = (uint32_t)__cvta_generic_to_shared(which ? sm.values_empty : sm.keys_empty);
+  const unsigned char* pages = a.cache + ((int64_t)which * a.heads + h) * a.page_bytes;
+  const int32_t* table = a.table + (int64_t)r * a.table_stride;
+  uint4 codes[G];
+  uint32_t pair[G];
+  bool bad = false;
+  auto load = [&](int i) {
+    const int t = i * kWideTile + tid;
+    int32_t entry = -1;
+    if (t < limit) {
+      entry = __ldg(table + a.block((uint32_t)t));
+      if ((uint32_t)entry >= (uint32_t)a.n_blocks || entry < 0) {
+        entry = -1;
+        bad = true;  // reported by the other kernel, which leaves its tokens out
+      }
+    }
+    if (entry >= 0) {
+      const uint32_t row = (uint32_t)t - a.block((uint32_t)t) * a.block.d;
+      const unsigned char* page = pages + (int64_t)entry * a.block_stride;
+      const uint4* from = reinterpret_cast<const uint4*>(page + (int64_t)row * (16 * G));
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(page + ((int64_t)a.block.d * 16 + (int64_t)row * 4) * G);
+#pragma unroll
+      for (int j = 0; j < G; ++j) codes[j] = __ldg(from + j);
+      if constexpr (G % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < G; j += 4) *reinterpret_cast<uint4*>(pair + j) = __ldg(reinterpret_cast<const uint4*>(words + j));
+      } else {
+#pragma unroll
+        for (int j = 0; j < G; ++j) pair[j] = __ldg(words + j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        codes[j] = make_uint4(0, 0, 0, 0);
+        pair[j] = 0;
+      }
+    }
+  };
+  load(0);
+  // the unit: the largest of the first 128 tokens becomes 2^6 to 2^7
+  float most = 0.f;
+#pragma unroll
+  for (int j = 0; j < G; ++j) most = fmaxf(most, fabsf(bf16_high(pair[j])) + 16.f * bf16_low(pair[j]));
+  if (!(most < INFINITY)) most = 0.f;
+  most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
+  if (lane == 0) sm.largest[which][tid >> 5] = most;
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + which) : "memory");
+#pragma unroll
+  for (int w = 0; w < 4; ++w) most = fmaxf(most, sm.largest[which][w]);
+  const int power = min(max((__float_as_int(most) >> 23) - 127 - 6, -100), 100);
+  if (tid == 0) sm.power[which] = most > 0.f ? power : 0;
+  const float unit = power_of_2(most > 0.f ? -power : 0);
+  barrier_arrive((uint32_t)__cvta_generic_to_shared(&sm.units_full));
+
+  for (int i = 0; i < n_tiles; ++i) {
+    const int stage = i % Shape::kStages;
+    uint4 now[G];
+    uint32_t z[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      now[j] = codes[j];
+      z[j] = pair[j];
+    }
+    if (i + 1 < n_tiles) load(i + 1);
+    if (!barrier_wait(empty + 8 * stage, (i / Shape::kStages & 1) ^ 1, &sm.gave_up)) return;
+    const uint32_t to = tile0 + stage * Shape::kBytes + tid * 128;
+    __half2 st[G], ba[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const float s = bf16_low(z[j]) * unit, b = bf16_high(z[j]) * unit, size = fabsf(b) + 16.f * s;
+      // too large for halves or no number; of values also too small for what is left of their bits
+      if (!(size < 32768.f) || (which && size > 0.f && size < 0x1p-9f)) bad = true;
+      st[j] = __float2half2_rn(s);
+      ba[j] = __float2half2_rn(b);
+    }
+    const __half2 less = __float2half2_rn(-1024.f), by = __float2half2_rn(0.0625f), less16 = __float2half2_rn(-64.f);
+    auto convert = [&](uint32_t w, int j, int chunk) {  // chunk: of 8 elements, in the row
+      uint32_t out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = e < 2 ? w : w >> 8;
+        const uint32_t y = (x & (e & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+        const __half2 n = e & 1 ? __hfma2(*reinterpret_cast<const __half2*>(&y), by, less16)
+                                : __hadd2(*reinterpret_cast<const __half2*>(&y), less);
+        const __half2 v = __hfma2(n, st[j], ba[j]);
+        out[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      const uint32_t at = to + (chunk >> 3) * Shape::kSub + (((chunk & 7) ^ (tid & 7)) << 4);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(out[0]), "r"(out[1]), "r"(out[2]), "r"(out[3])
+                   : "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < G; ++k) {  // the row's 16-byte pieces
+      const uint32_t w[4] = {now[k].x, now[k].y, now[k].z, now[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int u = k / 2;
+        if (2 * u + 1 < G) {  // words of two groups in turn
+          const int word = (k % 2) * 4 + e, c = word / 2, half = word % 2;
+          convert(w[e], (2 * u + half) % G, 8 * u + 4 * half + c);
+        } else {
+          convert(w[e], k, 8 * u + e);
+        }
+      }
+    }
+    publish();
+    barrier_arrive(full + 8 * stage);
+  }
+  if (bad) atomicOr(redo + r, 1);
+}
+
+template <int G>
+__global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, int* redo) {
+  using Shape = WideShape<G>;
+  constexpr int kCols = Shape::kTiles * kWideTile;
+  extern __shared__ unsigned char raw[];
+  __shared__ WideShared sm;
+  __shared__ int64_t upto[kWideThreads + 1];
+  __shared__ int64_t warp_sum[kWideThreads / 32];
+  __shared__ int found[4];  // request, head, first column
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- this block's columns: requests in order, each from its last columns on, heads in turn ----
+  const int each = (a.n + kWideThreads - 1) / kWideThreads;
+  const int r0 = min(a.n, tid * each), r1 = min(a.n, r0 + each);
+  auto blocks_of = [&](int r) -> int64_t {
+    const AttendRequest q = attend_request(a, r, false);
+    const int64_t cols = (int64_t)q.fresh * a.group.d;
+    return cols < kWideMin ? 0 : (cols + kCols - 1) / kCols * a.heads;
+  };
+  int64_t x = 0;
+  for (int r = r0; r < r1; ++r) x += blocks_of(r);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += o;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) x += warp_sum[w];
+  upto[tid + 1] = x;
+  if (tid == 0) upto[0] = 0;
+  __syncthreads();
+  const int64_t me = blockIdx.x;
+  if (me >= upto[kWideThreads]) return;
+  if (upto[tid] <= me && me < upto[tid + 1]) {
+    int64_t rest = me - upto[tid];
+    for (int r = r0; r < r1; ++r) {
+      const int64_t n = blocks_of(r);
+      if (rest < n) {
+        const int tiles = (int)(n / a.heads);
+        found[0] = r;
+        found[1] = (int)(rest % a.heads);
+        found[2] = (tiles - 1 - (int)(rest / a.heads)) * kCols;
+        break;
+      }
+      rest -= n;
+    }
+  }
+  if (tid == 0) {
+    auto at = [&](uint64_t& b) { return (uint32_t)__cvta_generic_to_shared(&b); };
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      barrier_init(at(sm.keys_full[s]), 128);
+      barrier_init(at(sm.keys_empty[s]), 1);
+      barrier_init(at(sm.values_full[s]), 128);
+      barrier_init(at(sm.values_empty[s]), 1);
+      barrier_init(at(sm.scores_full[s]), 1);
+      barrier_init(at(sm.weights_full[s]), 128);
+      barrier_init(at(sm.results_full[s]), 1);
+    }
+    barrier_init(at(sm.queries_full), 128 * Shape::kTiles);
+    barrier_init(at(sm.units_full), 256);
+    barrier_init(at(sm.drained), 1);
+    sm.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 16) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    before_sync();
+  }
+  __syncthreads();
+  after_sync();
+  const uint32_t tmem = sm.tmem;
+  const int r = found[0], h = found[1], first_col = found[2], group = (int)a.group.d;
+  const AttendRequest q = attend_request(a, r, false);
+  const int cols = min(kCols, q.fresh * group - first_col);
+  const int tiles = (cols + kWideTile - 1) / kWideTile;  // of columns that there are
+  // tokens that the last column sees
+  const int limit = max(0, q.len - q.fresh + (first_col + cols - 1) / group + 1);
+  const int n_tiles = (limit + kWideTile - 1) / kWideTile;
+  const uint32_t smem = ((uint32_t)__cvta_generic_to_shared(raw) + 1023u) & ~1023u;
+  auto bar = [&](uint64_t& b) { return (uint32_t)__cvta_generic_to_shared(&b); };
+
+  if (n_tiles == 0) {
+    // nothing is seen: zeros below
+  } else if (warp == 16) {
+    if (lane == 0) {
+      constexpr uint32_t kToScores = 1u << 4 | (kWideTile / 8) << 17 | (kWideTile / 16) << 24;
+      constexpr uint32_t kToResults = 1u << 4 | 1u << 16 | (uint32_t)(Shape::kDim / 8) << 17 | (kWideTile / 16) << 24;
+      auto scores = [&](int t, int i) {
+        const uint32_t qs = smem + Shape::kQueries + t * Shape::kBytes;
+        const uint32_t ks = smem + Shape::kKeys + i % Shape::kStages * Shape::kBytes;
+#pragma unroll
+        for (int k = 0; k < 2 * G; ++k)
+          product_smem(tmem + Shape::kScoresAt + t * kWideTile, matrix_at(qs + k / 4 * Shape::kSub + k % 4 * 32, 16),
+                       matrix_at(ks + k / 4 * Shape::kSub + k % 4 * 32, 16), kToScores, k > 0);
+        products_done(bar(sm.scores_full[t]));
+      };
+      bool ok = barrier_wait(bar(sm.queries_full), 0, &sm.gave_up) && barrier_wait(bar(sm.keys_full[0]), 0, &sm.gave_up);
+      if (ok) {
+        after_sync();
+        for (int t = 0; t < tiles; ++t) scores(t, 0);
+        products_done(bar(sm.keys_empty[0]));
+      }
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        const int stage = i % Shape::kStages, next = (i + 1) % Shape::kStages;
+        ok = barrier_wait(bar(sm.values_full[stage]), i / Shape::kStages & 1, &sm.gave_up);
+        for (int t = 0; ok && t < tiles; ++t) {
+          ok = barrier_wait(bar(sm.weights_full[t]), i & 1, &sm.gave_up);
+          if (!ok) break;
+          after_sync();
+          const uint32_t vs = smem + Shape::kValues + stage * Shape::kBytes;
+#pragma unroll
+          for (int k = 0; k < kWideTile / 16; ++k)
+            product_tmem(tmem + Shape::kResultsAt + t * Shape::kDim, tmem + Shape::kScoresAt + t * kWideTile + k * 8,
+                         matrix_at(vs + k * 2048, Shape::kSub), kToResults, i > 0 || k > 0);
+          if (i + 1 < n_tiles) {
+            if (t == 0) ok = barrier_wait(bar(sm.keys_full[next]), (i + 1) / Shape::kStages & 1, &sm.gave_up);
+            if (!ok) break;
+            after_sync();
+            scores(t, i + 1);
+          } else {
+            products_done(bar(sm.results_full[t]));
+          }
+        }
+        if (ok) {
+          products_done(bar(sm.values_empty[stage]));
+          if (i + 1 < n_tiles) products_done(bar(sm.keys_empty[next]));
+        }
+      }
+      if (!ok) {  // products must not outlive the block
+        int alone = 0;
+        products_done(bar(sm.drained));
+        barrier_wait(bar(sm.drained), 0, &alone);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    const int which = (warp - 8) / 4;
+    wide_fill<G>(a, sm, which, smem + (which ? Shape::kValues : Shape::kKeys), q, r, h, limit, n_tiles, redo);
+  } else if (warp / 4 >= tiles) {
+    if (warp / 4 < Shape::kTiles) barrier_arrive(bar(sm.queries_full));
+  } else {
+    // ---- a thread a column ----
+    const int t = warp / 4, row = tid & 127, col = first_col + t * kWideTile + row;
+    const bool real = t * kWideTile + row < cols;
+    const int token = (int)a.group((uint32_t)col), head = h * group + col - token * group;
+    const int sees = real ? max(0, q.len - q.fresh + token + 1) : 0;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // of tensor memory
+    const uint32_t s_at = tmem + lanes + Shape::kScoresAt + t * kWideTile;
+    const uint32_t o_at = tmem + lanes + Shape::kResultsAt + t * Shape::kDim;
+    float to_score;
+    {
+      const int64_t from = (int64_t)(q.first + token) * a.q_token + head * a.q_head;
+      auto queries = [&](auto type) {
+        using T = decltype(type);
+        const T* x = static_cast<const T*>(a.queries) + from;
+        auto get = [&](int at, float (&e)[8]) {
+          if (real && a.q_wide && at < a.dim) {
+            Vec<T, 8> v;
+            v.template load<true>(x + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = to_f32(v.x[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = real && at + i < a.dim ? to_f32(x[at + i]) : 0.f;
+          }
+        };
+        float most = 0.f, e[8];
+#pragma unroll 4
+        for (int k = 0; k < 4 * G; ++k) {
+          get(8 * k, e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(e[i]));
+        }
+        // the largest element in [2^6, 2^7)
+        const int by = min(max(6 - ((__float_as_int(most) >> 23) - 127), -120), 120);
+        const float scale = power_of_2(by);
+        to_score = fabsf(a.scale) / scale;
+        const float signed_scale = a.scale < 0.f ? -scale : scale;
+        const uint32_t to = smem + Shape::kQueries + t * Shape::kBytes + row * 128;
+#pragma unroll 4
+        for (int k = 0; k < 4 * G; ++k) {
+          get(8 * k, e);
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack_halves(e[i] * signed_scale, e[i + 4] * signed_scale);
+          const uint32_t at = to + (k >> 3) * Shape::kSub + (((k & 7) ^ (row & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      };
+      if (a.q_type == BPE_F16) queries(__half{});
+      else queries(__nv_bfloat16{});
+    }
+    publish();
+    barrier_arrive(bar(sm.queries_full));
+    bool ok = barrier_wait(bar(sm.units_full), 0, &sm.gave_up);
+    to_score *= power_of_2(sm.power[0]);
+    // weights are 2^6 at the reference, which follows the maximum only when it is 2^8 behind
+    float reference = -INFINITY, total = 0.f;
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      ok = barrier_wait(bar(sm.scores_full[t]), i & 1, &sm.gave_up);
+      if (!ok) break;
+      after_sync();
+      const int left = sees - i * kWideTile;  // tokens of these that the column sees
+      const bool all = __all_sync(0xFFFFFFFFu, left >= kWideTile);
+      float most = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t s[32];
+        tmem_load(s, s_at + 32 * k);
+        tmem_loaded();
+        if (all) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            most = fmaxf(most, fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * k + j < left) most = fmaxf(most, __uint_as_float(s[j]));
+        }
+      }
+      most *= to_score;
+      const bool behind = most > reference + 8.f;
+      if (__any_sync(0xFFFFFFFFu, behind)) {
+        const float next = fmaxf(reference, most), f = next > reference ? exp2_fast(reference - next) : 1.f;
+        total *= f;
+        reference = next;
+        if (i > 0) {
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            uint32_t o[32];
+            tmem_load(o, o_at + 32 * k);
+            tmem_loaded();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_store(o_at + 32 * k, o);
+          }
+        }
+      }
+      const float minus = 6.f - (reference == -INFINITY ? 0.f : reference);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t s[32], p[16];
+        tmem_load(s, s_at + 32 * k);
+        tmem_loaded();
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float x = exp2_fast(__uint_as_float(s[j]) * to_score + minus);
+          float y = exp2_fast(__uint_as_float(s[j + 1]) * to_score + minus);
+          if (!all) {
+            if (32 * k + j >= left) x = 0.f;
+            if (32 * k + j + 1 >= left) y = 0.f;
+          }
+          total += x + y;
+          p[j / 2] = pack_halves(x, y);
+        }
+        tmem_store16(s_at + 16 * k, p);
+      }
+      tmem_stored();
+      before_sync();
+      barrier_arrive(bar(sm.weights_full[t]));
+    }
+    ok = ok && barrier_wait(bar(sm.results_full[t]), 0, &sm.gave_up);
+    if (ok) {
+      after_sync();
+      const float by = total == 0.f ? 0.f : power_of_2(sm.power[1]) / total;
+      const int64_t to = (int64_t)(q.first + token) * a.o_token + head * a.o_head;
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        uint32_t o[32];
+        tmem_load(o, o_at + 32 * k);
+        tmem_loaded();
+        if (real) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // in the order 0, 4, 1, 5, 2, 6, 3, 7
+            auto e = [&](int i) { return __uint_as_float(o[8 * c + (i % 4) * 2 + i / 4]) * by; };
+            attend_store(a, to, 32 * k + 8 * c, make_float4(e(0), e(1), e(2), e(3)));
+            attend_store(a, to, 32 * k + 8 * c + 4, make_float4(e(4), e(5), e(6), e(7)));
+          }
+        }
+      }
+      before_sync();
+    }
+  }
+  if (n_tiles == 0) {
+    for (int i = tid; i < cols * (Shape::kDim / 4); i += kWideThreads) {
+      const int col = first_col + i / (Shape::kDim / 4), token = col / group, head = h * group + col - token * group;
+      attend_store(a, (int64_t)(q.first + token) * a.o_token + head * a.o_head, i % (Shape::kDim / 4) * 4,
+                   make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && sm.gave_up) atomicOr(&a.small->op_status, kStTimeout);
+  after_sync();
+  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+}  // namespace

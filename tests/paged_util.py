@@ -104,19 +104,23 @@ def random_cache(rng, blocks, heads, block, dim):
     return cache
 
 
-def attention(q, cache, table, lens, block, offsets=None, scale=None, parts=2):
+def attention(q, cache, table, lens, block, offsets=None, scale=None, parts=1):
     """(out, bound) in 64 bits: what attend gives for float64 queries [tokens,
-    rows, dim], and what its 32-bit sums may be off by. NaN where no request has
-    the token. parts: pieces of bfloat16 that a weight is cut into.
+    rows, dim], and what its sums may be off by. NaN where no request has the
+    token. parts: halves that a weight or a query is cut into (1 for 16-bit
+    queries, 2 for 32-bit ones).
 
     The bound, with u = 2^-24 and the tensor cores' sums taken to lose up to 2 u
-    of what they hold at each of their additions: a score's sums have at most
-    dim + 3 groups additions of terms below |q_i| (2 * 16 step + |base| + 16
-    step), and its products with scale and log2 e two roundings of |s|; e^x is off
-    by 2 u and by the error of its argument, a score's and the maximum's. A
-    weight's parts leave 2^-(8 parts + 1) of it. The sum over tokens is one of
-    at most tokens + 64 additions of terms below p (3 * 16 step + |base|), the
-    joining of parts among them."""
+    of what they hold at each of their additions. A score's sums have at most
+    dim + 3 groups additions of terms below |q_i| (48 step + |base|), and its
+    products with scale and log2 e two roundings of |s|. With one part, keys are
+    halves, off by 2^-12 of themselves, or codes as subnormal halves, whose
+    products lose what lies 24 bits below their exponent's 2^-14: of queries
+    scaled to 2^14 at most 2^-13 of the largest, times the step. e^x is off by 2 u
+    and by the error of its argument, a score's and the maximum's. A weight is
+    rounded twice, or once and its value once, to 2^-(12 parts) each. The sum over
+    tokens is one of at most tokens + 64 additions of terms below p (48 step +
+    |base|), the joining of parts among them."""
     tokens, rows, dim = q.shape
     heads = cache.shape[2]
     group = rows // heads
@@ -131,7 +135,7 @@ def attention(q, cache, table, lens, block, offsets=None, scale=None, parts=2):
         if m == 0:
             continue
         for h in range(heads):
-            kv, size = [], []
+            kv, size, steps = [], [], []
             for which in (0, 1):
                 rows_c, rows_p = [], []
                 for b in range(-(-length // block)):
@@ -143,6 +147,7 @@ def attention(q, cache, table, lens, block, offsets=None, scale=None, parts=2):
                 step, base = bf16_value(p & 0xFFFF).astype(np.float64), bf16_value(p >> 16).astype(np.float64)
                 with np.errstate(invalid="ignore"):
                     kv.append((np.repeat(base, GROUP, 1) + np.repeat(step, GROUP, 1) * c)[:, :dim])
+                steps.append(step)
                 size.append(np.repeat(48 * step + np.abs(base), GROUP, 1)[:, :dim])
             for i in range(m):
                 seen = min(max(length - m + i + 1, 0), length)
@@ -155,11 +160,14 @@ def attention(q, cache, table, lens, block, offsets=None, scale=None, parts=2):
                     with np.errstate(invalid="ignore"):
                         s = scale * (kv[0][:seen] @ x)
                         off = abs(scale) * (size[0][:seen] @ np.abs(x)) * (dim + 3 * g) * 2 * U + 4 * U * np.abs(s)
+                        if parts == 1:
+                            off += abs(scale) * (size[0][:seen] @ np.abs(x)) * 2.0 ** -12
+                            off += abs(scale) * np.abs(x).max() * 2.0 ** -13 * 34 * steps[0][:seen].sum(1)
                         w = np.exp(s - s.max())
                         w /= w.sum()
                         out[at] = w @ kv[1][:seen]
                         rel = 2 * off.max() + 4 * U * (s.max() - s.min() + 1) + 4 * U
-                        rel += 2.0 ** -(8 * parts + 1) + (seen + 64) * 2 * U
+                        rel += 2.0 ** -(12 * parts - 1) + (seen + 64) * 2 * U
                         bound[at] = np.expm1(rel) * (w @ size[1][:seen])
     return out, bound
 
