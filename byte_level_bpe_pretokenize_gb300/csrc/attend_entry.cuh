@@ -49,7 +49,11 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
     const int64_t groups = cache_groups(p.dim);
     const size_t records = align256((size_t)h->n_sms * kAttMaxWarps * 2 * sizeof(int4));
     const size_t partials = align256((size_t)h->n_sms * BPE_ATTEND_PARTIALS * (32 * groups + 2) * sizeof(float));
-    const bool wide = p.query_type != BPE_F32 && p.offsets && p.n_tokens * p.group >= kWideMin;
+    // The host knows how many columns there are, not whose. Few in all and few a request (drafted tokens of many
+    // requests): that one has kWideMin of them is not worth the launch, 10 us.
+    const int64_t columns = p.n_tokens * p.group;
+    const bool wide = p.query_type != BPE_F32 && p.offsets && columns >= kWideMin &&
+                      (columns >= 4096 || columns >= 16 * p.n_requests);
     rc = ensure_ws(h, records + partials + (wide ? (size_t)p.n_requests * sizeof(int) : 0), st);
     if (rc) return rc;
     auto fits = [&](const void* q, int64_t token, int64_t head, int64_t size, int64_t V) {
@@ -100,8 +104,8 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
         if (ok) return ok;
         CK(cudaMemsetAsync(redo, 0, (size_t)p.n_requests * sizeof(int), st));
         // as many blocks as requests of kWideMin columns on can need
-        const int64_t cols = p.n_tokens * p.group, at_once = Wide::kTiles * kWideTile;
-        const int64_t blocks = (cols / at_once + std::min(p.n_requests, cols / kWideMin)) * p.n_heads;
+        const int64_t at_once = Wide::kTiles * kWideTile;
+        const int64_t blocks = (columns / at_once + std::min(p.n_requests, columns / kWideMin)) * p.n_heads;
         k_attend_wide<G><<<(unsigned)std::min<int64_t>(blocks, INT32_MAX), kWideThreads, Wide::kSmem, st>>>(a, redo);
         CK(cudaGetLastError());
         a.redo = redo;

@@ -56,32 +56,38 @@ __device__ __forceinline__ bool barrier_wait(uint32_t at, uint32_t parity, volat
   return false;
 }
 
-// Matrix in shared memory in rows of 128 bytes, swizzled in groups of 8 rows.
-// K-major (a row: 64 elements of the summed dimension): groups of rows are
-// 1024 bytes apart. MN-major (a row: 64 elements of the other one): groups of 8
-// along the sum 1024 bytes, blocks of 64 elements `block` bytes apart.
-__device__ __forceinline__ uint64_t matrix_at(uint32_t at, uint32_t block) {
-  return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Matrix in shared memory in rows of 128 bytes, swizzled in groups of 8 rows,
+// as the low word of its description. K-major (a row: 64 elements of the summed
+// dimension): groups of rows are 1024 bytes apart. MN-major (a row: 64 elements
+// of the other one): groups of 8 along the sum 1024 bytes, blocks of 64 elements
+// `block` bytes apart. Steps within the matrix are added in units of 16 bytes.
+__device__ __forceinline__ uint32_t matrix_at(uint32_t at, uint32_t block) { return (at & 0x3FFFF) >> 4 | block >> 4 << 16; }
+constexpr uint32_t kMatrixHigh = 1024 >> 4 | 1 << 14 | 2u << 29;
 
-__device__ __forceinline__ void product_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+// d (+)= a b, by the one thread with `issue`; all of the warp calls it, so that
+// what describes the matrices stays in uniform registers.
+__device__ __forceinline__ void product_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add, uint32_t issue) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(issue), "r"(kMatrixHigh)
       : "memory");
 }
-__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add, uint32_t issue) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n mov.b64 b, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(issue), "r"(kMatrixHigh)
       : "memory");
 }
 // Arrives at a barrier when the products issued so far are done.
-__device__ __forceinline__ void products_done(uint32_t barrier) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(barrier) : "memory");
+__device__ __forceinline__ void products_done(uint32_t barrier, uint32_t issue) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(barrier),
+      "r"(issue)
+      : "memory");
 }
 
 // 32 columns of a thread's row of tensor memory.
@@ -105,17 +111,43 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Two additions, or products and sums, at once.
+__device__ __forceinline__ float2 add_two(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 c, a, b;\n mov.b64 {%0, %1}, c;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma_two(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float max_three(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 // What this thread wrote to shared memory is there for the tensor cores.
 __device__ __forceinline__ void publish() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -135,8 +167,11 @@ struct WideShape {
 };
 
 struct WideShared {
-  uint64_t keys_full[2], keys_empty[2], values_full[2], values_empty[2];
-  uint64_t scores_full[2], weights_full[2], results_full[2], queries_full, units_full, drained;
+  uint64_t keys_full[2], values_full[2];
+  // of each tile of columns, for even and odd steps; those of the last tile also say that a stage is free: of keys
+  // when its scores are there, of values when the next step's are, which are made behind its results
+  uint64_t scores_full[2][2];
+  uint64_t weights_full[2], results_full[2], queries_full, units_full, drained;
   uint32_t tmem;
   int power[2];      // of keys and of values: they are stored in units of 2^power
   float largest[2][4];
@@ -147,12 +182,12 @@ struct WideShared {
 // A code gets the exponent of 1024 before it, becomes n by one exact operation,
 // and base + step n by another that rounds.
 template <int G>
-__device__ void wide_fill(const AttendArgs& a, WideShared& sm, int which, uint32_t tile0, const AttendRequest& q, int r,
-                          int h, int limit, int n_tiles, int* redo) {
+__device__ void wide_fill(const AttendArgs& a, WideShared& sm, int which, uint32_t tile0, int r, int h, int limit,
+                          int n_tiles, int last_tile, int* redo) {
   using Shape = WideShape<G>;
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const uint32_t full = (uint32_t)__cvta_generic_to_shared(which ? sm.values_full : sm.keys_full);
-  const uint32_t empty = (uint32_t)__cvta_generic_to_shared(which ? sm.values_empty : sm.keys_empty);
+  const uint32_t free = (uint32_t)__cvta_generic_to_shared(sm.scores_full[last_tile]);
   const unsigned char* pages = a.cache + ((int64_t)which * a.heads + h) * a.page_bytes;
   const int32_t* table = a.table + (int64_t)r * a.table_stride;
   uint4 codes[G];
@@ -216,7 +251,10 @@ __device__ void wide_fill(const AttendArgs& a, WideShared& sm, int which, uint32
       z[j] = pair[j];
     }
     if (i + 1 < n_tiles) load(i + 1);
-    if (!barrier_wait(empty + 8 * stage, (i / Shape::kStages & 1) ^ 1, &sm.gave_up)) return;
+    if (i >= Shape::kStages) {  // which step's scores say that the stage is free
+      const int by = i - Shape::kStages + which;
+      if (!barrier_wait(free + 8 * (by & 1), by >> 1 & 1, &sm.gave_up)) return;
+    }
     const uint32_t to = tile0 + stage * Shape::kBytes + tid * 128;
     __half2 st[G], ba[G];
 #pragma unroll
@@ -316,10 +354,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       barrier_init(at(sm.keys_full[s]), 128);
-      barrier_init(at(sm.keys_empty[s]), 1);
       barrier_init(at(sm.values_full[s]), 128);
-      barrier_init(at(sm.values_empty[s]), 1);
-      barrier_init(at(sm.scores_full[s]), 1);
+      barrier_init(at(sm.scores_full[s][0]), 1);
+      barrier_init(at(sm.scores_full[s][1]), 1);
       barrier_init(at(sm.weights_full[s]), 128);
       barrier_init(at(sm.results_full[s]), 1);
     }
@@ -352,60 +389,58 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
   if (n_tiles == 0) {
     // nothing is seen: zeros below
   } else if (warp == 16) {
-    if (lane == 0) {
-      constexpr uint32_t kToScores = 1u << 4 | (kWideTile / 8) << 17 | (kWideTile / 16) << 24;
-      constexpr uint32_t kToResults = 1u << 4 | 1u << 16 | (uint32_t)(Shape::kDim / 8) << 17 | (kWideTile / 16) << 24;
-      auto scores = [&](int t, int i) {
-        const uint32_t qs = smem + Shape::kQueries + t * Shape::kBytes;
-        const uint32_t ks = smem + Shape::kKeys + i % Shape::kStages * Shape::kBytes;
+    constexpr uint32_t kToScores = 1u << 4 | (kWideTile / 8) << 17 | (kWideTile / 16) << 24;
+    constexpr uint32_t kToResults = 1u << 4 | 1u << 16 | (uint32_t)(Shape::kDim / 8) << 17 | (kWideTile / 16) << 24;
+    const uint32_t issue = lane == 0;
+    const uint32_t queries = matrix_at(smem + Shape::kQueries, 16), keys = matrix_at(smem + Shape::kKeys, 16);
+    const uint32_t values = matrix_at(smem + Shape::kValues, Shape::kSub);
+    auto scores = [&](int t, int i) {
+      const uint32_t qs = queries + t * (Shape::kBytes / 16), ks = keys + i % Shape::kStages * (Shape::kBytes / 16);
 #pragma unroll
-        for (int k = 0; k < 2 * G; ++k)
-          product_smem(tmem + Shape::kScoresAt + t * kWideTile, matrix_at(qs + k / 4 * Shape::kSub + k % 4 * 32, 16),
-                       matrix_at(ks + k / 4 * Shape::kSub + k % 4 * 32, 16), kToScores, k > 0);
-        products_done(bar(sm.scores_full[t]));
-      };
-      bool ok = barrier_wait(bar(sm.queries_full), 0, &sm.gave_up) && barrier_wait(bar(sm.keys_full[0]), 0, &sm.gave_up);
-      if (ok) {
+      for (int k = 0; k < 2 * G; ++k)
+        product_smem(tmem + Shape::kScoresAt + t * kWideTile, qs + (k / 4 * Shape::kSub + k % 4 * 32) / 16,
+                     ks + (k / 4 * Shape::kSub + k % 4 * 32) / 16, kToScores, k > 0, issue);
+      products_done(bar(sm.scores_full[t][i & 1]), issue);
+    };
+    bool ok = barrier_wait(bar(sm.queries_full), 0, &sm.gave_up) && barrier_wait(bar(sm.keys_full[0]), 0, &sm.gave_up);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok) {
+      after_sync();
+      for (int t = 0; t < tiles; ++t) scores(t, 0);
+    }
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      const int stage = i % Shape::kStages, next = (i + 1) % Shape::kStages;
+      ok = __all_sync(0xFFFFFFFFu, barrier_wait(bar(sm.values_full[stage]), i / Shape::kStages & 1, &sm.gave_up));
+      for (int t = 0; ok && t < tiles; ++t) {
+        ok = __all_sync(0xFFFFFFFFu, barrier_wait(bar(sm.weights_full[t]), i & 1, &sm.gave_up));
+        if (!ok) break;
         after_sync();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-        products_done(bar(sm.keys_empty[0]));
-      }
-      for (int i = 0; ok && i < n_tiles; ++i) {
-        const int stage = i % Shape::kStages, next = (i + 1) % Shape::kStages;
-        ok = barrier_wait(bar(sm.values_full[stage]), i / Shape::kStages & 1, &sm.gave_up);
-        for (int t = 0; ok && t < tiles; ++t) {
-          ok = barrier_wait(bar(sm.weights_full[t]), i & 1, &sm.gave_up);
+        const uint32_t vs = values + stage * (Shape::kBytes / 16);
+#pragma unroll
+        for (int k = 0; k < kWideTile / 16; ++k)
+          product_tmem(tmem + Shape::kResultsAt + t * Shape::kDim, tmem + Shape::kScoresAt + t * kWideTile + k * 8,
+                       vs + k * 2048 / 16, kToResults, i > 0 || k > 0, issue);
+        if (i + 1 < n_tiles) {
+          if (t == 0)
+            ok = __all_sync(0xFFFFFFFFu,
+                            barrier_wait(bar(sm.keys_full[next]), (i + 1) / Shape::kStages & 1, &sm.gave_up));
           if (!ok) break;
           after_sync();
-          const uint32_t vs = smem + Shape::kValues + stage * Shape::kBytes;
-#pragma unroll
-          for (int k = 0; k < kWideTile / 16; ++k)
-            product_tmem(tmem + Shape::kResultsAt + t * Shape::kDim, tmem + Shape::kScoresAt + t * kWideTile + k * 8,
-                         matrix_at(vs + k * 2048, Shape::kSub), kToResults, i > 0 || k > 0);
-          if (i + 1 < n_tiles) {
-            if (t == 0) ok = barrier_wait(bar(sm.keys_full[next]), (i + 1) / Shape::kStages & 1, &sm.gave_up);
-            if (!ok) break;
-            after_sync();
-            scores(t, i + 1);
-          } else {
-            products_done(bar(sm.results_full[t]));
-          }
-        }
-        if (ok) {
-          products_done(bar(sm.values_empty[stage]));
-          if (i + 1 < n_tiles) products_done(bar(sm.keys_empty[next]));
+          scores(t, i + 1);
+        } else {
+          products_done(bar(sm.results_full[t]), issue);
         }
       }
-      if (!ok) {  // products must not outlive the block
-        int alone = 0;
-        products_done(bar(sm.drained));
-        barrier_wait(bar(sm.drained), 0, &alone);
-      }
+    }
+    if (!ok) {  // products must not outlive the block
+      int alone = 0;
+      products_done(bar(sm.drained), issue);
+      barrier_wait(bar(sm.drained), 0, &alone);
     }
     __syncwarp();
   } else if (warp >= 8) {
     const int which = (warp - 8) / 4;
-    wide_fill<G>(a, sm, which, smem + (which ? Shape::kValues : Shape::kKeys), q, r, h, limit, n_tiles, redo);
+    wide_fill<G>(a, sm, which, smem + (which ? Shape::kValues : Shape::kKeys), r, h, limit, n_tiles, tiles - 1, redo);
   } else if (warp / 4 >= tiles) {
     if (warp / 4 < Shape::kTiles) barrier_arrive(bar(sm.queries_full));
   } else {
@@ -468,30 +503,37 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
     // weights are 2^6 at the reference, which follows the maximum only when it is 2^8 behind
     float reference = -INFINITY, total = 0.f;
     for (int i = 0; ok && i < n_tiles; ++i) {
-      ok = barrier_wait(bar(sm.scores_full[t]), i & 1, &sm.gave_up);
+      ok = barrier_wait(bar(sm.scores_full[t][i & 1]), i >> 1 & 1, &sm.gave_up);
       if (!ok) break;
       after_sync();
       const int left = sees - i * kWideTile;  // tokens of these that the column sees
       const bool all = __all_sync(0xFFFFFFFFu, left >= kWideTile);
-      float most = -INFINITY;
+      // the scores, 16 at a time, the next ones on their way
+      auto scores = [&](auto use) {
+        uint32_t s[2][16];
+        tmem_load16(s[0], s_at);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t s[32];
-        tmem_load(s, s_at + 32 * k);
-        tmem_loaded();
-        if (all) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            most = fmaxf(most, fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (32 * k + j < left) most = fmaxf(most, __uint_as_float(s[j]));
+        for (int k = 0; k < 8; ++k) {
+          tmem_loaded();
+          if (k < 7) tmem_load16(s[(k + 1) & 1], s_at + 16 * (k + 1));
+          use(k, s[k & 1]);
         }
+      };
+      float most = -INFINITY;
+      if (all) {
+        scores([&](int, const uint32_t* s) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) most = max_three(most, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+        });
+      } else {
+        scores([&](int k, const uint32_t* s) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (16 * k + j < left) most = fmaxf(most, __uint_as_float(s[j]));
+        });
       }
       most *= to_score;
-      const bool behind = most > reference + 8.f;
-      if (__any_sync(0xFFFFFFFFu, behind)) {
+      if (__any_sync(0xFFFFFFFFu, most > reference + 8.f)) {
         const float next = fmaxf(reference, most), f = next > reference ? exp2_fast(reference - next) : 1.f;
         total *= f;
         reference = next;
@@ -508,24 +550,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
         }
       }
       const float minus = 6.f - (reference == -INFINITY ? 0.f : reference);
+      const float2 by = make_float2(to_score, to_score), less = make_float2(minus, minus);
+      float2 sum = make_float2(0.f, 0.f);
+      auto weigh = [&](auto all_tag) {
+        scores([&](int k, const uint32_t* s) {
+          uint32_t p[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t s[32], p[16];
-        tmem_load(s, s_at + 32 * k);
-        tmem_loaded();
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float x = exp2_fast(__uint_as_float(s[j]) * to_score + minus);
-          float y = exp2_fast(__uint_as_float(s[j + 1]) * to_score + minus);
-          if (!all) {
-            if (32 * k + j >= left) x = 0.f;
-            if (32 * k + j + 1 >= left) y = 0.f;
+          for (int j = 0; j < 16; j += 2) {
+            const float2 z = fma_two(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), by, less);
+            float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+            if (!decltype(all_tag)::value) {
+              if (16 * k + j >= left) e.x = 0.f;
+              if (16 * k + j + 1 >= left) e.y = 0.f;
+            }
+            sum = add_two(sum, e);
+            p[j / 2] = pack_halves(e.x, e.y);
           }
-          total += x + y;
-          p[j / 2] = pack_halves(x, y);
-        }
-        tmem_store16(s_at + 16 * k, p);
-      }
+          tmem_store8(s_at + 8 * k, p);  // over scores that were read
+        });
+      };
+      if (all) weigh(std::true_type{});
+      else weigh(std::false_type{});
+      total += sum.x + sum.y;
       tmem_stored();
       before_sync();
       barrier_arrive(bar(sm.weights_full[t]));
