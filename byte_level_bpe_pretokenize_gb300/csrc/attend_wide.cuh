@@ -64,30 +64,30 @@ __device__ __forceinline__ bool barrier_wait(uint32_t at, uint32_t parity, volat
 __device__ __forceinline__ uint32_t matrix_at(uint32_t at, uint32_t block) { return (at & 0x3FFFF) >> 4 | block >> 4 << 16; }
 constexpr uint32_t kMatrixHigh = 1024 >> 4 | 1 << 14 | 2u << 29;
 
-// d (+)= a b, by the one thread with `issue`; all of the warp calls it, so that
-// what describes the matrices stays in uniform registers.
-__device__ __forceinline__ void product_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add, uint32_t issue) {
+// d (+)= a b, by one thread.
+__device__ __forceinline__ void product_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-      " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(issue), "r"(kMatrixHigh)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kMatrixHigh)
       : "memory");
 }
-__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add, uint32_t issue) {
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n mov.b64 b, {%2, %6};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(issue), "r"(kMatrixHigh)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)add), "r"(kMatrixHigh)
       : "memory");
 }
 // Arrives at a barrier when the products issued so far are done.
-__device__ __forceinline__ void products_done(uint32_t barrier, uint32_t issue) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(barrier),
-      "r"(issue)
-      : "memory");
+__device__ __forceinline__ void products_done(uint32_t barrier) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(barrier) : "memory");
+}
+// Whether this is the one thread of its warp that issues.
+__device__ __forceinline__ bool elected() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+  return yes != 0;
 }
 
 // 32 columns of a thread's row of tensor memory.
@@ -175,6 +175,7 @@ struct WideShared {
   uint32_t tmem;
   int power[2];      // of keys and of values: they are stored in units of 2^power
   float largest[2][4];
+  int query_size[2][kWideTile];  // the largest element of a column's query, as bits
   int gave_up;
 };
 
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
   }
   __syncthreads();
   after_sync();
-  const uint32_t tmem = sm.tmem;
+  constexpr uint32_t tmem = 0;  // all of it: it begins at its beginning
   const int r = found[0], h = found[1], first_col = found[2], group = (int)a.group.d;
   const AttendRequest q = attend_request(a, r, false);
   const int cols = min(kCols, q.fresh * group - first_col);
@@ -391,51 +392,52 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
   } else if (warp == 16) {
     constexpr uint32_t kToScores = 1u << 4 | (kWideTile / 8) << 17 | (kWideTile / 16) << 24;
     constexpr uint32_t kToResults = 1u << 4 | 1u << 16 | (uint32_t)(Shape::kDim / 8) << 17 | (kWideTile / 16) << 24;
-    const uint32_t issue = lane == 0;
     const uint32_t queries = matrix_at(smem + Shape::kQueries, 16), keys = matrix_at(smem + Shape::kKeys, 16);
     const uint32_t values = matrix_at(smem + Shape::kValues, Shape::kSub);
     auto scores = [&](int t, int i) {
       const uint32_t qs = queries + t * (Shape::kBytes / 16), ks = keys + i % Shape::kStages * (Shape::kBytes / 16);
+      const uint32_t d = tmem + Shape::kScoresAt + t * kWideTile;
 #pragma unroll
       for (int k = 0; k < 2 * G; ++k)
-        product_smem(tmem + Shape::kScoresAt + t * kWideTile, qs + (k / 4 * Shape::kSub + k % 4 * 32) / 16,
-                     ks + (k / 4 * Shape::kSub + k % 4 * 32) / 16, kToScores, k > 0, issue);
-      products_done(bar(sm.scores_full[t][i & 1]), issue);
+        product_smem(d, qs + (k / 4 * Shape::kSub + k % 4 * 32) / 16, ks + (k / 4 * Shape::kSub + k % 4 * 32) / 16,
+                     kToScores, k > 0);
+      products_done(bar(sm.scores_full[t][i & 1]));
     };
-    bool ok = barrier_wait(bar(sm.queries_full), 0, &sm.gave_up) && barrier_wait(bar(sm.keys_full[0]), 0, &sm.gave_up);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    if (ok) {
-      after_sync();
-      for (int t = 0; t < tiles; ++t) scores(t, 0);
-    }
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      const int stage = i % Shape::kStages, next = (i + 1) % Shape::kStages;
-      ok = __all_sync(0xFFFFFFFFu, barrier_wait(bar(sm.values_full[stage]), i / Shape::kStages & 1, &sm.gave_up));
-      for (int t = 0; ok && t < tiles; ++t) {
-        ok = __all_sync(0xFFFFFFFFu, barrier_wait(bar(sm.weights_full[t]), i & 1, &sm.gave_up));
-        if (!ok) break;
+    if (elected()) {
+      bool ok = barrier_wait(bar(sm.queries_full), 0, &sm.gave_up) && barrier_wait(bar(sm.keys_full[0]), 0, &sm.gave_up);
+      if (ok) {
         after_sync();
-        const uint32_t vs = values + stage * (Shape::kBytes / 16);
-#pragma unroll
-        for (int k = 0; k < kWideTile / 16; ++k)
-          product_tmem(tmem + Shape::kResultsAt + t * Shape::kDim, tmem + Shape::kScoresAt + t * kWideTile + k * 8,
-                       vs + k * 2048 / 16, kToResults, i > 0 || k > 0, issue);
-        if (i + 1 < n_tiles) {
-          if (t == 0)
-            ok = __all_sync(0xFFFFFFFFu,
-                            barrier_wait(bar(sm.keys_full[next]), (i + 1) / Shape::kStages & 1, &sm.gave_up));
+        for (int t = 0; t < tiles; ++t) scores(t, 0);
+      }
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        const int stage = i % Shape::kStages, next = (i + 1) % Shape::kStages;
+        ok = barrier_wait(bar(sm.values_full[stage]), i / Shape::kStages & 1, &sm.gave_up);
+        for (int t = 0; ok && t < tiles; ++t) {
+          ok = barrier_wait(bar(sm.weights_full[t]), i & 1, &sm.gave_up);
           if (!ok) break;
           after_sync();
-          scores(t, i + 1);
-        } else {
-          products_done(bar(sm.results_full[t]), issue);
+          const uint32_t vs = values + stage * (Shape::kBytes / 16);
+          const uint32_t d = tmem + Shape::kResultsAt + t * Shape::kDim, w = tmem + Shape::kScoresAt + t * kWideTile;
+#pragma unroll
+          for (int k = 0; k < kWideTile / 16; ++k)
+            product_tmem(d, w + k * 8, vs + k * 2048 / 16, kToResults, i > 0 || k > 0);
+          if (i + 1 < n_tiles) {
+            if (t == 0) {
+              ok = barrier_wait(bar(sm.keys_full[next]), (i + 1) / Shape::kStages & 1, &sm.gave_up);
+              if (!ok) break;
+              after_sync();
+            }
+            scores(t, i + 1);
+          } else {
+            products_done(bar(sm.results_full[t]));
+          }
         }
       }
-    }
-    if (!ok) {  // products must not outlive the block
-      int alone = 0;
-      products_done(bar(sm.drained), issue);
-      barrier_wait(bar(sm.drained), 0, &alone);
+      if (!ok) {  // products must not outlive the block
+        int alone = 0;
+        products_done(bar(sm.drained));
+        barrier_wait(bar(sm.drained), 0, &alone);
+      }
     }
     __syncwarp();
   } else if (warp >= 8) {
@@ -447,54 +449,82 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
     // ---- a thread a column ----
     const int t = warp / 4, row = tid & 127, col = first_col + t * kWideTile + row;
     const bool real = t * kWideTile + row < cols;
-    const int token = (int)a.group((uint32_t)col), head = h * group + col - token * group;
+    const int token = (int)a.group((uint32_t)col);
     const int sees = real ? max(0, q.len - q.fresh + token + 1) : 0;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // of tensor memory
     const uint32_t s_at = tmem + lanes + Shape::kScoresAt + t * kWideTile;
     const uint32_t o_at = tmem + lanes + Shape::kResultsAt + t * Shape::kDim;
     float to_score;
     {
-      const int64_t from = (int64_t)(q.first + token) * a.q_token + head * a.q_head;
-      auto queries = [&](auto type) {
+      // The tile's queries, 8 elements a thread at a time, neighbours in a row: read once for each row's largest
+      // element, and again, from the caches, to be scaled and stored.
+      auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(3 + t) : "memory"); };
+      sm.query_size[t][row] = 0;
+      meet();
+      auto scale_of = [&](int of) {  // the largest element in [2^6, 2^7)
+        return power_of_2(min(max(6 - ((sm.query_size[t][of] >> 23) - 127), -120), 120));
+      };
+      auto queries = [&](auto type, auto wide_tag) {
         using T = decltype(type);
-        const T* x = static_cast<const T*>(a.queries) + from;
-        auto get = [&](int at, float (&e)[8]) {
-          if (real && a.q_wide && at < a.dim) {
+        constexpr bool kVectors = decltype(wide_tag)::value;
+        // without branches where rows are vectors, so that loads are in flight together
+        auto get = [&](int k, int& of, int& at, float (&e)[8]) {
+          const int i = k * kWideTile + row;
+          of = i / (4 * G);
+          at = i % (4 * G);
+          const bool there = t * kWideTile + of < cols && 8 * at < a.dim;
+          const int c = first_col + (there ? t * kWideTile + of : 0), of_token = (int)a.group((uint32_t)c);
+          const T* x = static_cast<const T*>(a.queries) + (int64_t)(q.first + of_token) * a.q_token +
+                       (h * group + c - of_token * group) * a.q_head + (there ? 8 * at : 0);
+          if constexpr (kVectors) {
             Vec<T, 8> v;
-            v.template load<true>(x + at);
+            v.template load<true>(x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = to_f32(v.x[i]);
+            for (int j = 0; j < 8; ++j) e[j] = there ? to_f32(v.x[j]) : 0.f;
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = real && at + i < a.dim ? to_f32(x[at + i]) : 0.f;
+            for (int j = 0; j < 8; ++j) e[j] = there && 8 * at + j < a.dim ? to_f32(x[j]) : 0.f;
           }
         };
-        float most = 0.f, e[8];
-#pragma unroll 4
-        for (int k = 0; k < 4 * G; ++k) {
-          get(8 * k, e);
+        constexpr int kAtOnce = kVectors ? 4 : 1;
+        int of[kAtOnce], at[kAtOnce];
+        float e[kAtOnce][8];
+        for (int k0 = 0; k0 < 4 * G; k0 += kAtOnce) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(e[i]));
+          for (int k = 0; k < kAtOnce; ++k) get(k0 + k, of[k], at[k], e[k]);
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(e[k][j]));
+            atomicMax(&sm.query_size[t][of[k]], __float_as_int(most));
+          }
         }
-        // the largest element in [2^6, 2^7)
-        const int by = min(max(6 - ((__float_as_int(most) >> 23) - 127), -120), 120);
-        const float scale = power_of_2(by);
-        to_score = fabsf(a.scale) / scale;
-        const float signed_scale = a.scale < 0.f ? -scale : scale;
-        const uint32_t to = smem + Shape::kQueries + t * Shape::kBytes + row * 128;
-#pragma unroll 4
-        for (int k = 0; k < 4 * G; ++k) {
-          get(8 * k, e);
-          uint32_t w[4];
+        meet();
+        const uint32_t to = smem + Shape::kQueries + t * Shape::kBytes;
+        for (int k0 = 0; k0 < 4 * G; k0 += kAtOnce) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack_halves(e[i] * signed_scale, e[i + 4] * signed_scale);
-          const uint32_t at = to + (k >> 3) * Shape::kSub + (((k & 7) ^ (row & 7)) << 4);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
+          for (int k = 0; k < kAtOnce; ++k) get(k0 + k, of[k], at[k], e[k]);
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            const float by = a.scale < 0.f ? -scale_of(of[k]) : scale_of(of[k]);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack_halves(e[k][i] * by, e[k][i + 4] * by);
+            const uint32_t place = to + (at[k] >> 3) * Shape::kSub + of[k] * 128 + (((at[k] & 7) ^ (of[k] & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
         }
       };
-      if (a.q_type == BPE_F16) queries(__half{});
-      else queries(__nv_bfloat16{});
+      if (a.q_type == BPE_F16) {
+        if (a.q_wide) queries(__half{}, std::true_type{});
+        else queries(__half{}, std::false_type{});
+      } else {
+        if (a.q_wide) queries(__nv_bfloat16{}, std::true_type{});
+        else queries(__nv_bfloat16{}, std::false_type{});
+      }
+      to_score = fabsf(a.scale) / scale_of(row);
     }
     publish();
     barrier_arrive(bar(sm.queries_full));
@@ -580,20 +610,59 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
     if (ok) {
       after_sync();
       const float by = total == 0.f ? 0.f : power_of_2(sm.power[1]) / total;
-      const int64_t to = (int64_t)(q.first + token) * a.o_token + head * a.o_head;
+      // 32 columns at a time through shared memory, where the queries are needed no more, so that a row's neighbours
+      // are stored together
+      const uint32_t stage = smem + Shape::kQueries + t * Shape::kBytes + (warp & 3) * 4096;
+      int64_t to[8];  // rows that this thread stores in
+      uint32_t there = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int in_block = t * kWideTile + (warp & 3) * 32 + 4 * i + lane / 8;
+        const int at = first_col + in_block, of_token = (int)a.group((uint32_t)at);
+        to[i] = (int64_t)(q.first + of_token) * a.o_token + (h * group + at - of_token * group) * a.o_head;
+        there |= (uint32_t)(in_block < cols) << i;
+      }
 #pragma unroll
       for (int k = 0; k < G; ++k) {
         uint32_t o[32];
         tmem_load(o, o_at + 32 * k);
         tmem_loaded();
-        if (real) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {  // in the order 0, 4, 1, 5, 2, 6, 3, 7
-            auto e = [&](int i) { return __uint_as_float(o[8 * c + (i % 4) * 2 + i / 4]) * by; };
-            attend_store(a, to, 32 * k + 8 * c, make_float4(e(0), e(1), e(2), e(3)));
-            attend_store(a, to, 32 * k + 8 * c + 4, make_float4(e(4), e(5), e(6), e(7)));
-          }
+        for (int c = 0; c < 8; ++c) {  // in each 8 in the order 0, 4, 1, 5, 2, 6, 3, 7
+          auto e = [&](int i) { return __uint_as_float(o[8 * (c / 2) + 2 * i + c % 2]) * by; };
+          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(stage + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                       "f"(e(0)), "f"(e(1)), "f"(e(2)), "f"(e(3))
+                       : "memory");
         }
+        __syncwarp();
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int of = 4 * i + lane / 8;
+          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(v[i].x), "=f"(v[i].y), "=f"(v[i].z), "=f"(v[i].w)
+                       : "r"(stage + of * 128 + (((lane % 8) ^ (of & 7)) << 4)));
+        }
+        const int at = 32 * k + 4 * (lane % 8);
+        if (a.o_wide && a.out_type != BPE_F32) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint2 w;
+            if (a.out_type == BPE_F16) {
+              w = make_uint2(pack_halves(v[i].x, v[i].y), pack_halves(v[i].z, v[i].w));
+            } else {
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v[i].y), "f"(v[i].x));
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v[i].w), "f"(v[i].z));
+            }
+            if (there >> i & 1 && at < a.dim)
+              __stcs(reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.out) + to[i] + at), w);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (there >> i & 1) attend_store(a, to[i], at, v[i]);
+        }
+        __syncwarp();
       }
       before_sync();
     }
