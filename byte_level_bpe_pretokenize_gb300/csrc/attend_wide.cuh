@@ -19,7 +19,10 @@
 namespace {
 
 constexpr int kWideTile = 128;
-constexpr int kWideThreads = 17 * 32;  // two softmax groups of 4 warps, keys' and values' 4 each, one that issues products
+// Warps: 8 for the softmax of each tile of columns, 4 for each half of 128 tokens; 4 that fill in keys, 4 values; and
+// one that issues products.
+constexpr int kWideSoftmax = 8, kWideFill = 16, kWideIssue = 24;
+constexpr int kWideThreads = 25 * 32;
 constexpr uint64_t kPatience = 2000000000;  // nanoseconds of a wait, which lasts microseconds
 
 __device__ __forceinline__ void barrier_init(uint32_t at, uint32_t count) {
@@ -175,125 +178,124 @@ struct WideShared {
   uint32_t tmem;
   int power[2];      // of keys and of values: they are stored in units of 2^power
   float largest[2][4];
+  float half_row[2][2][kWideTile];  // of each tile: what the halves of a row tell each other
   int query_size[2][kWideTile];  // the largest element of a column's query, as bits
   int gave_up;
 };
 
-// Keys (or values) of 128 tokens at a time, a thread a token: codes to halves.
-// A code gets the exponent of 1024 before it, becomes n by one exact operation,
-// and base + step n by another that rounds.
+// Keys (or values) of 128 tokens at a time, a thread a token, 64 elements after
+// another with the next ones on their way. A code gets the exponent of 1024
+// before it, becomes n by one exact operation, and base + step n by another that
+// rounds.
 template <int G>
 __device__ void wide_fill(const AttendArgs& a, WideShared& sm, int which, uint32_t tile0, int r, int h, int limit,
                           int n_tiles, int last_tile, int* redo) {
   using Shape = WideShape<G>;
+  constexpr int U = Shape::kSubs;
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const uint32_t full = (uint32_t)__cvta_generic_to_shared(which ? sm.values_full : sm.keys_full);
   const uint32_t free = (uint32_t)__cvta_generic_to_shared(sm.scores_full[last_tile]);
   const unsigned char* pages = a.cache + ((int64_t)which * a.heads + h) * a.page_bytes;
   const int32_t* table = a.table + (int64_t)r * a.table_stride;
-  uint4 codes[G];
-  uint32_t pair[G];
   bool bad = false;
-  auto load = [&](int i) {
+  const unsigned char* codes = nullptr;  // of the token's row, or null
+  const uint32_t* words = nullptr;       // its pairs
+  int32_t entry = -1;
+  auto look_up = [&](int i) {
     const int t = i * kWideTile + tid;
-    int32_t entry = -1;
-    if (t < limit) {
-      entry = __ldg(table + a.block((uint32_t)t));
-      if ((uint32_t)entry >= (uint32_t)a.n_blocks || entry < 0) {
-        entry = -1;
-        bad = true;  // reported by the other kernel, which leaves its tokens out
-      }
-    }
-    if (entry >= 0) {
-      const uint32_t row = (uint32_t)t - a.block((uint32_t)t) * a.block.d;
-      const unsigned char* page = pages + (int64_t)entry * a.block_stride;
-      const uint4* from = reinterpret_cast<const uint4*>(page + (int64_t)row * (16 * G));
-      const uint32_t* words = reinterpret_cast<const uint32_t*>(page + ((int64_t)a.block.d * 16 + (int64_t)row * 4) * G);
-#pragma unroll
-      for (int j = 0; j < G; ++j) codes[j] = __ldg(from + j);
-      if constexpr (G % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < G; j += 4) *reinterpret_cast<uint4*>(pair + j) = __ldg(reinterpret_cast<const uint4*>(words + j));
-      } else {
-#pragma unroll
-        for (int j = 0; j < G; ++j) pair[j] = __ldg(words + j);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        codes[j] = make_uint4(0, 0, 0, 0);
-        pair[j] = 0;
-      }
-    }
+    entry = t < limit ? __ldg(table + a.block((uint32_t)t)) : -1;
   };
-  load(0);
+  auto find = [&](int i) {
+    const int t = i * kWideTile + tid;
+    codes = nullptr;
+    if (t >= limit) return;
+    if ((uint32_t)entry >= (uint32_t)a.n_blocks || entry < 0) {
+      bad = true;  // reported by the other kernel, which leaves its tokens out
+      return;
+    }
+    const uint32_t row = (uint32_t)t - a.block((uint32_t)t) * a.block.d;
+    const unsigned char* page = pages + (int64_t)entry * a.block_stride;
+    codes = page + (int64_t)row * (16 * G);
+    words = reinterpret_cast<const uint32_t*>(page + ((int64_t)a.block.d * 16 + (int64_t)row * 4) * G);
+  };
+  look_up(0);
+  find(0);
   // the unit: the largest of the first 128 tokens becomes 2^6 to 2^7
   float most = 0.f;
 #pragma unroll
-  for (int j = 0; j < G; ++j) most = fmaxf(most, fabsf(bf16_high(pair[j])) + 16.f * bf16_low(pair[j]));
+  for (int j = 0; j < G; ++j) {
+    const uint32_t z = codes ? __ldg(words + j) : 0;
+    most = fmaxf(most, fabsf(bf16_high(z)) + 16.f * bf16_low(z));
+  }
   if (!(most < INFINITY)) most = 0.f;
   most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
   if (lane == 0) sm.largest[which][tid >> 5] = most;
   asm volatile("bar.sync %0, 128;" ::"r"(1 + which) : "memory");
 #pragma unroll
   for (int w = 0; w < 4; ++w) most = fmaxf(most, sm.largest[which][w]);
-  const int power = min(max((__float_as_int(most) >> 23) - 127 - 6, -100), 100);
-  if (tid == 0) sm.power[which] = most > 0.f ? power : 0;
-  const float unit = power_of_2(most > 0.f ? -power : 0);
+  const int power = most > 0.f ? min(max((__float_as_int(most) >> 23) - 127 - 6, -100), 100) : 0;
+  if (tid == 0) sm.power[which] = power;
+  const float unit = power_of_2(-power);
   barrier_arrive((uint32_t)__cvta_generic_to_shared(&sm.units_full));
 
+  uint4 next[2];
+  uint32_t next_pair[2];
+  auto load = [&](int u) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool there = codes && 2 * u + k < G;
+      next[k] = there ? __ldg(reinterpret_cast<const uint4*>(codes) + 2 * u + k) : make_uint4(0, 0, 0, 0);
+      next_pair[k] = there ? __ldg(words + 2 * u + k) : 0;
+    }
+  };
+  load(0);
+  if (n_tiles > 1) look_up(1);
+  const __half2 less = __float2half2_rn(-1024.f), by = __float2half2_rn(0.0625f), less16 = __float2half2_rn(-64.f);
   for (int i = 0; i < n_tiles; ++i) {
     const int stage = i % Shape::kStages;
-    uint4 now[G];
-    uint32_t z[G];
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      now[j] = codes[j];
-      z[j] = pair[j];
-    }
-    if (i + 1 < n_tiles) load(i + 1);
-    if (i >= Shape::kStages) {  // which step's scores say that the stage is free
-      const int by = i - Shape::kStages + which;
-      if (!barrier_wait(free + 8 * (by & 1), by >> 1 & 1, &sm.gave_up)) return;
-    }
     const uint32_t to = tile0 + stage * Shape::kBytes + tid * 128;
-    __half2 st[G], ba[G];
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const float s = bf16_low(z[j]) * unit, b = bf16_high(z[j]) * unit, size = fabsf(b) + 16.f * s;
-      // too large for halves or no number; of values also too small for what is left of their bits
-      if (!(size < 32768.f) || (which && size > 0.f && size < 0x1p-9f)) bad = true;
-      st[j] = __float2half2_rn(s);
-      ba[j] = __float2half2_rn(b);
-    }
-    const __half2 less = __float2half2_rn(-1024.f), by = __float2half2_rn(0.0625f), less16 = __float2half2_rn(-64.f);
-    auto convert = [&](uint32_t w, int j, int chunk) {  // chunk: of 8 elements, in the row
-      uint32_t out[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t x = e < 2 ? w : w >> 8;
-        const uint32_t y = (x & (e & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-        const __half2 n = e & 1 ? __hfma2(*reinterpret_cast<const __half2*>(&y), by, less16)
-                                : __hadd2(*reinterpret_cast<const __half2*>(&y), less);
-        const __half2 v = __hfma2(n, st[j], ba[j]);
-        out[e] = *reinterpret_cast<const uint32_t*>(&v);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t now[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
+      const uint32_t z[2] = {next_pair[0], next_pair[1]};
+      if (u + 1 < U) {
+        load(u + 1);
+      } else if (i + 1 < n_tiles) {
+        find(i + 1);
+        load(0);
+        if (i + 2 < n_tiles) look_up(i + 2);
       }
-      const uint32_t at = to + (chunk >> 3) * Shape::kSub + (((chunk & 7) ^ (tid & 7)) << 4);
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(out[0]), "r"(out[1]), "r"(out[2]), "r"(out[3])
-                   : "memory");
-    };
+      if (u == 0 && i >= Shape::kStages) {  // which step's scores say that the stage is free
+        const int step = i - Shape::kStages + which;
+        if (!barrier_wait(free + 8 * (step & 1), step >> 1 & 1, &sm.gave_up)) return;
+      }
+      __half2 st[2], ba[2];
 #pragma unroll
-    for (int k = 0; k < G; ++k) {  // the row's 16-byte pieces
-      const uint32_t w[4] = {now[k].x, now[k].y, now[k].z, now[k].w};
+      for (int k = 0; k < 2; ++k) {
+        const float x = bf16_low(z[k]) * unit, y = bf16_high(z[k]) * unit, size = fabsf(y) + 16.f * x;
+        // too large for halves or no number; of values also too small for what is left of their bits
+        if (!(size < 32768.f) || (which && size > 0.f && size < 0x1p-9f)) bad = true;
+        st[k] = __float2half2_rn(x);
+        ba[k] = __float2half2_rn(y);
+      }
+      const bool pair = 2 * u + 1 < G;  // else a group by itself
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int u = k / 2;
-        if (2 * u + 1 < G) {  // words of two groups in turn
-          const int word = (k % 2) * 4 + e, c = word / 2, half = word % 2;
-          convert(w[e], (2 * u + half) % G, 8 * u + 4 * half + c);
-        } else {
-          convert(w[e], k, 8 * u + e);
+      for (int w = 0; w < 8; ++w) {
+        if (!pair && w >= 4) break;
+        const int k = pair ? w & 1 : 0, chunk = pair ? 4 * (w & 1) + w / 2 : w;  // group, and 8 elements of 64
+        uint32_t out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = e < 2 ? now[w] : now[w] >> 8;
+          const uint32_t y = (x & (e & 1 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+          const __half2 n = e & 1 ? __hfma2(*reinterpret_cast<const __half2*>(&y), by, less16)
+                                  : __hadd2(*reinterpret_cast<const __half2*>(&y), less);
+          const __half2 v = __hfma2(n, st[k], ba[k]);
+          out[e] = *reinterpret_cast<const uint32_t*>(&v);
         }
+        const uint32_t at = to + u * Shape::kSub + ((chunk ^ (tid & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(out[0]), "r"(out[1]), "r"(out[2]), "r"(out[3])
+                     : "memory");
       }
     }
     publish();
@@ -358,16 +360,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
       barrier_init(at(sm.values_full[s]), 128);
       barrier_init(at(sm.scores_full[s][0]), 1);
       barrier_init(at(sm.scores_full[s][1]), 1);
-      barrier_init(at(sm.weights_full[s]), 128);
+      barrier_init(at(sm.weights_full[s]), 256);
       barrier_init(at(sm.results_full[s]), 1);
     }
-    barrier_init(at(sm.queries_full), 128 * Shape::kTiles);
+    barrier_init(at(sm.queries_full), 256 * Shape::kTiles);
     barrier_init(at(sm.units_full), 256);
     barrier_init(at(sm.drained), 1);
     sm.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) {
+  if (warp == kWideIssue) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&sm.tmem))
                  : "memory");
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
 
   if (n_tiles == 0) {
     // nothing is seen: zeros below
-  } else if (warp == 16) {
+  } else if (warp == kWideIssue) {
     constexpr uint32_t kToScores = 1u << 4 | (kWideTile / 8) << 17 | (kWideTile / 16) << 24;
     constexpr uint32_t kToResults = 1u << 4 | 1u << 16 | (uint32_t)(Shape::kDim / 8) << 17 | (kWideTile / 16) << 24;
     const uint32_t queries = matrix_at(smem + Shape::kQueries, 16), keys = matrix_at(smem + Shape::kKeys, 16);
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
           const uint32_t d = tmem + Shape::kResultsAt + t * Shape::kDim, w = tmem + Shape::kScoresAt + t * kWideTile;
 #pragma unroll
           for (int k = 0; k < kWideTile / 16; ++k)
-            product_tmem(d, w + k * 8, vs + k * 2048 / 16, kToResults, i > 0 || k > 0);
+            product_tmem(d, w + k / 4 * 64 + k % 4 * 8, vs + k * 2048 / 16, kToResults, i > 0 || k > 0);
           if (i + 1 < n_tiles) {
             if (t == 0) {
               ok = barrier_wait(bar(sm.keys_full[next]), (i + 1) / Shape::kStages & 1, &sm.gave_up);
@@ -440,25 +442,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
       }
     }
     __syncwarp();
-  } else if (warp >= 8) {
-    const int which = (warp - 8) / 4;
+  } else if (warp >= kWideFill) {
+    const int which = (warp - kWideFill) / 4;
     wide_fill<G>(a, sm, which, smem + (which ? Shape::kValues : Shape::kKeys), r, h, limit, n_tiles, tiles - 1, redo);
-  } else if (warp / 4 >= tiles) {
-    if (warp / 4 < Shape::kTiles) barrier_arrive(bar(sm.queries_full));
+  } else if (warp / kWideSoftmax >= tiles) {
+    if (warp / kWideSoftmax < Shape::kTiles) barrier_arrive(bar(sm.queries_full));
   } else {
-    // ---- a thread a column ----
-    const int t = warp / 4, row = tid & 127, col = first_col + t * kWideTile + row;
+    // ---- two threads a column: each has half of every 128 tokens, and of the results ----
+    const int t = warp / kWideSoftmax, half = warp >> 2 & 1, row = tid & 127, col = first_col + t * kWideTile + row;
     const bool real = t * kWideTile + row < cols;
     const int token = (int)a.group((uint32_t)col);
     const int sees = real ? max(0, q.len - q.fresh + token + 1) : 0;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // of tensor memory
-    const uint32_t s_at = tmem + lanes + Shape::kScoresAt + t * kWideTile;
+    const uint32_t s_at = tmem + lanes + Shape::kScoresAt + t * kWideTile + half * 64;
     const uint32_t o_at = tmem + lanes + Shape::kResultsAt + t * Shape::kDim;
+    float* const mine = &sm.half_row[t][half][row];
+    const float* const other = &sm.half_row[t][1 - half][row];
+    auto meet = [&] { asm volatile("bar.sync %0, 256;" ::"r"(3 + t) : "memory"); };  // all threads of the tile
     float to_score;
     {
       // The tile's queries, 8 elements a thread at a time, neighbours in a row: read once for each row's largest
       // element, and again, from the caches, to be scaled and stored.
-      auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(3 + t) : "memory"); };
+      const int in_tile = tid & 255;
       sm.query_size[t][row] = 0;
       meet();
       auto scale_of = [&](int of) {  // the largest element in [2^6, 2^7)
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
         constexpr bool kVectors = decltype(wide_tag)::value;
         // without branches where rows are vectors, so that loads are in flight together
         auto get = [&](int k, int& of, int& at, float (&e)[8]) {
-          const int i = k * kWideTile + row;
+          const int i = k * 256 + in_tile;
           of = i / (4 * G);
           at = i % (4 * G);
           const bool there = t * kWideTile + of < cols && 8 * at < a.dim;
@@ -486,10 +491,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
             for (int j = 0; j < 8; ++j) e[j] = there && 8 * at + j < a.dim ? to_f32(x[j]) : 0.f;
           }
         };
-        constexpr int kAtOnce = kVectors ? 4 : 1;
+        constexpr int kAtOnce = kVectors && G % 2 == 0 ? 4 : kVectors ? 2 : 1;
         int of[kAtOnce], at[kAtOnce];
         float e[kAtOnce][8];
-        for (int k0 = 0; k0 < 4 * G; k0 += kAtOnce) {
+        for (int k0 = 0; k0 < 2 * G; k0 += kAtOnce) {
 #pragma unroll
           for (int k = 0; k < kAtOnce; ++k) get(k0 + k, of[k], at[k], e[k]);
 #pragma unroll
@@ -497,12 +502,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
             float most = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(e[k][j]));
-            atomicMax(&sm.query_size[t][of[k]], __float_as_int(most));
+            if constexpr (32 % (4 * G) == 0) {  // a row's threads are neighbours
+#pragma unroll
+              for (int d = 1; d < 4 * G; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+              if (at[k] == 0) sm.query_size[t][of[k]] = __float_as_int(most);
+            } else {
+              atomicMax(&sm.query_size[t][of[k]], __float_as_int(most));
+            }
           }
         }
         meet();
         const uint32_t to = smem + Shape::kQueries + t * Shape::kBytes;
-        for (int k0 = 0; k0 < 4 * G; k0 += kAtOnce) {
+        for (int k0 = 0; k0 < 2 * G; k0 += kAtOnce) {
 #pragma unroll
           for (int k = 0; k < kAtOnce; ++k) get(k0 + k, of[k], at[k], e[k]);
 #pragma unroll
@@ -532,44 +543,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
     to_score *= power_of_2(sm.power[0]);
     // weights are 2^6 at the reference, which follows the maximum only when it is 2^8 behind
     float reference = -INFINITY, total = 0.f;
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      ok = barrier_wait(bar(sm.scores_full[t][i & 1]), i >> 1 & 1, &sm.gave_up);
-      if (!ok) break;
+    for (int i = 0; i < n_tiles; ++i) {  // to the end even where a wait gave up: the threads of a tile meet in each step
+      ok = ok && barrier_wait(bar(sm.scores_full[t][i & 1]), i >> 1 & 1, &sm.gave_up);
+      ok = __all_sync(0xFFFFFFFFu, ok);
       after_sync();
-      const int left = sees - i * kWideTile;  // tokens of these that the column sees
-      const bool all = __all_sync(0xFFFFFFFFu, left >= kWideTile);
+      const int left = sees - i * kWideTile - half * 64;  // tokens of this half that the column sees
+      const bool all = __all_sync(0xFFFFFFFFu, left >= 64);
       // the scores, 16 at a time, the next ones on their way
       auto scores = [&](auto use) {
         uint32_t s[2][16];
         tmem_load16(s[0], s_at);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           tmem_loaded();
-          if (k < 7) tmem_load16(s[(k + 1) & 1], s_at + 16 * (k + 1));
+          if (k < 3) tmem_load16(s[(k + 1) & 1], s_at + 16 * (k + 1));
           use(k, s[k & 1]);
         }
       };
       float most = -INFINITY;
-      if (all) {
+      if (ok && all) {
         scores([&](int, const uint32_t* s) {
 #pragma unroll
           for (int j = 0; j < 16; j += 2) most = max_three(most, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
         });
-      } else {
+      } else if (ok) {
         scores([&](int k, const uint32_t* s) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (16 * k + j < left) most = fmaxf(most, __uint_as_float(s[j]));
         });
       }
-      most *= to_score;
+      *mine = most;
+      meet();
+      if (!ok) continue;
+      most = fmaxf(most, *other) * to_score;
       if (__any_sync(0xFFFFFFFFu, most > reference + 8.f)) {
         const float next = fmaxf(reference, most), f = next > reference ? exp2_fast(reference - next) : 1.f;
         total *= f;
         reference = next;
         if (i > 0) {
-#pragma unroll
-          for (int k = 0; k < G; ++k) {
+          for (int k = half; k < G; k += 2) {
             uint32_t o[32];
             tmem_load(o, o_at + 32 * k);
             tmem_loaded();
@@ -606,13 +619,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
       before_sync();
       barrier_arrive(bar(sm.weights_full[t]));
     }
+    meet();  // what the halves told each other is read
+    *mine = total;
+    meet();
+    total += *other;
     ok = ok && barrier_wait(bar(sm.results_full[t]), 0, &sm.gave_up);
-    if (ok) {
+    if (__all_sync(0xFFFFFFFFu, ok)) {
       after_sync();
       const float by = total == 0.f ? 0.f : power_of_2(sm.power[1]) / total;
       // 32 columns at a time through shared memory, where the queries are needed no more, so that a row's neighbours
       // are stored together
-      const uint32_t stage = smem + Shape::kQueries + t * Shape::kBytes + (warp & 3) * 4096;
+      constexpr bool kBoth = Shape::kBytes >= 8 * 4096;  // room for both halves' threads
+      const uint32_t stage = smem + Shape::kQueries + t * Shape::kBytes + (warp & (kBoth ? 7 : 3)) * 4096;
       int64_t to[8];  // rows that this thread stores in
       uint32_t there = 0;
 #pragma unroll
@@ -622,8 +640,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
         to[i] = (int64_t)(q.first + of_token) * a.o_token + (h * group + at - of_token * group) * a.o_head;
         there |= (uint32_t)(in_block < cols) << i;
       }
-#pragma unroll
-      for (int k = 0; k < G; ++k) {
+      for (int k = kBoth || !half ? half : G; k < G; k += kBoth ? 2 : 1) {
         uint32_t o[32];
         tmem_load(o, o_at + 32 * k);
         tmem_loaded();
@@ -677,7 +694,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
   __syncthreads();
   if (tid == 0 && sm.gave_up) atomicOr(&a.small->op_status, kStTimeout);
   after_sync();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == kWideIssue) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 }  // namespace
