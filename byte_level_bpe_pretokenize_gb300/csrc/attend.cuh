@@ -221,14 +221,15 @@ struct AttendShape {
   static constexpr int kStage = 2 * kHalfStage;
   static constexpr int kScores = NT * kUnit * 8 * 4;
   static constexpr int kSteps = G * kUnit * 2;                       // values' steps as halves, and mids likewise
-  // As many warps an SM as registers allow: 8 x 2 of 128, 6 x 2 of 168 or 8 of 255. The queries, which only the first half of a
-  // step needs, stay in shared memory where it has room for them.
+  // As many warps an SM as registers allow: 8 x 2 of 128, 6 x 2 of 168 or 8 of 255. The queries, which only the first
+  // half of a step needs, stay in shared memory where it has room for them.
   static constexpr bool kSmall = G <= 4 && NT == 1 && kParts == 1;
+  static constexpr bool kMiddle = kParts == 1 && (NT == 1 ? G == 3 || G == 4 : G <= 2);
   static constexpr bool kQueriesShared = kParts == 1 && G <= 6;
   static constexpr int kQueries = kQueriesShared ? NT * G * 512 : 0;
   static constexpr int kWarp = 2 * kStage + kScores + (1 + kParts) * kSteps + kQueries;
-  static constexpr int kBlocks = kSmall ? 2 : 1;
-  static constexpr int kWarps = kSmall && G == 4 ? 6 : 8;
+  static constexpr int kBlocks = kSmall || kMiddle ? 2 : 1;
+  static constexpr int kWarps = kMiddle ? 6 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kSmem = kWarps * kWarp;
   static constexpr int kPartial = kCols * (32 * G + 2);              // floats of an item's partial sums

@@ -49,10 +49,11 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
     const int64_t groups = cache_groups(p.dim);
     const size_t records = align256((size_t)h->n_sms * kAttMaxWarps * 2 * sizeof(int4));
     const size_t partials = align256((size_t)h->n_sms * BPE_ATTEND_PARTIALS * (32 * groups + 2) * sizeof(float));
-    // The host knows how many columns there are, not whose. Few in all and few a request (drafted tokens of many
-    // requests): that one has kWideMin of them is not worth the launch, 10 us.
+    // The host knows how many columns there are, not whose. Where all heads' are below 8192, long runs keep too few
+    // SMs busy (2 requests of 256 behind 4,000 tokens, 8 heads: 110 us, here 83; 2 of 512: 109 and 144). Few a request
+    // (drafted tokens of many): that one has kWideMin of them is not worth the launch, 10 us.
     const int64_t columns = p.n_tokens * p.group;
-    const bool wide = p.query_type != BPE_F32 && p.offsets && columns >= kWideMin &&
+    const bool wide = p.query_type != BPE_F32 && p.offsets && columns >= kWideMin && columns * p.n_heads >= 8192 &&
                       (columns >= 4096 || columns >= 16 * p.n_requests);
     rc = ensure_ws(h, records + partials + (wide ? (size_t)p.n_requests * sizeof(int) : 0), st);
     if (rc) return rc;
@@ -87,6 +88,8 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
         });
         if (ok) return ok;
         using Shape = AttendShape<G, P, NT>;
+        static_assert(Shape::kBlocks * Shape::kWarps * 2 * Shape::kCols <= BPE_ATTEND_PARTIALS &&
+                      Shape::kBlocks * Shape::kWarps <= kAttMaxWarps, "the workspace");
         const unsigned blocks = (unsigned)(h->n_sms * Shape::kBlocks);
         k_attend<P, G, NT><<<blocks, Shape::kThreads, kSmem, st>>>(a);
         CK(cudaGetLastError());

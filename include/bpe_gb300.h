@@ -584,7 +584,7 @@ int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, cons
  * group <= 256. Workspace: partial sums, at most BPE_ATTEND_PARTIALS * multiprocessors * (dim + 2) * 4
  * bytes (dim rounded up to 32, 64, 96, 128, 192 or 256), for any lengths.
  */
-#define BPE_ATTEND_PARTIALS 256
+#define BPE_ATTEND_PARTIALS 384
 typedef struct bpe_attend_args {
   const void* queries;
   void* out;
