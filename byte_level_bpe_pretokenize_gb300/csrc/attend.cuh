@@ -19,7 +19,7 @@ namespace {
 constexpr int kUnit = 32;      // tokens of a step
 constexpr int kItemCost = 3;   // what beginning and ending an item takes, in steps
 constexpr int kAttMaxWarps = 16;  // workers of an SM
-constexpr int kWideMin = 64;      // columns of a request from which attend_wide.cuh takes it
+constexpr int kWideMin = BPE_ATTEND_LONG;  // columns of a request from which attend_wide.cuh takes it
 
 struct AttendArgs {
   const void* queries;
@@ -265,7 +265,6 @@ __device__ __forceinline__ void attend_store(const AttendArgs& a, int64_t row, i
   else if (a.out_type == BPE_F16) put(__half{});
   else put(__nv_bfloat16{});
 }
-
 
 // A warp is a worker: it walks its share of the steps with the next step's codes
 // on their way into its own half of shared memory, and waits for no other warp.

@@ -571,9 +571,14 @@ int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, cons
  *   offsets        int64[n_requests + 1]: request r's new tokens are
  *                  [offsets[r], offsets[r + 1]). NULL: one each (a decode
  *                  step; n_tokens is then n_requests at least).
- * Sums and the softmax are in 32 bits. Products run on the tensor cores with
- * codes, which are exact there, and with queries and weights cut into parts of
- * bfloat16: queries without loss, weights to 2^-17 (f32: 2^-25) of their value.
+ * Sums and the softmax are in 32 bits. Products run on the tensor cores in
+ * halves: codes, and 16-bit queries scaled by a power of two, without loss;
+ * weights to 2^-11 of theirs; 32-bit queries and weights in two parts, to 2^-23.
+ * In long runs of new tokens (16-bit queries; BPE_ATTEND_LONG columns of a
+ * request, a column being a query head of a token, and 8192 of all heads) keys
+ * and values are halves too, to 2^-12 of theirs; a request whose cache has NaNs,
+ * infinities or sizes 2^15 apart is computed as short runs are. So what a token
+ * may not see changes nothing in its result but the last bits.
  * Left out and reported (BPE_ERR_BAD_INPUT): requests whose offsets are not
  * monotone in [0, n_tokens] (their rows are left as they are), those with a
  * length outside [0, max_blocks * block_size], or
@@ -581,9 +586,11 @@ int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, cons
  * is outside the cache (not seen). Where offsets fall, rows that several
  * requests share hold what one of them gives.
  * Sizes: n_requests and n_tokens < 2^31 - 1, n_tokens * n_heads * group < 2^31,
- * group <= 256. Workspace: partial sums, at most BPE_ATTEND_PARTIALS * multiprocessors * (dim + 2) * 4
- * bytes (dim rounded up to 32, 64, 96, 128, 192 or 256), for any lengths.
+ * group <= 256. Workspace: partial sums, at most BPE_ATTEND_PARTIALS *
+ * multiprocessors * (dim + 2) * 4 bytes (dim rounded up to 32, 64, 96, 128, 192
+ * or 256) for any lengths, 512 bytes a multiprocessor and 4 a request.
  */
+#define BPE_ATTEND_LONG 64
 #define BPE_ATTEND_PARTIALS 384
 typedef struct bpe_attend_args {
   const void* queries;
