@@ -150,17 +150,6 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool t
   }
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-  return v;
-}
-
 // Cuts x and y into kParts halves each that add up to them: two leave 2^-24 of a
 // number that stays above 2^-2.
 template <int kParts>
@@ -371,7 +360,10 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     asm volatile("mov.b32 %0, %1;" : "=r"(minus8[i]) : "r"(i & 1 ? kMinus8Odd : kMinus8Even));
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * Shape::kWarp;
+  // places in shared memory, from its first byte on
+  const uint32_t smem_at = (uint32_t)__cvta_generic_to_shared(smem), ring = warp * Shape::kWarp;
+  auto lds64 = [&](uint32_t at) { return *reinterpret_cast<const uint2*>(smem + at); };
+  auto lds32 = [&](uint32_t at) { return *reinterpret_cast<const uint32_t*>(smem + at); };
   const uint32_t scores = ring + 2 * Shape::kStage, steps = scores + Shape::kScores;
 
   // ---- the copies of a step, one ahead of its use ----
@@ -413,7 +405,7 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
     if (!there && t < ahead_len) atomicOr(&a.small->op_status, kStBadInput);
     const uint32_t row = (uint32_t)t - a.block((uint32_t)t) * a.block.d;
     const uint32_t all = __ballot_sync(0xFFFFFFFFu, there);
-    const uint32_t to = ring + stage * Shape::kStage;
+    const uint32_t to = smem_at + ring + stage * Shape::kStage;
     // Addresses are counted in 16 bytes from the cache's first, in 32 bits where it is below 64 GB.
     auto get = [&](auto type, auto whole_tag) {
       using T = decltype(type);
@@ -526,9 +518,8 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
           for (int p = 0; p < P; ++p) q_kept[n][j][p][i] = part[p];
         }
         if (Shape::kQueriesShared)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(queries + (n * G + j) * 512), "r"(q_kept[n][j][0][0]),
-                       "r"(q_kept[n][j][0][1]), "r"(q_kept[n][j][0][2]), "r"(q_kept[n][j][0][3])
-                       : "memory");
+          *reinterpret_cast<uint4*>(smem + queries + (n * G + j) * 512) =
+              make_uint4(q_kept[n][j][0][0], q_kept[n][j][0][1], q_kept[n][j][0][2], q_kept[n][j][0][3]);
       }
       // the products of bases: part s / U of the sums of groups 2 (s % U) and the next, in place s
 #pragma unroll
@@ -569,9 +560,8 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         if (Shape::kQueriesShared) {
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(q[n][j][0][0]), "=r"(q[n][j][0][1]), "=r"(q[n][j][0][2]), "=r"(q[n][j][0][3])
-                       : "r"(queries + (n * G + j) * 512));
+          const uint4 w = *reinterpret_cast<const uint4*>(smem + queries + (n * G + j) * 512);
+          q[n][j][0][0] = w.x, q[n][j][0][1] = w.y, q[n][j][0][2] = w.z, q[n][j][0][3] = w.w;
         } else {
 #pragma unroll
           for (int p = 0; p < P; ++p)
@@ -669,8 +659,8 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t to = scores + n * (kUnit * 32) + c * 8;
-        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + k0 * 32), "f"(s[n][0]), "f"(s[n][1]) : "memory");
-        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + k1 * 32), "f"(s[n][2]), "f"(s[n][3]) : "memory");
+        *reinterpret_cast<float2*>(smem + to + k0 * 32) = make_float2(s[n][0], s[n][1]);
+        *reinterpret_cast<float2*>(smem + to + k1 * 32) = make_float2(s[n][2], s[n][3]);
       }
     }
     // the pairs of values of token `lane`, meanwhile
@@ -790,11 +780,11 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
         }
         const uint32_t to = steps + j * (kUnit * 2) + place;
         const __half wh = __float2half_rn(w), mh = __float2half_rn(m);
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(__half_as_ushort(wh)) : "memory");
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + Shape::kSteps), "h"(__half_as_ushort(mh)) : "memory");
+        *reinterpret_cast<__half*>(smem + to) = wh;
+        *reinterpret_cast<__half*>(smem + to + Shape::kSteps) = mh;
         if (P == 2) {
           const __half ml = __float2half_rn(m - __half2float(mh));
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * Shape::kSteps), "h"(__half_as_ushort(ml)) : "memory");
+          *reinterpret_cast<__half*>(smem + to + 2 * Shape::kSteps) = ml;
         }
       }
       __syncwarp();
