@@ -828,7 +828,7 @@ class Tokenizer:
         if two != 2 or page != want:
             raise ValueError(f"cache: {tuple(cache.shape)}, need [blocks, 2, heads, {want}] for blocks of {block_size} "
                              f"slots and rows of {dim}")
-        if s3 != 1 or s2 != page or s1 != heads * page:
+        if s3 != 1 or (s2 != page and heads > 1) or s1 != heads * page:
             raise ValueError("cache: the pages of a block must be adjacent")
         return cache.data_ptr(), n_blocks, block_stride, heads
 

@@ -137,6 +137,50 @@ def test_long_runs_of_new_tokens(tok, dtype, heads, group, dim, block, share):
     assert bool((got == b.run(tok)).all())
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.0, -0.4, 0.01])
+def test_long_runs_scale(tok, scale):
+    b = Batch([200, 330], 16, 1, 64, 16, new=[200, 330], seed=21)
+    b.check(b.run(tok, scale=scale), scale)
+
+
+def test_long_runs_with_sharp_scores(tok):
+    """Scores hundreds apart: results are scaled as the maximum grows."""
+    b = Batch([600, 200], 16, 1, 64, 16, "float16", new=[330, 190], seed=22, by=40.0)
+    b.check(b.run(tok))
+
+
+def test_long_runs_that_see_little(tok):
+    """Requests that were not served, or only in part: tokens that see nothing get zeros."""
+    b = Batch([0, 100, 300, 0], 16, 1, 32, 16, new=[128, 250, 64, 130], seed=23)
+    got = b.run(tok)
+    b.check(got)
+    assert not bool(got[:128 + 150].any()) and bool(got[128 + 150].any())
+
+
+def test_long_runs_of_strided_queries_and_results(tok):
+    import torch
+    heads, dim = 16, 64
+    b = Batch([300, 260], heads, 1, dim, 16, new=[300, 230], seed=24)
+    want = b.run(tok)
+    q = b.q
+    for start in (0, 1, 4):  # aligned and not
+        wide = torch.zeros(530, (heads + 2) * dim + 3, dtype=q.dtype)
+        b.q = wide[:, start:start + heads * dim].unflatten(1, (heads, dim))
+        b.q.copy_(q)
+        out = torch.full((530, (heads + 2) * dim + 3), 7.0, dtype=q.dtype, device="cuda")
+        y = out[:, start:start + heads * dim].unflatten(1, (heads, dim))
+        given = wide.cuda()[:, start:start + heads * dim].unflatten(1, (heads, dim))
+        got = tok.attend(given, torch.from_numpy(b.cache).cuda(), torch.from_numpy(b.table).cuda(),
+                         torch.from_numpy(b.lens.astype(np.int32)).cuda(), 16, offsets=torch.from_numpy(b.offsets).cuda(),
+                         out=y)
+        assert got is y and torch.equal(y, want)
+        out[:, start:start + heads * dim] = 7.0
+        assert bool((out == 7.0).all())
+    b.q = q
+    assert b.run(tok, dtype=torch.float32).dtype is torch.float32
+    b.check(b.run(tok, dtype=torch.float32))
+
+
 def test_long_runs_with_values_far_apart(tok):
     """What halves do not hold in one unit is computed in 32 bits: tokens of sizes 2^40 apart, seen by some."""
     b = Batch([400, 300], 12, 2, 64, 16, new=[150, 200], seed=3)
