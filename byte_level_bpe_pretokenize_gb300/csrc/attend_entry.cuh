@@ -100,17 +100,25 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
       constexpr std::integral_constant<int, 2> two{};
       if (p.query_type == BPE_F32) return launch(two, one);
       if (wide) {
-        using Wide = WideShape<G>;
-        int ok = once_per_device(h->device, [&] {
-          return cudaFuncSetAttribute(k_attend_wide<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::kSmem);
-        });
-        if (ok) return ok;
         CK(cudaMemsetAsync(redo, 0, (size_t)p.n_requests * sizeof(int), st));
-        // as many blocks as requests of kWideMin columns on can need
-        const int64_t at_once = Wide::kTiles * kWideTile;
-        const int64_t blocks = (columns / at_once + std::min(p.n_requests, columns / kWideMin)) * p.n_heads;
-        k_attend_wide<G><<<(unsigned)std::min<int64_t>(blocks, INT32_MAX), kWideThreads, Wide::kSmem, st>>>(a, redo);
-        CK(cudaGetLastError());
+        auto launch_wide = [&](auto tiles) -> int {
+          constexpr int T = decltype(tiles)::value;
+          using Wide = WideShape<G, T>;
+          int ok = once_per_device(h->device, [&] {
+            return cudaFuncSetAttribute(k_attend_wide<G, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::kSmem);
+          });
+          if (ok) return ok;
+          // as many blocks as requests of kWideMin columns on can need
+          const int64_t blocks = (columns / (T * kWideTile) + std::min(p.n_requests, columns / kWideMin)) * p.n_heads;
+          k_attend_wide<G, T><<<(unsigned)std::min<int64_t>(blocks, INT32_MAX), kWideThreads, Wide::kSmem, st>>>(a, redo);
+          CK(cudaGetLastError());
+          return BPE_OK;
+        };
+        int ok;
+        // two tiles share what is filled in, one takes less time a step: where blocks of two leave SMs idle
+        if constexpr (G <= 4) ok = columns / (2 * kWideTile) * p.n_heads >= h->n_sms ? launch_wide(two) : launch_wide(one);
+        else ok = launch_wide(one);
+        if (ok) return ok;
         a.redo = redo;
       }
       return two_tiles ? launch(one, two) : launch(one, one);

@@ -14,7 +14,6 @@
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotHeads = 4;  // heads that a thread holds in flight
 constexpr int64_t kRotMaxDim = 65536, kRotMaxHeads = 65536;
 
 struct RotateArgs {
@@ -41,6 +40,7 @@ struct RotateArgs {
 template <class TI, class TO, int V, int A, bool kAdjacent>
 __global__ void __launch_bounds__(kRotThreads) k_rotate(RotateArgs a) {
   constexpr int kPairs = kAdjacent ? V / 2 : V, kVecs = kAdjacent ? 1 : 2;
+  constexpr int kRotHeads = V * sizeof(TI) * kVecs >= 32 ? 4 : 8;  // heads that a thread holds in flight
   const uint32_t index = blockIdx.x * kRotThreads + threadIdx.x;
   if (index >= a.total) return;
   const uint32_t row = a.items(index), item = index - row * a.items.d;
@@ -190,12 +190,15 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
       return with_type(out_type, [&](auto to) -> int {
         using TI = decltype(ti);
         using TO = decltype(to);
-        auto launch = [&](auto width, auto access, auto adjacent) -> int {
+        // elements [from, from + dim) of each head, of which the first 2 * n_pairs turn
+        auto launch = [&](auto width, auto access, auto adjacent, int64_t from, int64_t dim, int64_t n_pairs) -> int {
           constexpr int V = decltype(width)::value, A = decltype(access)::value;
           constexpr bool kAdjacent = decltype(adjacent)::value;
-          const int64_t turning = kAdjacent ? (2 * n_pairs + V - 1) / V : n_pairs / V;
+          int64_t turning = kAdjacent ? (2 * n_pairs + V - 1) / V : n_pairs / V;
           // in place, what is behind the turned part stays
           const int64_t items = same ? turning : kAdjacent ? (dim + V - 1) / V : turning + (dim - 2 * n_pairs) / V;
+          // adjacent pairs that do not turn go with those that do: lanes of a warp have both
+          if (kAdjacent && A == V) turning = items;
           if (items == 0) return BPE_OK;
           // As many threads share a token's heads as give the GPU half of the threads that it holds: with
           // more, sines are computed again, with fewer, loads are too few.
@@ -204,7 +207,8 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
           const int64_t at_once = std::min(n_tokens, (int64_t)INT32_MAX / 2 / (items * shares));
           for (int64_t t = 0; t < n_tokens; t += at_once) {
             const int64_t n = std::min(at_once, n_tokens - t);
-            RotateArgs a{static_cast<const TI*>(d_x) + t * x_token_stride, static_cast<TO*>(d_out) + t * out_token_stride,
+            RotateArgs a{static_cast<const TI*>(d_x) + t * x_token_stride + from,
+                         static_cast<TO*>(d_out) + t * out_token_stride + from,
                          x_token_stride, x_head_stride, out_token_stride, out_head_stride,
                          d_positions ? d_positions + t : nullptr, d_turns, (uint32_t)(n * items * shares),
                          FastDiv(items), FastDiv(shares), (int)n_heads, (int)n_pairs, (int)dim, (int)turning, scale,
@@ -214,29 +218,39 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
           }
           return BPE_OK;
         };
-        auto fits = [&](int64_t V) {
+        auto rows_fit = [&](int64_t V) {
           auto rows = [&](const void* p, int64_t token, int64_t head, int64_t size) {
             return vec_ok(p, n_tokens > 1 ? token : 0, size, V) && vec_ok(p, n_heads > 1 ? head : 0, size, V);
           };
-          return dim % V == 0 && (interleaved || n_pairs % V == 0) &&
-                 rows(d_x, x_token_stride, x_head_stride, sizeof(TI)) &&
+          return dim % V == 0 && rows(d_x, x_token_stride, x_head_stride, sizeof(TI)) &&
                  rows(d_out, out_token_stride, out_head_stride, sizeof(TO));
         };
+        auto fits = [&](int64_t V) { return rows_fit(V) && (interleaved || n_pairs % V == 0); };
         using std::integral_constant;
         constexpr integral_constant<int, 8> c8{};
         constexpr integral_constant<int, 4> c4{};
         constexpr integral_constant<int, 2> c2{};
         constexpr integral_constant<int, 1> c1{};
         if (interleaved) {
-          if (fits(8)) return launch(c8, c8, std::true_type{});
-          if (fits(4)) return launch(c4, c4, std::true_type{});
-          if (fits(2)) return launch(c2, c2, std::true_type{});
-          return launch(c2, c1, std::true_type{});
+          if (fits(8)) return launch(c8, c8, std::true_type{}, 0, dim, n_pairs);
+          if (fits(4)) return launch(c4, c4, std::true_type{}, 0, dim, n_pairs);
+          if (fits(2)) return launch(c2, c2, std::true_type{}, 0, dim, n_pairs);
+          return launch(c2, c1, std::true_type{}, 0, dim, n_pairs);
         }
-        if (fits(8)) return launch(c8, c8, std::false_type{});
-        if (fits(4)) return launch(c4, c4, std::false_type{});
-        if (fits(2)) return launch(c2, c2, std::false_type{});
-        return launch(c1, c1, std::false_type{});
+        if (fits(8)) return launch(c8, c8, std::false_type{}, 0, dim, n_pairs);
+        // Rows are aligned, but not the second halves of their pairs: what is behind the turned part is copied by
+        // itself, where it is enough for a launch.
+        const int64_t behind = (2 * n_pairs + 7) / 8 * 8;
+        if (!same && rows_fit(8) && n_tokens * n_heads * (dim - behind) >= (1 << 20)) {
+          const int rc = launch(c8, c8, std::false_type{}, behind, dim - behind, 0);
+          if (rc) return rc;
+          if (n_pairs % 4 == 0) return launch(c4, c4, std::false_type{}, 0, behind, n_pairs);
+          if (n_pairs % 2 == 0) return launch(c2, c2, std::false_type{}, 0, behind, n_pairs);
+          return launch(c1, c1, std::false_type{}, 0, behind, n_pairs);
+        }
+        if (fits(4)) return launch(c4, c4, std::false_type{}, 0, dim, n_pairs);
+        if (fits(2)) return launch(c2, c2, std::false_type{}, 0, dim, n_pairs);
+        return launch(c1, c1, std::false_type{}, 0, dim, n_pairs);
       });
     });
   });

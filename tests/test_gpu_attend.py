@@ -137,6 +137,15 @@ def test_long_runs_of_new_tokens(tok, dtype, heads, group, dim, block, share):
     assert bool((got == b.run(tok)).all())
 
 
+@pytest.mark.parametrize("dtype,dim,block", [("bfloat16", 128, 16), ("float16", 64, 5), ("bfloat16", 21, 16),
+                                             ("float16", 96, 32)])
+def test_long_runs_of_many_heads(tok, dtype, dim, block):
+    """Enough columns (322 x 8 of 16 heads) for blocks of two tiles of 128 to keep the GPU busy."""
+    new = [128, 1, 129, 64]
+    b = Batch([300, 500, 129, 64], 16, 8, dim, block, dtype, new=new, pad=2, seed=dim)
+    b.check(b.run(tok))
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.0, -0.4, 0.01])
 def test_long_runs_scale(tok, scale):
     b = Batch([200, 330], 16, 1, 64, 16, new=[200, 330], seed=21)
