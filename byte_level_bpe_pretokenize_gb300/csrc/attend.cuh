@@ -265,6 +265,14 @@ __device__ __forceinline__ void attend_store(const AttendArgs& a, int64_t row, i
 // of keys from shared memory in 16 bits, four times the bytes that a code has
 // there.
 //
+// Bound by issue and latency: 370 instructions for 16 tokens of 128 elements (80
+// of them take the codes apart, 25 are products, 45 the copies, 60 the softmax),
+// at 57% of the slots with the 12 warps that 168 registers leave; 8 x 2 warps of
+// 128 registers spill and take 455 us where 6 x 2 take 428, 7 x 2 450. 384
+// requests of 4,000 tokens (8 x 128, 8 query heads each): 417 us, 4.7 TB/s of
+// codes and pairs. Weights in two bfloat16 parts outside the codes' products, and
+// codes as 1 + n / 16, took 868 us.
+//
 // P is 1 for 16-bit queries, which a half holds without loss once they are
 // scaled by a power of two, and 2 for 32-bit ones. Weights are halves too (P of
 // them): 2^-12 of a weight, which is what a result of 11 bits rounds away.

