@@ -71,6 +71,50 @@ __device__ __forceinline__ uint32_t pack_codes(const int (&n)[8]) {
   return w;
 }
 
+// The first n of 16 elements from any address on, by the 16-byte granules that
+// hold them (what else lies in a granule is read, but not used).
+template <class T>
+__device__ __forceinline__ void load_granules(T (&x)[kCacheTake], const T* from, int n) {
+  constexpr int kBytes = kCacheTake * (int)sizeof(T), kGranules = kBytes / 16 + 1, kWords = kBytes / 4 + 1;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(from), first = at & ~(uintptr_t)15, end = at + n * sizeof(T);
+  uint32_t w[4 * kGranules + 3];  // three more, so that every choice below has both sides
+#pragma unroll
+  for (int g = 0; g < kGranules; ++g) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (first + 16 * g < end) v = __ldcs(reinterpret_cast<const uint4*>(first) + g);
+    w[4 * g] = v.x, w[4 * g + 1] = v.y, w[4 * g + 2] = v.z, w[4 * g + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 4 * kGranules; i < 4 * kGranules + 3; ++i) w[i] = 0;
+  const bool one = at & 4, two = at & 8;
+#pragma unroll
+  for (int i = 0; i < kWords + 2; ++i) w[i] = one ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) w[i] = two ? w[i + 2] : w[i];
+  const uint32_t select = at & 2 ? 0x5432 : 0x3210;
+#pragma unroll
+  for (int i = 0; i < kBytes / 4; ++i) {
+    const uint32_t v = sizeof(T) == 2 ? __byte_perm(w[i], w[i + 1], select) : w[i];
+    reinterpret_cast<uint32_t*>(x)[i] = v;
+  }
+}
+
+// 16 halves to any address, in words where they lie in them.
+template <class T>
+__device__ __forceinline__ void store_words(T* to, const T (&x)[kCacheTake]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+  if (reinterpret_cast<uintptr_t>(to) & 2) {
+    to[0] = x[0];
+#pragma unroll
+    for (int i = 0; i < kCacheTake / 2 - 1; ++i)
+      __stcs(reinterpret_cast<unsigned int*>(to + 1) + i, __byte_perm(w[i], w[i + 1], 0x5432));
+    to[kCacheTake - 1] = x[kCacheTake - 1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCacheTake / 2; ++i) __stcs(reinterpret_cast<unsigned int*>(to) + i, w[i]);
+  }
+}
+
 // A thread quantises 16 elements of a key and of a value, two threads a group.
 // Halves of the elements are subtracted, for the difference of two finite ones
 // may pass the largest float, and multiplied by the step's reciprocal, the
@@ -100,10 +144,8 @@ __global__ void __launch_bounds__(kCacheThreads) k_cache_write(CacheArgs a, Cach
 #pragma unroll
       for (int v = 0; v < 2; ++v)
         if (v * 8 < n) reinterpret_cast<Vec<T, 8>*>(x[w])[v].load(row + v * 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kCacheTake; ++e)
-        if (e < n) x[w][e] = row[e];
+    } else if (n > 0) {
+      load_granules(x[w], row, n);
     }
   }
   uint32_t row = 0;
@@ -180,21 +222,22 @@ __global__ void __launch_bounds__(kCacheThreads) k_cache_read(CacheArgs a, Cache
   for (int w = 0; w < 2; ++w) {
     T* out = static_cast<T*>(r.out[w]) + token * r.token[w] + h * r.head[w] + at;
     const float step = bf16_low(pair[w]), base = bf16_high(pair[w]);
+    __align__(16) T y[kCacheTake];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      Vec<T, 8> y;
+    for (int e = 0; e < kCacheTake; ++e) {
+      const float code = __uint_as_float(((codes[w][e / 8] >> (4 * (e % 8))) & 15u) | 0x4B000000u) - 0x1p23f;
+      y[e] = from_f32<T>(base + step * code);
+    }
+    if constexpr (V == 8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float code = __uint_as_float(((codes[w][v] >> (4 * e)) & 15u) | 0x4B000000u) - 0x1p23f;
-        y.x[e] = from_f32<T>(base + step * code);
-      }
-      if constexpr (V == 8) {
-        if (8 * v < n) y.store(out + 8 * v);
-      } else {
+      for (int v = 0; v < 2; ++v)
+        if (8 * v < n) reinterpret_cast<const Vec<T, 8>*>(y)[v].store(out + 8 * v);
+    } else if (sizeof(T) == 2 && n >= kCacheTake) {
+      if constexpr (sizeof(T) == 2) store_words(out, y);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (8 * v + e < n) out[8 * v + e] = y.x[e];
-      }
+      for (int e = 0; e < kCacheTake; ++e)
+        if (e < n) out[e] = y[e];
     }
   }
 }
