@@ -451,6 +451,27 @@ def test_a_cache_past_4_gigabytes(tok):
     assert torch.equal(got, b.run(tok))
 
 
+@pytest.mark.parametrize("new", [None, [300, 290]])
+def test_blocks_far_apart(tok, new):
+    """Two blocks 33 gigabytes apart: addresses that 32 bits do not hold even in units of 16 bytes."""
+    import torch
+    heads, dim, block = 16, 32, 512
+    b = Batch([400, 300], heads, 1, dim, block, new=new, spare=0, seed=8)
+    apart = 33 * 2 ** 30
+    try:
+        room = torch.empty(apart + b.cache[0].size, dtype=torch.uint8, device="cuda")
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("no 33 gigabytes free")
+    page = b.cache.shape[-1]
+    cache = room.as_strided(b.cache.shape, (apart, heads * page, page, 1))
+    cache.copy_(torch.from_numpy(b.cache))
+    k = {} if new is None else {"offsets": torch.from_numpy(b.offsets).cuda()}
+    got = tok.attend(b.q.cuda(), cache, torch.from_numpy(b.table).cuda(), torch.from_numpy(b.lens.astype(np.int32)).cuda(),
+                     block, **k)
+    assert torch.equal(got, b.run(tok))
+    b.check(got)
+
+
 def test_replays_follow_lengths_tables_and_queries(tok):
     """A captured decode step, replayed while its inputs change in place."""
     import torch

@@ -224,6 +224,34 @@ def test_captured_forward_and_backward(tok):
     assert torch.equal(y, tok.rotate(x, p, table)) and torch.equal(back, want)
 
 
+def test_a_captured_training_step(tok):
+    """Forward and backward through autograd in one graph, replayed on new inputs."""
+    import torch
+    x, p = inputs(64, 4, 64, "float32")
+    g, _ = inputs(64, 4, 64, "float32", seed=3)
+    table = tok.rotary_table(64)
+    x.requires_grad_()
+
+    def step():
+        y = tok.rotate(x, p, table, scale=1.5)
+        (grad,) = torch.autograd.grad((y * g).sum(), x)
+        return grad
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grad = step()
+    for seed in (5, 6):
+        g.copy_(inputs(64, 4, 64, "float32", seed=seed)[0])
+        p.copy_(inputs(64, 1, 1, "float32", seed=seed)[1])
+        graph.replay()
+        assert torch.equal(grad, tok.rotate(g, p, table, scale=1.5, inverse=True))
+
+
 def test_refusals(tok):
     import torch
 
