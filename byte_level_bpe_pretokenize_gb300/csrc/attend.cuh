@@ -687,9 +687,14 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
     }
     float size = 0.f;  // of what they stand for
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
-      if (!kPartial || most < INFINITY) size = fmaxf(size, most);
+    for (int j = 0; j < G; ++j) size = fmaxf(size, fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]));
+    if (!(size < INFINITY)) {  // an infinity gives no unit
+      size = 0.f;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
+        if (most < INFINITY) size = fmaxf(size, most);
+      }
     }
     __syncwarp();
     // from here on a thread has column g and tokens c, c + 4, .. of the step

@@ -323,6 +323,22 @@ def test_a_nan_is_seen(tok):
     assert bool(got[0, :2].isnan().all()) and not bool(got[1].isnan().any())
 
 
+@pytest.mark.parametrize("lens,new", [([64, 50], None), ([64, 50], [3, 40]), ([300, 290], [300, 200])])
+def test_an_infinity_is_seen_by_its_group_alone(tok, lens, new):
+    """A base of infinity, which no write leaves, among the values that every token sees."""
+    import torch
+    heads = 16 if new and new[0] > 200 else 2
+    b = Batch(lens, heads, 2, 64, 16, new=new, seed=2)
+    clean = Batch(lens, heads, 2, 64, 16, new=new, seed=2)
+    page = b.cache[b.table[0, 0]]
+    page[1, 1, 16 * 32 + 4:16 * 32 + 8] = np.array([0x7F803E80], "<u4").view(np.uint8)  # token 0, group 1
+    got, want = b.run(tok), clean.run(tok)
+    rows = slice(0, 1 if new is None else new[0])
+    assert not bool(got[rows, 2:4, 32:].isfinite().any())
+    got[rows, 2:4, 32:] = want[rows, 2:4, 32:]
+    clean.check(got)
+
+
 def test_strides(tok):
     import torch
     heads, group, dim, block = 2, 3, 64, 16
