@@ -687,14 +687,9 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
     }
     float size = 0.f;  // of what they stand for
 #pragma unroll
-    for (int j = 0; j < G; ++j) size = fmaxf(size, fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]));
-    if (!(size < INFINITY)) {  // an infinity gives no unit
-      size = 0.f;
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
-        if (most < INFINITY) size = fmaxf(size, most);
-      }
+    for (int j = 0; j < G; ++j) {
+      const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
+      if (!kPartial || most < INFINITY) size = fmaxf(size, most);
     }
     __syncwarp();
     // from here on a thread has column g and tokens c, c + 4, .. of the step
@@ -764,7 +759,16 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
     auto values = [&](uint32_t mask) {
       const bool mine = !kPartial || (mask >> lane & 1);
       const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, mine ? __float_as_uint(size) : 0u);
-      const int need = max((int)(largest >> 23) - 127 - 7, -120);
+      int need = max((int)(largest >> 23) - 127 - 7, -120);
+      if (!kPartial && need > power && need > 120) {  // an infinity gives no unit; no number needs more
+        float finite = 0.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
+          if (most < INFINITY) finite = fmaxf(finite, most);
+        }
+        need = max((int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite)) >> 23) - 127 - 7, -120);
+      }
       if (need > power) {
         const float f = power - need < -126 ? 0.f : power_of_2(power - need);
         power = need;
