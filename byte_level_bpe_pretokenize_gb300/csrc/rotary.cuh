@@ -198,8 +198,9 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
           int64_t turning = kAdjacent ? (2 * n_pairs + V - 1) / V : n_pairs / V;
           // in place, what is behind the turned part stays
           const int64_t items = same ? turning : kAdjacent ? (dim + V - 1) / V : turning + (dim - 2 * n_pairs) / V;
-          // adjacent pairs that do not turn go with those that do: lanes of a warp have both
-          if (kAdjacent && A == V) turning = items;
+          // adjacent pairs that do not turn go with those that do: lanes of a warp have both (but where none turn
+          // there may be no positions)
+          if (kAdjacent && A == V && n_pairs > 0) turning = items;
           if (items == 0) return BPE_OK;
           // As many threads share a token's heads as give the GPU half of the threads that it holds: with
           // more, sines are computed again, with fewer, loads are too few.

@@ -476,7 +476,8 @@ int bpe_rotary_table(const double* frequencies, int64_t n_pairs, double base, do
  *                  strides >= 0), elements adjacent.
  *   d_positions    device int32[n_tokens], any values (bpe_plan_blocks writes
  *                  them).
- *   d_turns        device uint64[n_pairs], 2 * n_pairs <= dim.
+ *   d_turns        device uint64[n_pairs], 2 * n_pairs <= dim. Without pairs the
+ *                  call copies; d_positions and d_turns may then be NULL.
  *   interleaved    0: pair i is elements i and n_pairs + i; else 2 i and 2 i + 1.
  *   inverse        not 0: turns by -a. With the same scale that is the gradient:
  *                  of d_x for the gradient d_x of the result.
