@@ -284,8 +284,9 @@ __device__ void wide_fill(const AttendArgs& a, WideShared& sm, int which, uint32
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float x = bf16_low(z[k]) * unit, y = bf16_high(z[k]) * unit, size = fabsf(y) + 16.f * x;
-        // too large for halves or no number; of values also too small for what is left of their bits
-        if (!(size < 32768.f) || (which && size > 0.f && size < 0x1p-9f)) bad = true;
+        // too large for halves or no number, or too small for what is left of their bits (of keys too: a query may ask
+        // for a small group alone)
+        if (!(size < 32768.f) || (size > 0.f && size < 0x1p-9f)) bad = true;
         st[k] = __float2half2_rn(x);
         ba[k] = __float2half2_rn(y);
       }
