@@ -349,6 +349,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attend_wide(AttendArgs a, i
   if (tid == 0) upto[0] = 0;
   __syncthreads();
   const int64_t me = blockIdx.x;
+  if (me == 0 && upto[kWideThreads] > gridDim.x) {
+    // Offsets fall, so that requests share tokens and have more columns than the tokens. Those that the blocks do not
+    // reach are left to attend.cuh.
+    int64_t end = upto[tid];
+    for (int r = r0; r < r1; ++r) {
+      const int64_t n = blocks_of(r);
+      end += n;
+      if (n > 0 && end > gridDim.x) atomicOr(redo + r, 1);
+    }
+  }
   if (me >= upto[kWideThreads]) return;
   if (upto[tid] <= me && me < upto[tid + 1]) {
     int64_t rest = me - upto[tid];
