@@ -19,6 +19,21 @@ namespace {
 constexpr int kUnit = 32;      // tokens of a step
 constexpr int kItemCost = 3;   // what beginning and ending an item takes, in steps
 constexpr int kAttMaxWarps = 16;  // workers of an SM
+// Sizes of values, |base| + 16 step, are compared as the bits of floats. Those that a worker takes as halves lie below a
+// cap, a power of two, which becomes 2^8, and at most kApart powers of two below it. Weights are 2^11 at most and off by
+// 2^-25 where that is more than their own rounding, so a token loses at most 2^(kApart - 36) of the largest part of a
+// sum. Where sizes are further apart a step is added up in 32 bits (below). 2^12 leaves room for first tokens of next to
+// nothing among others; 32-bit queries expect more of their sums. 384 requests of 4,000 tokens (8 x 128, 8 query heads
+// each) with one group of every value 2^20 smaller: 2,450 us, with all values of one block in 50 2^20 larger 840,
+// without either 425. No look at sizes: 417, and what is 2^20 smaller is off by 2^-8, what is 2^30 smaller lost.
+template <int P>
+constexpr int kApart = P == 1 ? 12 : 6;
+constexpr int kLeastCap = 16 << 23;    // so that 1 / unit is a float
+constexpr int kFarApart = 32 << 23;    // above the cap, where sums are in 32 bits
+constexpr int kNoLow = 0x7FFFFFFF;
+// The unit of values below a cap, and what divides by it.
+__device__ __forceinline__ float unit_of(int cap) { return __int_as_float(cap - (8 << 23)); }
+__device__ __forceinline__ float per_unit(int cap) { return __uint_as_float((262u << 23) - (uint32_t)cap); }
 constexpr int kWideMin = BPE_ATTEND_LONG;  // columns of a request from which attend_wide.cuh takes it
 
 struct AttendArgs {
@@ -269,7 +284,7 @@ __device__ __forceinline__ void attend_store(const AttendArgs& a, int64_t row, i
 // of them take the codes apart, 25 are products, 45 the copies, 60 the softmax),
 // at 57% of the slots with the 12 warps that 168 registers leave; 8 x 2 warps of
 // 128 registers spill and take 455 us where 6 x 2 take 428, 7 x 2 450. 384
-// requests of 4,000 tokens (8 x 128, 8 query heads each): 417 us, 4.7 TB/s of
+// requests of 4,000 tokens (8 x 128, 8 query heads each): 425 us, 4.7 TB/s of
 // codes and pairs. Weights in two bfloat16 parts outside the codes' products, and
 // codes as 1 + n / 16, took 868 us.
 //
@@ -458,14 +473,15 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
   float mid[NT][4];       // of group g (and nothing), columns 2 c and 2 c + 1
   float top[NT], total_p[NT];  // of column g; the weights of this thread's tokens
   int sees[NT];           // tokens that column g sees
-  int power;              // weights are in units of 2^power, as large as the values met
+  int cap, low;           // of sizes of values: what all are below, and the smallest that this lane met (zeros aside)
   bool whole = false;     // the item begins with this worker's first step of it
   // the pairs of groups whose bases this thread has in the products of bases
   auto base_unit = [&](int m, int half) { return (m * 8 + half * 4 + c) % U; };
 
   auto begin = [&] {
     const AttendCursor use = *item;
-    power = -120;
+    cap = kLeastCap;
+    low = kNoLow;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = use.tile * kCols + 8 * n + g;
@@ -687,12 +703,30 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
 #pragma unroll
       for (int j = 0; j < G; ++j) z[j] = lds32(value_pairs + j * 4);
     }
-    float size = 0.f;  // of what they stand for
+    // the largest and the smallest size of what they stand for, but of groups behind the row's end
+    auto size_of = [](uint32_t pair) { return __float_as_int(fabsf(bf16_high(pair)) + 16.f * bf16_low(pair)); };
+    const bool padded = G > 4 && a.dim <= 32 * (G - 1);
+    int largest = 0, smallest = kNoLow;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
-      if (!kPartial || most < INFINITY) size = fmaxf(size, most);
+      if (j == G - 1 && padded) break;
+      const int size = size_of(z[j]);
+      largest = max(largest, size);
+      smallest = min(smallest, size);
     }
+    // Whether the sizes lie where this worker's do. Tokens that no column sees do not count.
+    uint32_t all = 0xFFFFFFFFu;
+    if (kPartial) {
+      int furthest = 0;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (sees[n] != INT32_MAX) furthest = max(furthest, sees[n]);
+      const int k = __reduce_max_sync(0xFFFFFFFFu, furthest) - u * kUnit;
+      all = there & (k >= kUnit ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u);
+    }
+    const bool mine = !kPartial || (all >> lane & 1);
+    constexpr int kSpan = (kApart<P> + 1) << 23;
+    const bool odd = mine && (largest >= cap || smallest < cap - kSpan);
     __syncwarp();
     // from here on a thread has column g and tokens c, c + 4, .. of the step
     float p[NT][8];
@@ -718,7 +752,40 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
       most[n] = m;
       grows |= m > top[n];
     }
-    if (__any_sync(0xFFFFFFFFu, grows)) {
+    bool close = true;
+    if (__any_sync(0xFFFFFFFFu, grows || odd)) {
+      if (__any_sync(0xFFFFFFFFu, odd)) {
+        // seldom: the same without zeros and what is no number, which spoils its own group in any unit
+        largest = 0, smallest = kNoLow;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const int size = size_of(z[j]);
+          if (!mine || (j == G - 1 && padded) || (uint32_t)size - 1u >= 0x7F7FFFFFu) continue;
+          largest = max(largest, size);
+          smallest = min(smallest, size);
+        }
+        const int most_here = (int)(__reduce_max_sync(0xFFFFFFFFu, (uint32_t)largest) >> 23) + 1 << 23;
+        const int least_met = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)low);
+        const int least = min(least_met, (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)smallest));
+        // (a cap that no halves have gone by may fall, but not so far that sums pass the largest float)
+        int then = max(most_here, least_met == kNoLow && cap - most_here <= kFarApart ? kLeastCap : cap);
+        close = least >= then - kSpan;
+        if (!close) then = most_here - cap > kFarApart ? most_here : cap;
+        if (then != cap) {
+          const int by = (cap - then) >> 23;
+          const float f = by < -126 ? 0.f : power_of_2(by);
+          cap = then;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2 * G; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[n][j][i] *= f;
+            mid[n][0] *= f;
+            mid[n][1] *= f;
+          }
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float f = most[n] > top[n] ? exp2_fast(top[n] - most[n]) : 1.f;
@@ -736,16 +803,20 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
         }
       }
     }
-    // weights of at most 2^7: those down to 2^-21 of the largest are normal halves
-    uint32_t ph[NT][P][4];
+    // weights of at most 2^11: those down to 2^-25 of the largest are normal halves
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float m = (top[n] == -INFINITY ? 0.f : top[n]) - 7.f;
+      const float m = (top[n] == -INFINITY ? 0.f : top[n]) - 11.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         p[n][i] = exp2_fast(p[n][i] - m);
         total_p[n] += p[n][i];
       }
+    }
+
+    uint32_t ph[NT][P][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t part[P];
@@ -754,37 +825,53 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
         for (int k = 0; k < P; ++k) ph[n][k][i] = part[k];
       }
     }
-
-    // Values by the tokens of `mask`: with one unit for all of them, and all of the step's at once, but
-    // where some columns see tokens that others do not and whose values are far larger, which would leave
-    // those nothing of theirs.
-    auto values = [&](uint32_t mask) {
-      const bool mine = !kPartial || (mask >> lane & 1);
-      const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, mine ? __float_as_uint(size) : 0u);
-      int need = max((int)(largest >> 23) - 127 - 7, -120);
-      if (!kPartial && need > power && need > 120) {  // an infinity gives no unit; no number needs more
-        float finite = 0.f;
+    if (!close) {
+      // in 32 bits, a token after another: no size matters to another
+      // weights where the scores are, those of columns that do not see a token below zero
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float m = (top[n] == -INFINITY ? 0.f : top[n]) - 11.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float* const at = reinterpret_cast<float*>(smem + scores + n * (kUnit * 32) + (c + 4 * i) * 32 + g * 4);
+          *at = kPartial && !(seen[n] >> i & 1) ? -1.f : exp2_fast(to_score[n] * *at - m);
+        }
+      }
+      __syncwarp();
+      const float unit = per_unit(cap);
+      const uint32_t pairs = codes + kUnit * Shape::kRow;
+#pragma unroll 1
+      for (int t = 0; t < kUnit; ++t) {
+        if (kPartial && !(all >> t & 1)) continue;
+        float2 weight[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          weight[n] = *reinterpret_cast<const float2*>(smem + scores + n * (kUnit * 32) + t * 32 + c * 8);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const float most = fabsf(bf16_high(z[j])) + 16.f * bf16_low(z[j]);
-          if (most < INFINITY) finite = fmaxf(finite, most);
+          const bool paired = !kOddGroups || j < G - 1;
+          const uint32_t row = codes + t * Shape::kRow + (paired ? attend_piece<G>(t, j / 2) * 32 + (g >> 1) * 8 + (j & 1) * 4
+                                                                 : j * 16 + (g >> 1) * 4);
+          const uint32_t word = lds32(row) >> (g & 1) * 16, pair = lds32(pairs + t * Shape::kPair + j * 4);
+          const float st = bf16_low(pair) * unit, ba = bf16_high(pair) * unit;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float code = __uint_as_float((word >> 4 * i & 15u) | 0x4B000000u) - 0x1p23f;
+            const float value = fmaf(st, code, ba) * (i & 1 ? 1.f / kOdd : 1.f / kEven);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float* const to = acc[n][2 * j + i / 2] + (i & 1) * 2;
+              if (!(weight[n].x < 0.f)) to[0] = fmaf(weight[n].x, value, to[0]);
+              if (!(weight[n].y < 0.f)) to[1] = fmaf(weight[n].y, value, to[1]);
+            }
+          }
         }
-        need = max((int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite)) >> 23) - 127 - 7, -120);
       }
-      if (need > power) {
-        const float f = power - need < -126 ? 0.f : power_of_2(power - need);
-        power = need;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int j = 0; j < 2 * G; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][j][i] *= f;
-          mid[n][0] *= f;
-          mid[n][1] *= f;
-        }
-      }
-      const float unit = power_of_2(-power), middle = P == 2 || a.centre ? 8.f : 0.f;
+      return;
+    }
+    if (mine) low = min(low, smallest);
+    {
+      const float unit = per_unit(cap), middle = P == 2 || a.centre ? 8.f : 0.f;
       // in the order of a thread's tokens: c, c + 4, c + 8, c + 12 of each half of the step are neighbours
       const uint32_t place = ((lane & 16) | (lane & 3) << 2 | (lane >> 2 & 3)) * 2;
 #pragma unroll
@@ -918,37 +1005,6 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
             for (int e = 0; e < 4; ++e)
               if (4 * u + i < 2 * G) acc[n][4 * u + i][e] += o[n][i][e];
       }
-    };
-    if (!kPartial) {
-      values(0xFFFFFFFFu);
-    } else {
-      int least = INT32_MAX, furthest = 0;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        least = min(least, sees[n]);
-        if (sees[n] != INT32_MAX) furthest = max(furthest, sees[n]);
-      }
-      auto first_tokens = [&](int limit) {
-        const int k = limit - u * kUnit;
-        return k >= kUnit ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
-      };
-      const uint32_t all = there & first_tokens(__reduce_max_sync(0xFFFFFFFFu, furthest));
-      const uint32_t common = all & first_tokens(__reduce_min_sync(0xFFFFFFFFu, least));
-      const bool counts = (all >> lane & 1) && size > 0.f;
-      const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, counts ? __float_as_uint(size) : 0u);
-      const uint32_t smallest = __reduce_min_sync(0xFFFFFFFFu, counts ? __float_as_uint(size) : 0xFFFFFFFFu);
-      if (common == all || largest <= smallest || largest - smallest < (8u << 23)) {
-        values(all);
-      } else {
-        uint32_t left = all & ~common, now = common;
-        while (true) {  // at most 33 times
-          if (now) values(now);
-          __syncwarp();
-          if (!left) break;
-          now = left & (0u - left);
-          left &= left - 1;
-        }
-      }
     }
   };
 
@@ -957,7 +1013,7 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
     const AttendCursor use = *item;
     const bool done = whole && last;
     float* part = a.partial + (2 * me + (whole ? 1 : 0)) * Shape::kPartial;
-    const float unit = power_of_2(power);
+    const float unit = unit_of(cap);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float l = total_p[n];

@@ -573,13 +573,23 @@ int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, cons
  *                  [offsets[r], offsets[r + 1]). NULL: one each (a decode
  *                  step; n_tokens is then n_requests at least).
  * Sums and the softmax are in 32 bits. Products run on the tensor cores in
- * halves: codes, and 16-bit queries scaled by a power of two, without loss;
- * weights to 2^-11 of theirs; 32-bit queries and weights in two parts, to 2^-23.
+ * halves. Codes lose nothing there, nor do 16-bit queries, scaled by a power of
+ * two, but for elements 2^-29 of a row's largest. With 16-bit queries, whatever
+ * the result's type, a weight is off by up to 2^-11 of itself, and its product
+ * with a step again; 32-bit queries and weights are two halves, to 2^-22. A
+ * weight may always be off by 2^-36 of the largest. Values whose sizes, by
+ * token and group of 32 elements, are not within 2^12 of the others that a warp
+ * adds up (2^6 with 32-bit queries) are added up in 32 bits, several times as
+ * slowly: what a column's sum holds of small values does not depend on large
+ * ones beside them.
  * In long runs of new tokens (16-bit queries; BPE_ATTEND_LONG columns of a
  * request, a column being a query head of a token, and 8192 of all heads) keys
- * and values are halves too, to 2^-12 of theirs; a request whose cache has NaNs,
- * infinities or sizes 2^15 apart is computed as short runs are. So what a token
- * may not see changes nothing in its result but the last bits.
+ * and values are halves too, to 2^-11 of theirs, weights are halves once, or off
+ * by 2^-31 of the largest, and queries hold elements down to 2^-20 of a row's
+ * largest without loss. A request is computed as short runs are, after the
+ * attempt, if the cache holds NaNs or infinities of it, or groups not zero that
+ * are 2^9 larger or 2^15 smaller than the largest of its first 128 tokens. So
+ * what a token may not see changes nothing in its result but the last bits.
  * Left out and reported (BPE_ERR_BAD_INPUT): requests whose offsets are not
  * monotone in [0, n_tokens] (their rows are left as they are), those with a
  * length outside [0, max_blocks * block_size], or
