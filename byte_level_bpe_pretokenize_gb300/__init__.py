@@ -758,7 +758,7 @@ class Tokenizer:
         """Rotary positions (see bpe_rotate) of x [tokens, heads, dim] in 32 or
         16 bits: the first 2 * len(table) elements of each head turn, the rest
         is copied; into a new tensor of x's type or ``dtype``, or into ``out``
-        (which may be x). positions int32[tokens]; table: from rotary_table;
+        (which may be x, but must not overlap it otherwise). positions int32[tokens]; table: from rotary_table;
         interleaved: pairs lie next to each other, else half the turned part
         apart; inverse turns back. Differentiable with respect to x in backward
         and forward mode, as often as wanted; ``out`` is refused for inputs that
@@ -893,8 +893,9 @@ class Tokenizer:
         seq_lens int32[n] as plan_blocks leaves them; offsets int64[n + 1] of
         the packed new tokens, or None for one new token each; scale: dim **
         -0.5 unless given. Each token sees its request's tokens up to itself.
-        Returns [tokens, heads, dim] in queries' type or ``dtype``, or ``out``;
-        tokens of no request get zeros, or what was in out. Has no derivative: a
+        Returns [tokens, heads, dim] in queries' type or ``dtype``, or ``out``,
+        which must not overlap queries; tokens of no request get zeros, or what
+        was in out. Has no derivative: a
         backward pass through its result raises, and ``out`` is refused for
         inputs that torch records derivatives of."""
         torch, types, device = _torch(), _type_codes, self.device

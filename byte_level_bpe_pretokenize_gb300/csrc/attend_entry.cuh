@@ -44,6 +44,13 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
       return bad("a pointer is not aligned to its elements");
     const int64_t n_rows = p.n_heads * p.group;
     if (rows_meet(p.n_tokens, p.out_token_stride, n_rows, p.out_head_stride, p.dim)) return bad("output rows overlap");
+    // (a long run that is computed again reads its queries again)
+    auto rows = [&](const void* at, int64_t token, int64_t head, int64_t size) {
+      return Rows{reinterpret_cast<uintptr_t>(at), p.n_tokens, n_rows, token * size, head * size, p.dim * size};
+    };
+    if (rows_share(rows(p.queries, p.query_token_stride, p.query_head_stride, type_size(p.query_type)),
+                   rows(p.out, p.out_token_stride, p.out_head_stride, type_size(p.out_type))))
+      return bad("out overlaps queries");
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
     const int64_t groups = cache_groups(p.dim);

@@ -106,6 +106,46 @@ inline bool rows_meet(int64_t n, int64_t s, int64_t m, int64_t t, int64_t dim) {
   return !(t >= dim && s >= (m - 1) * t + dim) && !(s >= dim && t >= (n - 1) * s + dim);
 }
 
+// n x m rows of `row` bytes from `at` on, s and t bytes apart (>= 0).
+struct Rows {
+  uintptr_t at;
+  int64_t n, m, s, t, row;
+  int64_t reach() const { return (n - 1) * s + (m - 1) * t + row; }
+  bool gapless() const {
+    return (m <= 1 || t <= row) && (n <= 1 || s <= (m - 1) * t + row);
+  }
+};
+
+// Whether two such tensors share a byte, as far as that shows without looking at every pair of rows: always where
+// their strides are equal, and where one of them has no gaps and an end of the other lies in it.
+inline bool rows_share(const Rows& a, const Rows& b) {
+  if (a.n < 1 || a.m < 1 || b.n < 1 || b.m < 1) return false;
+  const int64_t d = (int64_t)(b.at - a.at);  // rows meet where -b.row < d + i s + j t < a.row
+  if (d >= a.reach() || -d >= b.reach()) return false;
+  if (a.gapless() && b.gapless()) return true;
+  if (a.n == b.n && a.m == b.m && (a.n == 1 || a.s == b.s) && (a.m == 1 || a.t == b.t)) {
+    for (int64_t j = 1 - a.m; j < a.m; ++j) {
+      const int64_t e = d + j * a.t;  // the smallest e + i s above -b.row
+      int64_t i = 0;
+      if (a.n > 1 && a.s > 0) {
+        const int64_t over = e + b.row - 1;
+        i = -(over >= 0 ? over / a.s : -((-over + a.s - 1) / a.s));
+        i = std::max(i, 1 - a.n);
+        if (i > a.n - 1) continue;
+      }
+      if (e + i * a.s > -b.row && e + i * a.s < a.row) return true;
+    }
+    return false;
+  }
+  auto in = [](const Rows& whole, const Rows& other) {
+    if (!whole.gapless()) return false;
+    const int64_t first = (int64_t)(other.at - whole.at), last = first + other.reach() - other.row;
+    auto meets = [&](int64_t at) { return at < whole.reach() && at + other.row > 0; };
+    return meets(first) || meets(last);
+  };
+  return in(a, b) || in(b, a);
+}
+
 // No exception (an allocation for an error message, say) leaves a C entry.
 template <class F>
 int guarded(const char* what, F f) noexcept {

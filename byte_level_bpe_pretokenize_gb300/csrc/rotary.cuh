@@ -185,6 +185,12 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
     if (same && (x_type != out_type || (n_tokens > 1 && x_token_stride != out_token_stride) ||
                  (n_heads > 1 && x_head_stride != out_head_stride)))
       return fail(BPE_ERR_INVALID_ARG, "bpe_rotate: in place needs one type and the same strides");
+    auto rows = [&](const void* at, int64_t token, int64_t head, int64_t size) {
+      return Rows{reinterpret_cast<uintptr_t>(at), n_tokens, n_heads, token * size, head * size, dim * size};
+    };
+    if (!same && rows_share(rows(d_x, x_token_stride, x_head_stride, type_size(x_type)),
+                            rows(d_out, out_token_stride, out_head_stride, type_size(out_type))))
+      return fail(BPE_ERR_INVALID_ARG, "bpe_rotate: out overlaps x");
     DeviceGuard g(h->device);
     cudaStream_t st = (cudaStream_t)stream;
     return with_type(x_type, [&](auto ti) {
