@@ -9,7 +9,8 @@
 // fraction of 2^64, so p f_i modulo a turn is one wrapping product of integers:
 // its error is p 2^-65 turns, below that of the 32-bit angle that its upper
 // half becomes, at every position. (In 32-bit floats a fast pair is off by a
-// radian after some million positions, and 64-bit ones are slow here.)
+// radian after some million positions, and 64-bit ones are slow here.) What f_i
+// itself is off by, 2^-53 of it where it is computed, p multiplies too.
 
 namespace {
 
@@ -132,6 +133,34 @@ __global__ void __launch_bounds__(kRotThreads) k_rotate(RotateArgs a) {
   }
 }
 
+// 1 / (2 pi) as a sum of three doubles, to 2^-163.
+constexpr double kPerTurn = 0x1.45f306dc9c883p-3, kPerTurn2 = -0x1.6b01ec5417056p-57, kPerTurn3 = -0x1.6447e493ad4cep-111;
+
+// f / (2 pi) modulo 1 as a fraction of 2^64, rounded, for f up to 2^90: f times each part is a sum of two doubles, and
+// a double modulo 1 is exact. So far positions turn by what f says, to p 2^-65 turns, where f / (2 pi) in 64 bits would
+// be off by up to p 2^-56, and p 2^-54 for a negative f.
+inline uint64_t fraction_of_turn(double f) {
+  auto fraction = [](double x) -> uint64_t {  // x modulo 1 in units of 2^-64, cut off below them
+    const double whole = std::trunc(x), part = std::fabs(x - whole);
+    const uint64_t u = (uint64_t)std::ldexp(part, 64);
+    return x < 0 ? 0 - u : u;
+  };
+  auto rest = [](double x) {  // what that cut off, in units
+    const double part = std::ldexp(x - std::trunc(x), 64);
+    return part - std::trunc(part);
+  };
+  uint64_t sum = 0;
+  double below = 0;
+  for (double c : {kPerTurn, kPerTurn2, kPerTurn3}) {
+    const double high = f * c, low = std::fma(f, c, -high);
+    for (double x : {high, low}) {
+      sum += fraction(x);
+      below += rest(x);
+    }
+  }
+  return sum + (uint64_t)(int64_t)std::nearbyint(below);
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,15 +177,14 @@ int bpe_rotary_table(const double* frequencies, int64_t n_pairs, double base, do
     for (int64_t i = 0; i < n_pairs; ++i) {
       double f = frequencies ? frequencies[i] : std::pow(base, -(double)i / (double)n_pairs);
       if (!std::isfinite(f)) return fail(BPE_ERR_INVALID_ARG, "bpe_rotary_table: a frequency is not finite");
-      f /= 6.283185307179586476925286766559;  // turns a position
       if (original > 0) {
-        const double keep = std::min(1.0, std::max(0.0, (original * std::fabs(f) - low) / (high - low)));
+        const double turns_over = original * (std::fabs(f) * kPerTurn);
+        const double keep = std::min(1.0, std::max(0.0, (turns_over - low) / (high - low)));
         f *= keep + (1.0 - keep) / factor;
       } else {
         f /= factor;
       }
-      const double part = f - std::floor(f);
-      turns[i] = part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;
+      turns[i] = fraction_of_turn(f);
     }
     return BPE_OK;
   });

@@ -456,8 +456,10 @@ int bpe_embed_grad(bpe_handle* h, const int32_t* d_ids, int64_t n_ids, const voi
  *                  factor, and between them f becomes
  *                  f * (g + (1 - g) / factor), g = (r - low) / (high - low).
  *   turns          host uint64[n_pairs], receives the turns a position as
- *                  fractions of 2^64; a copy on the device is what bpe_rotate
- *                  takes.
+ *                  fractions of 2^64, rounded once (frequencies are taken as
+ *                  exact up to 2^90; computed and stretched ones are 64-bit
+ *                  numbers, so off by some 2^-53 of theirs); a copy on the
+ *                  device is what bpe_rotate takes.
  * Host-only: needs no GPU and no handle. n_pairs <= 32768.
  */
 int bpe_rotary_table(const double* frequencies, int64_t n_pairs, double base, double factor, double original,
@@ -467,8 +469,8 @@ int bpe_rotary_table(const double* frequencies, int64_t n_pairs, double base, do
  * bpe_rotate — rotary positions: of each head of token t, the pairs (x1, x2) of
  * its first 2 * n_pairs elements become
  *   scale * (x1 cos a - x2 sin a, x1 sin a + x2 cos a),
- * a = the pair's angle at d_positions[t], computed to 2^-25 of a half turn at
- * every position; what is behind them is copied. One call takes the queries and
+ * a = the pair's angle at d_positions[t], which is what the table says to 2^-25
+ * of a half turn at every position; what is behind them is copied. One call takes the queries and
  * keys of a fused projection together, as heads of one tensor.
  *
  *   d_x            device [n_tokens][n_heads][dim] of x_type, tokens
