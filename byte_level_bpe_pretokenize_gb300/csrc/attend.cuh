@@ -1036,8 +1036,7 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
           const float m = __shfl_sync(0xFFFFFFFFu, mid[n][e], 4 * j + c);
           float4 r = make_float4(acc[n][2 * j][e] * kEven + m, acc[n][2 * j][2 + e] * kOdd + m,
                                  acc[n][2 * j + 1][e] * kEven + m, acc[n][2 * j + 1][2 + e] * kOdd + m);
-          const float f = done ? by : unit;
-          r.x *= f, r.y *= f, r.z *= f, r.w *= f;
+          r.x *= by, r.y *= by, r.z *= by, r.w *= by;  // partial sums too, which large values would take past a float
           if (!done) *reinterpret_cast<float4*>(part + (8 * n + 2 * c + e) * 32 * G + 32 * j + 4 * g) = r;
           else if (real) attend_store(a, row, 32 * j + 4 * g, r);
         }
@@ -1090,13 +1089,15 @@ __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G
   }
 }
 
-// Adds up the partial sums of items that lie in several workers' shares, in the
-// order of the shares or by a fixed tree. Block b looks at the border between
-// workers b and b + 1; of an item that spans k borders each of their blocks takes
-// columns. With few parts a thread reads all parts of its four elements; with
-// many, parts are spread over the threads, their factors first.
+// Adds up what several workers' shares have of an item (the mean of the values by
+// its weights, their sum and maximum), in the order of the shares or by a fixed
+// tree. Block b looks at the border between workers b and b + 1; of an item that
+// spans k borders each of their blocks takes columns. With few parts a thread
+// reads all parts of its four elements; with many, parts are spread over the
+// threads, their factors first.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 8;
+constexpr float kJoinUnit = 0x1p-44f;  // all weights of 2^31 tokens add up to less than 1
 template <int G, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
   using Shape = AttendShape<G, 1, NT>;
@@ -1140,8 +1141,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
 #pragma unroll
       for (int k = 0; k < kJoinFew; ++k) {
         if (k >= parts) break;
-        const float f = exp2_fast(top[k] - m);
-        total += f * part(k)[kTotal + col];
+        const float f = exp2_fast(top[k] - m) * (part(k)[kTotal + col] * kJoinUnit);
+        total += f;
         add(sum, f, part(k) + col * 32 * G + 4 * vec);
       }
       put(col, vec, sum, total);
@@ -1174,9 +1175,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
     for (int k0 = 0; k0 < parts; k0 += kRound) {
       if (k0) __syncthreads();  // factors may still be read
       for (int k = k0 + tid; k < min(parts, k0 + kRound); k += kJoinThreads) {
-        const float f = exp2_fast(part(k)[kTop + col] - m);
+        const float f = exp2_fast(part(k)[kTop + col] - m) * (part(k)[kTotal + col] * kJoinUnit);
         factor[k - k0] = f;
-        total += f * part(k)[kTotal + col];
+        total += f;
       }
       __syncthreads();
       if (slice < kSlices) {
