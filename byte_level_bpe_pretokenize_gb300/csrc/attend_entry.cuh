@@ -34,7 +34,8 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
         p.group > 256 || p.n_tokens * p.group >= INT32_MAX / p.n_heads || p.max_blocks < 0 || p.max_blocks > INT32_MAX ||
         p.query_token_stride < 0 || p.query_head_stride < 0 || p.out_token_stride < 0 || p.out_head_stride < 0)
       return bad("a size or stride is negative or too large");
-    if (!std::isfinite(p.scale)) return bad("scale is not finite");
+    const float scale = p.scale * 1.4426950408889634f;  // scores are powers of two
+    if (!std::isfinite(scale)) return bad("scale is not finite, or too large");
     if (p.n_requests > 1 && p.table_stride < p.max_blocks) return bad("table rows overlap");
     if (!p.offsets && p.n_tokens < p.n_requests) return bad("n_tokens is below one new token a request");
     if (p.n_requests == 0 || p.n_tokens == 0) return BPE_OK;
@@ -75,7 +76,7 @@ int bpe_attend(bpe_handle* h, const bpe_attend_args* args, bpe_stream_t stream) 
                  static_cast<const unsigned char*>(cache), p.n_blocks, p.block_stride,
                  cache_page_bytes(p.block_size, p.dim), FastDiv(p.block_size), p.table, p.table_stride,
                  std::min<int64_t>(p.max_blocks * p.block_size, INT32_MAX - 2 * kUnit), p.seq_lens, p.offsets, (int)p.n_requests,
-                 p.scale * 1.4426950408889634f,
+                 scale,
                  fits(p.queries, p.query_token_stride, p.query_head_stride, type_size(p.query_type), 8),
                  fits(p.out, p.out_token_stride, p.out_head_stride, type_size(p.out_type), 4),
                  p.query_type != BPE_BF16 || p.out_type != BPE_BF16,

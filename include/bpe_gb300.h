@@ -583,7 +583,8 @@ int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, cons
  * token and group of 32 elements, are not within 2^12 of the others that a warp
  * adds up (2^6 with 32-bit queries) are added up in 32 bits, several times as
  * slowly: what a column's sum holds of small values does not depend on large
- * ones beside them.
+ * ones beside them. Queries of 2^100 and more are not provided for, nor is a
+ * scale of 2^127 and more (refused).
  * In long runs of new tokens (16-bit queries; BPE_ATTEND_LONG columns of a
  * request, a column being a query head of a token, and 8192 of all heads) keys
  * and values are halves too, to 2^-11 of theirs, weights are halves once, or off
