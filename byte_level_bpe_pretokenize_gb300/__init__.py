@@ -895,7 +895,8 @@ class Tokenizer:
         -0.5 unless given. Each token sees its request's tokens up to itself.
         Returns [tokens, heads, dim] in queries' type or ``dtype``, or ``out``,
         which must not overlap queries; tokens of no request get zeros, or what
-        was in out. Has no derivative: a
+        was in out. What it is off by goes by the queries' type: 16-bit ones
+        give weights of 11 bits, for 32-bit results too. Has no derivative: a
         backward pass through its result raises, and ``out`` is refused for
         inputs that torch records derivatives of."""
         torch, types, device = _torch(), _type_codes, self.device

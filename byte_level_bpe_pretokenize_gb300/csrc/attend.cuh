@@ -25,7 +25,7 @@ constexpr int kAttMaxWarps = 16;  // workers of an SM
 // sum. Where sizes are further apart a step is added up in 32 bits (below). 2^12 leaves room for first tokens of next to
 // nothing among others; 32-bit queries expect more of their sums. 384 requests of 4,000 tokens (8 x 128, 8 query heads
 // each) with one group of every value 2^20 smaller: 2,450 us, with all values of one block in 50 2^20 larger 840,
-// without either 425. No look at sizes: 417, and what is 2^20 smaller is off by 2^-8, what is 2^30 smaller lost.
+// without either 427. No look at sizes: 417, and what is 2^20 smaller is off by 2^-8, what is 2^30 smaller lost.
 template <int P>
 constexpr int kApart = P == 1 ? 12 : 6;
 constexpr int kLeastCap = 16 << 23;    // so that 1 / unit is a float
@@ -280,17 +280,18 @@ __device__ __forceinline__ void attend_store(const AttendArgs& a, int64_t row, i
 // of keys from shared memory in 16 bits, four times the bytes that a code has
 // there.
 //
-// Bound by issue and latency: 370 instructions for 16 tokens of 128 elements (80
+// Bound by issue and latency: 373 instructions for 16 tokens of 128 elements (80
 // of them take the codes apart, 25 are products, 45 the copies, 60 the softmax),
-// at 57% of the slots with the 12 warps that 168 registers leave; 8 x 2 warps of
+// at 56% of the slots with the 12 warps that 168 registers leave; 8 x 2 warps of
 // 128 registers spill and take 455 us where 6 x 2 take 428, 7 x 2 450. 384
-// requests of 4,000 tokens (8 x 128, 8 query heads each): 425 us, 4.7 TB/s of
+// requests of 4,000 tokens (8 x 128, 8 query heads each): 427 us, 4.7 TB/s of
 // codes and pairs. Weights in two bfloat16 parts outside the codes' products, and
 // codes as 1 + n / 16, took 868 us.
 //
 // P is 1 for 16-bit queries, which a half holds without loss once they are
 // scaled by a power of two, and 2 for 32-bit ones. Weights are halves too (P of
-// them): 2^-12 of a weight, which is what a result of 11 bits rounds away.
+// them), and their products with steps once more: off by up to 2^-11 each, about
+// what a result of 11 bits rounds away, and for 32-bit results of 16-bit queries as well.
 template <int P, int G, int NT>
 __global__ void __launch_bounds__(AttendShape<G, P, NT>::kThreads, AttendShape<G, P, NT>::kBlocks) k_attend(AttendArgs a) {
   using Shape = AttendShape<G, P, NT>;

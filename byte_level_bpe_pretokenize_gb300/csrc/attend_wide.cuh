@@ -11,11 +11,12 @@
 //   scores [128 columns x 128 tokens] = queries x keys^T
 //   results [128 columns x dim] += weights x values
 //
-// A value is a half of its own 2^-12, in units of 2^e that the first 128 tokens
-// give. What does not fit that (an infinity, a NaN, sizes 2^15 apart) marks the
-// request, which attend.cuh then computes again: so masked tokens spoil no
-// column here that may not see them.
-
+// Keys and values are halves, off by up to 2^-11 of themselves, in units of 2^e
+// that the first 128 tokens give. What does not fit that (an infinity, a NaN,
+// sizes 2^9 larger or 2^15 smaller than the largest of those tokens) marks the
+// request, which attend.cuh then computes again: so masked tokens spoil no column
+// here that may not see them. 16 prompts with such sizes in one block of 50: 5.9 ms
+// in place of 0.54.
 //
 // A step (128 tokens, two tiles of columns, dim 128) takes 3,700 clocks. Its
 // 2 x 16 products take 2,450 of them, 76 each where 64 are the tensor cores'
@@ -25,7 +26,7 @@
 // block's beginning and end take 18,000 clocks (its place among the requests,
 // queries, results), so that runs behind little cost more than their products.
 // 8,000 new tokens of 16 prompts behind 3,000 each (8 x 128, 4 query heads each):
-// 530 us, 870 TFLOP/s, 45% of the measured rate.
+// 538 us, 855 TFLOP/s, 45% of the measured rate.
 
 namespace {
 

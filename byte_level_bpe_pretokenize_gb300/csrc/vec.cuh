@@ -1,6 +1,6 @@
 // Vector loads and stores of 32- and 16-bit elements as 32-bit floats.
 //
-// Included once by model_ops.cu; not a standalone header.
+// Included once by each translation unit of the operators; not a standalone header.
 //
 // A vector of V elements moves in accesses of at most 16 bytes, so its address
 // needs an alignment of min(16, V * size) only. Both directions use the
