@@ -184,6 +184,7 @@ int bpe_rotary_table(const double* frequencies, int64_t n_pairs, double base, do
       } else {
         f /= factor;
       }
+      if (!std::isfinite(f)) return fail(BPE_ERR_INVALID_ARG, "bpe_rotary_table: a stretched frequency is not finite");
       turns[i] = fraction_of_turn(f);
     }
     return BPE_OK;

@@ -55,3 +55,11 @@ def test_angles_at_the_last_position(bpe):
             got = Fraction((int(turn) * position) % 2 ** 64, 2 ** 64)
             d = (got - position * Fraction(float(x)) / TWO_PI) % 1
             assert min(d, 1 - d) <= Fraction(1, 2 ** 33)
+
+
+def test_frequencies_that_leave_the_doubles(bpe):
+    for k in (dict(frequencies=[1.0, 1e300], factor=1e-300), dict(frequencies=[-1e300, 0.0], factor=1e-200)):
+        with pytest.raises(bpe.BpeError) as e:
+            bpe.bpe_rotary_table(2, **k)
+        assert e.value.code == 1 and "finite" in str(e.value)
+    assert bpe.bpe_rotary_table(2, frequencies=[1.7e308, -1.7e308]).shape == (2,)
