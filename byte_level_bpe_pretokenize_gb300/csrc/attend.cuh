@@ -27,7 +27,7 @@ constexpr int kAttMaxWarps = 16;  // workers of an SM
 // each) with one group of every value 2^20 smaller: 2,450 us, with all values of one block in 50 2^20 larger 840,
 // without either 427. No look at sizes: 417, and what is 2^20 smaller is off by 2^-8, what is 2^30 smaller lost.
 template <int P>
-constexpr int kApart = P == 1 ? 12 : 6;
+constexpr int kApart = P == 1 ? 12 : 8;
 constexpr int kLeastCap = 16 << 23;    // so that 1 / unit is a float
 constexpr int kFarApart = 32 << 23;    // above the cap, where sums are in 32 bits
 constexpr int kNoLow = 0x7FFFFFFF;

@@ -576,12 +576,13 @@ int bpe_cache_read(bpe_handle* h, const int64_t* d_slots, int64_t n_tokens, cons
  *                  step; n_tokens is then n_requests at least).
  * Sums and the softmax are in 32 bits. Products run on the tensor cores in
  * halves. Codes lose nothing there, nor do 16-bit queries, scaled by a power of
- * two, but for elements 2^-29 of a row's largest. With 16-bit queries, whatever
- * the result's type, a weight is off by up to 2^-11 of itself, and its product
+ * two, but for elements 2^-29 of a row's largest; their products with codes are
+ * cut off at 2^-14 of the largest element of a group of 32 times its step. With
+ * 16-bit queries, whatever the result's type, a weight is off by up to 2^-11 of itself, and its product
  * with a step again; 32-bit queries and weights are two halves, to 2^-22. A
  * weight may always be off by 2^-36 of the largest. Values whose sizes, by
  * token and group of 32 elements, are not within 2^12 of the others that a warp
- * adds up (2^6 with 32-bit queries) are added up in 32 bits, several times as
+ * adds up (2^8 with 32-bit queries) are added up in 32 bits, several times as
  * slowly: what a column's sum holds of small values does not depend on large
  * ones beside them. Queries of 2^100 and more are not provided for, nor is a
  * scale of 2^127 and more (refused).
