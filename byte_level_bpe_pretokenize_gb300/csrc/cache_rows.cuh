@@ -117,15 +117,14 @@ __device__ __forceinline__ void store_words(T* to, const T (&x)[kCacheTake]) {
 
 // A thread quantises 16 elements of a key and of a value, two threads a group.
 // Halves of the elements are subtracted, for the difference of two finite ones
-// may pass the largest float, and multiplied by the step's reciprocal. The step
-// is a quotient too: a product with the rounded 1 / 7.5 gives one f16 group in a
-// thousand, whose quotient is a bfloat16 tie, another step. Rounding is an addition: below 2^22 the lowest bits of
+// may pass the largest float, and multiplied by the step's reciprocal, the
+// one division of a group. Rounding is an addition: below 2^22 the lowest bits of
 // x + 1.5 2^23 are the whole number next to x, ties to even. (|x| stays below
 // 2^20: the base is at most 2^-9 of an element above it, the step at least
 // 2^-24 of one over 15.) V is 8 where elements lie in aligned vectors, else 1.
 //
-// Bound by issue: 86% of the slots, 12 instructions an element. 131,072 tokens of
-// 8 x 128 in bf16 take 145 us, 4.8 TB/s. With 8 elements a thread, four threads a
+// Bound by issue: 84% of the slots, 12 instructions an element. 131,072 tokens of
+// 8 x 128 in bf16 take 143 us, 4.9 TB/s. With 8 elements a thread, four threads a
 // group, what is done once a group took as long as all else: 332 us.
 template <class T, int V>
 __global__ void __launch_bounds__(kCacheThreads) k_cache_write(CacheArgs a, CacheRows r, uint32_t total) {
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kCacheThreads) k_cache_write(CacheArgs a, Cach
     const bool lost = !empty && !(fabsf(ends.x) <= kBf16Max && fabsf(ends.y) <= kBf16Max);
     const __nv_bfloat16 base = __float2bfloat16_rn(empty ? 0.f : ends.x);
     const float half = 0.5f * __bfloat162float(base);
-    __nv_bfloat16 step = __float2bfloat16_rn(fmaxf(__fdiv_rn(0.5f * (empty ? 0.f : ends.y) - half, 7.5f), 0.f));
+    __nv_bfloat16 step = __float2bfloat16_rn(fmaxf((0.5f * (empty ? 0.f : ends.y) - half) * (1.f / 7.5f), 0.f));
     if (__bfloat162float(step) < 0x1p-100f) step = __float2bfloat16_rn(0.f);
     const float half_step = 0.5f * __bfloat162float(step), by = half_step > 0.f ? 1.f / half_step : 0.f;
     uint32_t* codes = reinterpret_cast<uint32_t*>(page + (int64_t)row * a.groups * 16);

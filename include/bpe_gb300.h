@@ -503,8 +503,8 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
  * rounded up to an even one. A group has a base and a step in bfloat16 and a
  * code of 4 bits for each element:
  *   base = bf16(smallest element)
- *   step = bf16((largest / 2 - base / 2) / 7.5), 0 where that is below 2^-100
- *          or negative
+ *   step = bf16((largest / 2 - base / 2) * (1 / 7.5)), 0 where that is below
+ *          2^-100 or negative
  *   code = (x / 2 - base / 2) * (1 / (step / 2)), to the nearest whole number
  *          in [0, 15]; 0 where step is 0
  * (32-bit operations, to nearest even), and stands for base + step * code. A group

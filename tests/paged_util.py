@@ -53,7 +53,7 @@ def quantise(row, dim):
             continue
         base_bits = bf16_bits(x.min())
         half = f(0.5) * bf16_value(base_bits)
-        step_bits = bf16_bits(max((f(0.5) * x.max() - half) / f(7.5), f(0)))
+        step_bits = bf16_bits(max((f(0.5) * x.max() - half) * (f(1) / f(7.5)), f(0)))
         step = bf16_value(step_bits)
         if step < 2.0 ** -100:
             step_bits, step = np.uint32(0), f(0)
