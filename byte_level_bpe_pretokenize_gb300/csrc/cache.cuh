@@ -7,6 +7,9 @@
 // each with a base and a step in bfloat16:
 //   base = bf16(smallest),  step = bf16((largest - base) / 15), 0 below 2^-100,
 //   code = round((x - base) / step) in [0, 15],   x is read back as base + step * code.
+// (Both quotients are products in 32 bits, of halves, with 1 / 7.5 and 2 / step. Where
+// (largest - base) / 15 is next to a tie of two bfloat16 numbers, as of one f16 group
+// in a thousand, the step may so be the other one of them; the codes follow it.)
 // Base and step are rounded first and the codes follow them, so the step's
 // rounding costs nothing but the largest element's last 2^-9 of the range, and the
 // base's is no worse than a bfloat16 of the same elements. A group with a NaN or

@@ -507,7 +507,9 @@ int bpe_rotate(bpe_handle* h, const void* d_x, int x_type, int64_t n_tokens, int
  *          2^-100 or negative
  *   code = (x / 2 - base / 2) * (1 / (step / 2)), to the nearest whole number
  *          in [0, 15]; 0 where step is 0
- * (32-bit operations, to nearest even), and stands for base + step * code. A group
+ * (32-bit operations, to nearest even; 1 / 7.5 is one of them: products decide
+ * between two bfloat16 numbers where the quotient lies next to their middle), and
+ * stands for base + step * code. A group
  * with a NaN or an element beyond bfloat16's largest stands for NaNs.
  *
  * A block is [2][n_heads] pages, keys before values. A page holds the
